@@ -13,7 +13,9 @@ from .ops import (BF16, F32, MXFP8, NVFP4, OUTER_GIVEN, OUTER_ROW, OUTER_TENSOR,
                   grouped_gemm_nvfp4_s2f6,
                   padded_segment_layout, quantize_mxfp8, quantize_mxfp8_dual, quantize_nvfp4, quantize_nvfp4_square,
                   requant_transpose_sr,
-                  rht_s2f6_combine, rht_s2f6_encode, rng_bits16, mfma_rate_probe, route, route_noalloc, gemm_nvfp4_inreg_scale, swiglu_quantize_nvfp4)
+                  rht_s2f6_combine, rht_s2f6_encode, rng_bits16, mfma_rate_probe, route, route_noalloc, gemm_nvfp4_inreg_scale, swiglu_quantize_nvfp4,
+                  gemm_int8, linear_int8, moe_few_tokens_nvfp4, moe_gate, moe_gate_backward, quantize_int8,
+                  swiglu_quantize_int8)
 
 __all__ = [
     "BsqError", "library_path", "load_library",
@@ -22,4 +24,6 @@ __all__ = [
     "grouped_gemm_mxfp8", "route", "route_noalloc", "gemm_nvfp4_inreg_scale", "dequantize_nvfp4", "dequantize_mxfp8", "rng_bits16", "mfma_rate_probe",
     "padded_segment_layout", "quantize_nvfp4_square", "rht_s2f6_encode", "rht_s2f6_combine",
     "swiglu_quantize_nvfp4", "grouped_gemm_nvfp4_s2f6",
+    "moe_gate", "moe_gate_backward", "moe_few_tokens_nvfp4",
+    "quantize_int8", "swiglu_quantize_int8", "gemm_int8", "linear_int8",
 ]

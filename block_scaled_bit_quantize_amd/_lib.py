@@ -14,6 +14,9 @@ c_vp = ctypes.c_void_p
 # include/bsq.h: BSQ_ROUTE_NOALLOC_MAX_BYTES
 ROUTE_NOALLOC_MAX_BYTES = 1 << 20
 
+# include/bsq.h: BSQ_MOE_FEW_MAX_PAIRS
+MOE_FEW_MAX_PAIRS = 2048
+
 # name -> (restype, argtypes); mirrors include/bsq.h
 SIGNATURES = {
     "bsq_status_string": (ctypes.c_char_p, [c_int]),
@@ -50,6 +53,16 @@ SIGNATURES = {
     "bsq_dequantize_mxfp8": (c_int, [c_vp, c_vp, c_i64, c_i64, c_vp, c_vp]),
     "bsq_rng_bits16": (c_int, [c_u64, c_u64, c_u64, c_i64, c_vp, c_vp]),
     "bsq_mfma_rate_probe": (c_int, [c_int, c_int, c_i64, c_i64, c_vp, c_vp]),
+    "bsq_moe_gate": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_int, c_vp, c_vp, c_vp]),
+    "bsq_moe_gate_backward": (c_int, [c_vp, c_vp, c_vp, c_vp, c_int, c_i64, c_i64, c_i64, c_int, c_vp, c_vp]),
+    "bsq_moe_few_nvfp4_workspace": (c_size, [c_i64, c_i64, c_i64, c_i64, c_i64]),
+    "bsq_moe_few_nvfp4": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                  c_vp, c_vp, c_vp, c_vp, c_size, c_vp]),
+    "bsq_quantize_int8": (c_int, [c_vp, c_int, c_i64, c_i64, c_vp, c_vp, c_vp]),
+    "bsq_swiglu_quantize_int8": (c_int, [c_vp, c_int, c_i64, c_i64, c_vp, c_vp, c_vp]),
+    "bsq_gemm_int8": (c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_int, c_vp]),
+    "bsq_linear_int8_workspace": (c_size, [c_i64, c_i64]),
+    "bsq_linear_int8": (c_int, [c_vp, c_int, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_int, c_vp, c_size, c_vp]),
 }
 
 

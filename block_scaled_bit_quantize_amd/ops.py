@@ -341,6 +341,168 @@ def route_noalloc(topk_ids, num_experts, row_index, seg_offsets, pair_row):
     return row_index, seg_offsets, pair_row
 
 
+def _need(cond, what):
+    if not cond:
+        raise BsqError(what)
+
+
+def _dtype(t, what):
+    dt = _OUT.get(t.dtype)
+    if dt is None:
+        raise BsqError(f"{what} must be float32 or bfloat16")
+    return dt
+
+
+def moe_gate(logits, k, renormalize=True):
+    """The k experts of each token: logits [T, E] (float32 or bfloat16) ->
+    (weights f32 [T, k], topk_ids int32 [T, k]), largest first, ties to the
+    lowest index. The weights are a softmax over the selected logits, or with
+    renormalize=False over all of them. Logits of -inf (and NaN) are masked; a
+    slot that finds no unmasked logit left gets id -1 and weight 0."""
+    lib = load_library()
+    _dev(logits)
+    _need(logits.dim() == 2, "moe_gate: logits must be [tokens, experts]")
+    T, E = logits.shape
+    dt = _dtype(logits, "logits")
+    weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    check(lib.bsq_moe_gate(logits.data_ptr(), dt, T, E, k, 1 if renormalize else 0, weights.data_ptr(),
+                           ids.data_ptr(), _stream()), "bsq_moe_gate")
+    return weights, ids
+
+
+def moe_gate_backward(dweights, weights, topk_ids, logits, renormalize=True):
+    """Gradient of moe_gate's weights to its logits, the selection held fixed:
+    dweights f32 [T, k] with moe_gate's outputs and input -> dlogits [T, E] of
+    logits' type (every element written)."""
+    lib = load_library()
+    _dev(dweights, weights, topk_ids, logits)
+    _need(logits.dim() == 2 and weights.dim() == 2, "moe_gate_backward: logits [tokens, experts], weights [tokens, k]")
+    T, E = logits.shape
+    k = weights.shape[1]
+    dt = _dtype(logits, "logits")
+    _need(weights.shape == (T, k) and dweights.shape == (T, k) and topk_ids.shape == (T, k),
+          "moe_gate_backward: dweights, weights and topk_ids must be [tokens, k]")
+    _need(dweights.dtype == torch.float32 and weights.dtype == torch.float32 and topk_ids.dtype == torch.int32,
+          "moe_gate_backward: dweights and weights must be float32, topk_ids int32")
+    dlogits = torch.empty_like(logits)
+    check(lib.bsq_moe_gate_backward(dweights.data_ptr(), weights.data_ptr(), topk_ids.data_ptr(), logits.data_ptr(),
+                                    dt, T, E, k, 1 if renormalize else 0, dlogits.data_ptr(), _stream()),
+          "bsq_moe_gate_backward")
+    return dlogits
+
+
+def moe_few_tokens_nvfp4(x, topk_ids, topk_weights, w13_codes, w13_scales, w13_outer, w2_codes, w2_scales, w2_outer):
+    """A whole expert layer for a few tokens (decode): y [T, H] of x's type =
+    sum over a token's experts of weight * W2 (silu(gate) * up), (gate; up) =
+    W13 x, from x [T, H] (float32 or bfloat16, not quantized), topk_ids int32
+    [T, k] and topk_weights f32 [T, k] as moe_gate returns them (ids outside
+    [0, E) add nothing) and NVFP4 weights with one outer scale per expert: w13
+    [E, 2F, H] (gate rows first), w2 [E, H, F]. T * k <= 2048."""
+    lib = load_library()
+    _dev(x, topk_ids, topk_weights, w13_codes, w13_scales, w13_outer, w2_codes, w2_scales, w2_outer)
+    _need(x.dim() == 2 and topk_ids.dim() == 2 and w13_codes.dim() == 3 and w2_codes.dim() == 3,
+          "moe_few_tokens_nvfp4: x [T, H], topk_ids [T, k], w13 and w2 codes [E, rows, cols / 2]")
+    T, H = x.shape
+    k = topk_ids.shape[1]
+    E, F = w2_codes.shape[0], 2 * w2_codes.shape[2]
+    dt = _dtype(x, "x")
+    _need(topk_ids.shape == (T, k) and topk_weights.shape == (T, k) and topk_ids.dtype == torch.int32
+          and topk_weights.dtype == torch.float32,
+          "moe_few_tokens_nvfp4: topk_ids must be int32 [T, k] and topk_weights float32 [T, k]")
+    _need(w13_codes.shape == (E, 2 * F, H // 2) and w2_codes.shape == (E, H, F // 2)
+          and w13_scales.shape == (E, 2 * F, H // 16) and w2_scales.shape == (E, H, F // 16)
+          and w13_outer.numel() == E and w2_outer.numel() == E,
+          "moe_few_tokens_nvfp4: w13 must be [E, 2F, H] and w2 [E, H, F] (codes, scales, outer [E])")
+    _need(w13_codes.dtype == w2_codes.dtype == w13_scales.dtype == w2_scales.dtype == torch.uint8
+          and w13_outer.dtype == w2_outer.dtype == torch.float32,
+          "moe_few_tokens_nvfp4: codes and scales must be uint8, outer scales float32")
+    out = torch.empty_like(x)
+    wsb = lib.bsq_moe_few_nvfp4_workspace(T, H, F, E, k)
+    ws = _ws(wsb, x.device)
+    check(lib.bsq_moe_few_nvfp4(x.data_ptr(), dt, T, H, F, E, k, topk_ids.data_ptr(), topk_weights.data_ptr(),
+                                w13_codes.data_ptr(), w13_scales.data_ptr(), w13_outer.data_ptr(),
+                                w2_codes.data_ptr(), w2_scales.data_ptr(), w2_outer.data_ptr(), out.data_ptr(),
+                                ws.data_ptr(), wsb, _stream()), "bsq_moe_few_nvfp4")
+    return out
+
+
+def quantize_int8(x):
+    """Rows of x [R, C] (float32 or bfloat16, C % 16 == 0) in 8-bit integers
+    with a scale each: (codes int8 [R, C], scales f32 [R])."""
+    lib = load_library()
+    _dev(x)
+    _need(x.dim() == 2, "quantize_int8: x must be [rows, cols]")
+    R, C = x.shape
+    dt = _dtype(x, "x")
+    codes = torch.empty((R, C), dtype=torch.int8, device=x.device)
+    scales = torch.empty((R,), dtype=torch.float32, device=x.device)
+    check(lib.bsq_quantize_int8(x.data_ptr(), dt, R, C, codes.data_ptr(), scales.data_ptr(), _stream()),
+          "bsq_quantize_int8")
+    return codes, scales
+
+
+def swiglu_quantize_int8(h13):
+    """quantize_int8 of silu(gate) * up, from h13 [R, 2F] (gate columns first)."""
+    lib = load_library()
+    _dev(h13)
+    _need(h13.dim() == 2 and h13.shape[1] % 2 == 0, "swiglu_quantize_int8: h13 must be [rows, 2 * ffn]")
+    R, F = h13.shape[0], h13.shape[1] // 2
+    dt = _dtype(h13, "h13")
+    codes = torch.empty((R, F), dtype=torch.int8, device=h13.device)
+    scales = torch.empty((R,), dtype=torch.float32, device=h13.device)
+    check(lib.bsq_swiglu_quantize_int8(h13.data_ptr(), dt, R, F, codes.data_ptr(), scales.data_ptr(), _stream()),
+          "bsq_swiglu_quantize_int8")
+    return codes, scales
+
+
+def _int8_operand(codes, scales, what):
+    _need(codes.dim() == 2 and codes.dtype == torch.int8 and scales.dtype == torch.float32
+          and scales.numel() == codes.shape[0], f"{what}: int8 codes [rows, K] with float32 scales [rows]")
+
+
+def gemm_int8(a_codes, a_scales, b_codes, b_scales, bias=None, out_dtype=torch.bfloat16):
+    """y [M, N] = (sum_k a[m, k] b[n, k]) a_scales[m] b_scales[n] + bias[n] of
+    int8 codes a [M, K] and b [N, K] (K % 16 == 0), exact integer sums; bias
+    float32 [N] or None; bfloat16 or float32 output."""
+    lib = load_library()
+    _dev(a_codes, a_scales, b_codes, b_scales, bias)
+    _int8_operand(a_codes, a_scales, "gemm_int8: a")
+    _int8_operand(b_codes, b_scales, "gemm_int8: b")
+    M, K = a_codes.shape
+    N = b_codes.shape[0]
+    _need(b_codes.shape[1] == K, "gemm_int8: a and b must share K")
+    _need(bias is None or (bias.dtype == torch.float32 and bias.numel() == N), "gemm_int8: bias must be float32 [N]")
+    _need(out_dtype in _OUT, "out_dtype must be float32 or bfloat16")
+    out = torch.empty((M, N), dtype=out_dtype, device=a_codes.device)
+    check(lib.bsq_gemm_int8(a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(), b_scales.data_ptr(),
+                            _ptr(bias), M, N, K, out.data_ptr(), _OUT[out_dtype], _stream()), "bsq_gemm_int8")
+    return out
+
+
+def linear_int8(x, b_codes, b_scales, bias=None, out_dtype=None):
+    """gemm_int8 of quantize_int8(x) in one call: x [M, K] (float32 or bfloat16,
+    K <= 32768), weights int8 [N, K] with float32 scales [N]; out_dtype is x's
+    unless given. The same bits as the two calls."""
+    lib = load_library()
+    _dev(x, b_codes, b_scales, bias)
+    _need(x.dim() == 2, "linear_int8: x must be [M, K]")
+    dt = _dtype(x, "x")
+    _int8_operand(b_codes, b_scales, "linear_int8: b")
+    M, K = x.shape
+    N = b_codes.shape[0]
+    out_dtype = out_dtype or x.dtype
+    _need(b_codes.shape[1] == K, "linear_int8: x and b must share K")
+    _need(bias is None or (bias.dtype == torch.float32 and bias.numel() == N), "linear_int8: bias must be float32 [N]")
+    _need(out_dtype in _OUT, "out_dtype must be float32 or bfloat16")
+    out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+    wsb = lib.bsq_linear_int8_workspace(M, K)
+    ws = _ws(wsb, x.device)
+    check(lib.bsq_linear_int8(x.data_ptr(), dt, b_codes.data_ptr(), b_scales.data_ptr(), _ptr(bias), M, N, K,
+                              out.data_ptr(), _OUT[out_dtype], ws.data_ptr(), wsb, _stream()), "bsq_linear_int8")
+    return out
+
+
 def rht_s2f6_encode(x, signs):
     """Combine-codec sender: x [R, C] (float32 or bfloat16, C % 32 == 0) ->
     (codes u8 [R, C] two's-complement S2F6, scales u8 [R, C/32] UE8M0) of the

@@ -397,6 +397,103 @@ int bsq_route_noalloc(const int32_t* topk_ids, int64_t tokens, int64_t k, int64_
                       bsq_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Expert selection over router logits and its gradient (the router in front
+ * of bsq_route and of bsq_moe_few_nvfp4).
+ *
+ * bsq_moe_gate
+ *   logits   [tokens, E] of `dtype` (F32 or BF16).
+ *   The k largest logits of a token, largest first, ties to the lowest index.
+ *   Logits of -inf and NaN are masked: never selected, probability 0. Slots
+ *   past the last unmasked logit get id -1 and weight 0 (a row with all logits
+ *   masked holds nothing else).
+ *   renormalize  1: weights are the softmax over the selected logits, 0: over
+ *            all unmasked logits of the row. Float32 arithmetic.
+ *   weights  FP32 [tokens, k]; topk_ids int32 [tokens, k]. A row with a -1 is
+ *            no input for bsq_route, which takes ids in [0, E) alone.
+ *   A logit of +inf gives unspecified weights (the ids are as described).
+ * bsq_moe_gate_backward: gradient of sum dweights * weights to the logits, the
+ *   selection held fixed: w_j (g_j - sum_s w_s g_s) on the selected experts
+ *   and 0 elsewhere (renormalize 1), p_i ([i selected] g_i - sum_s w_s g_s)
+ *   with the softmax p over all unmasked logits (0).
+ *   dweights, weights, topk_ids  as above (ids outside [0, E) add nothing);
+ *   logits   the forward's (may be NULL when renormalize is 1).
+ *   dlogits  [tokens, E] of `dtype`, every element written.
+ * 1 <= E <= 1024, 1 <= k <= min(E, 64), tokens < 2^31. logits and dlogits
+ * 16-byte aligned, the others 4.
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, ENUM (renormalize), LAUNCH.
+ * ---------------------------------------------------------------------- */
+int bsq_moe_gate(const void* logits, int dtype, int64_t tokens, int64_t E, int64_t k, int renormalize,
+                 float* weights, int32_t* topk_ids, bsq_stream_t stream);
+int bsq_moe_gate_backward(const float* dweights, const float* weights, const int32_t* topk_ids,
+                          const void* logits, int dtype, int64_t tokens, int64_t E, int64_t k,
+                          int renormalize, void* dlogits, bsq_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A whole expert layer for a few tokens (decode), weights in NVFP4 and
+ * activations unquantized:
+ *   out[t] = sum_j topk_weights[t, j] W2_e (silu(G) * U),  (G; U) = W13_e x[t],
+ *   e = topk_ids[t, j];  silu(g) = g / (1 + e^-g).
+ * Only the experts that occur are read, each once.
+ * x, out   [tokens, hidden] of `dtype` (F32 or BF16).
+ * topk_ids int32 [tokens, k]; an id outside [0, E) (as bsq_moe_gate's -1) adds
+ *          nothing, a token without a valid id gets zeros. topk_weights FP32.
+ * w13_*    codes [E, 2*ffn, hidden/2], scales [E, 2*ffn, hidden/16], outer [E]:
+ *          gate rows [0, ffn), then up rows; w2_* [E, hidden, ffn/2], ... as
+ *          bsq_quantize_nvfp4 writes them with BSQ_OUTER_TENSOR.
+ * Products of exactly decoded weights with x in float32 sums; silu(G) * U is
+ * kept to 16 significant bits or more; a token's experts are added in slot
+ * order in float32 (the same bits on every call).
+ * hidden % 16 == 0, ffn % 16 == 0, both in [16, 32768]; 1 <= E <= 1024,
+ * 1 <= k <= 64, tokens * k <= BSQ_MOE_FEW_MAX_PAIRS (more tokens: the grouped
+ * GEMMs).
+ * ws       bsq_moe_few_nvfp4_workspace() bytes.
+ * x, out, codes, scales and ws 16-byte aligned, the others 4.
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, WORKSPACE, LAUNCH.
+ * ---------------------------------------------------------------------- */
+#define BSQ_MOE_FEW_MAX_PAIRS 2048
+size_t bsq_moe_few_nvfp4_workspace(int64_t tokens, int64_t hidden, int64_t ffn, int64_t E, int64_t k);
+int bsq_moe_few_nvfp4(const void* x, int dtype, int64_t tokens, int64_t hidden, int64_t ffn, int64_t E,
+                      int64_t k, const int32_t* topk_ids, const float* topk_weights,
+                      const uint8_t* w13_codes, const uint8_t* w13_scales, const float* w13_outer,
+                      const uint8_t* w2_codes, const uint8_t* w2_scales, const float* w2_outer, void* out,
+                      void* ws, size_t ws_bytes, bsq_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Dense products in 8-bit integers (attention projections, shared experts): a
+ * scale for each row of activations (token) and each row of weights (output
+ * channel).
+ *
+ * bsq_quantize_int8: x [rows, cols] of `dtype` -> codes int8 [rows, cols] and
+ *   scales FP32 [rows]: s = f32(max|x| / 127) per row, or 1 where that is below
+ *   2^-126 (all codes are then 0); code = rint(f32(x * f32(1/s))), half to
+ *   even, within [-127, 127].
+ * bsq_swiglu_quantize_int8: the same of silu(g) * u in float32, h13
+ *   [rows, 2*ffn] with gate columns [0, ffn), then up columns.
+ * bsq_gemm_int8: out[m, n] = (sum_k a[m, k] b[n, k]) a_scales[m] b_scales[n]
+ *   + bias[n]; a_codes int8 [M, K], b_codes int8 [N, K] (any codes, -128
+ *   included), exact integer sums; bias FP32 [N] or NULL; out [M, N] of
+ *   out_dtype (F32, or BF16 rounded to nearest even). K % 16 == 0,
+ *   16 <= K < 131072.
+ * bsq_linear_int8: bsq_gemm_int8 of bsq_quantize_int8(x [M, K]); the same bits
+ *   as the two calls. ws bsq_linear_int8_workspace() bytes.
+ * cols, ffn and (linear) K: multiples of 16 in [16, 32768]. rows, M, N < 2^31,
+ * ceil(M / 128) * ceil(N / 128) < 2^31.
+ * x, h13, codes and ws 16-byte aligned; out to its type; scales and bias 4.
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, WORKSPACE, LAUNCH.
+ * ---------------------------------------------------------------------- */
+int bsq_quantize_int8(const void* x, int dtype, int64_t rows, int64_t cols, int8_t* codes, float* scales,
+                      bsq_stream_t stream);
+int bsq_swiglu_quantize_int8(const void* h13, int dtype, int64_t rows, int64_t ffn, int8_t* codes,
+                             float* scales, bsq_stream_t stream);
+int bsq_gemm_int8(const int8_t* a_codes, const float* a_scales, const int8_t* b_codes,
+                  const float* b_scales, const float* bias, int64_t M, int64_t N, int64_t K, void* out,
+                  int out_dtype, bsq_stream_t stream);
+size_t bsq_linear_int8_workspace(int64_t M, int64_t K);
+int bsq_linear_int8(const void* x, int dtype, const int8_t* b_codes, const float* b_scales,
+                    const float* bias, int64_t M, int64_t N, int64_t K, void* out, int out_dtype, void* ws,
+                    size_t ws_bytes, bsq_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Combine codec ("Quantized communications": before the combine exchange an
  * expert output row is rotated by a 32-dimensional random Hadamard transform
  * and quantized to block-scaled S2F6, one UE8M0 scale per 32 values, 8.25

@@ -21,6 +21,8 @@ quant    NVFP4 round-to-nearest quantize, dequantize, MXFP8 quantize (RN/SR),
          passes" and "Re-quantization with stochastic rounding").
 gemm     fp64 references of the NVFP4 grouped GEMM and the MXFP8 DGRAD/WGRAD.
 route    top-k routing -> per-expert token segments ("Quantized communications").
+serving  fp64 references of the router's selection and gradient, the few-token
+         expert layer and the 8-bit dense products.
 
 Parity status: every function here is pinned by a CPU test under tests/
 (worked examples of the pages, closed forms, brute force on tiny inputs,
