@@ -1,7 +1,7 @@
 // Dense products in 8-bit integers: a scale for each row of activations (a
 // token) and each row of weights (an output channel).
 //
-//   x_q = rint(x / s),  s = max|x| / 127 per row
+//   x_q = rint(x / s),  s = max|x| / 127 per row (in float32: max|x| * f32(1/127), x * f32(1/s))
 //   y[m, n] = (sum_k a_q[m, k] b_q[n, k]) s_a[m] s_b[n] + bias[n]
 //
 // The integer sums are exact (int32: K is limited so that they cannot
@@ -53,10 +53,10 @@ __device__ __forceinline__ uint32_t codes4(const float* v, float inv) {
   return w;
 }
 
-// The row's scale: max / 127, or 1 where that would be below the normal range
+// The row's scale: max * f32(1/127), or 1 where that would be below the normal range
 // (its reciprocal could overflow); all codes of such a row are 0.
 __device__ __forceinline__ float row_scale(float amax) {
-  const float s = amax / 127.0f;
+  const float s = amax * (1.0f / 127.0f);
   return s >= kFltMinNormal ? s : 1.0f;
 }
 

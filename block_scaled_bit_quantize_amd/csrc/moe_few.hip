@@ -4,24 +4,33 @@
 //
 // The many-token chain gathers rows into 256-row tiles per expert; for a few
 // tokens an expert sees one to some tens of rows, and what bounds the layer is
-// reading the chosen experts' weights (0.5625 bytes a value) once. Here one
-// workgroup owns 32 weight rows of one expert (for W13: 16 gate rows and their
-// 16 up rows) for every token that chose it, its eight waves share the inner
-// dimension, so no weight or activation is read twice by a workgroup, and the
-// partial sums meet in LDS.
+// reading the chosen experts' weights (0.5625 bytes a value) once.
 //
-// Weights are decoded to bf16 exactly (an E2M1 value times its E4M3 scale has
-// at most 6 significant bits); the activations are split into bf16 terms that
-// add up to them (bf16 inputs: themselves; the float32 SwiGLU result: two,
-// 2^-16 of a value; float32 inputs: three, exact), so that
-// v_mfma_f32_16x16x32_bf16 multiplies them with float32 sums. The two outer
-// scales and the token's weight are applied to the float32 sums.
+// Both products run as streams: one workgroup per CU takes an equal share of
+// the (expert, row tile) sequence of the experts that occur. Its eight waves
+// share the inner dimension. A wave keeps its part of the activations of an
+// expert's tokens in registers and lets the weights pass by through a ring of
+// three places in LDS: loads that go straight to LDS (no registers in flight,
+// and 8 lanes side by side read a whole 128-byte line; with each lane reading
+// its own MFMA row the address unit took one lane a cycle and was the limit).
+// Up to 108 KB a CU are in flight, across tile ends too; the waves' partial
+// sums meet in LDS, in two buffers, with one barrier a tile that leaves the
+// loads in flight.
 //
-// Which expert a workgroup owns comes from the ids themselves: slot s is the
-// s-th smallest expert id that occurs, and grid rows past the last one exit.
-// Three launches: W13 with SwiGLU, W2 into one row per (token, slot) pair, and
-// the sum over a token's pairs in slot order (no atomics: the same bits every
-// time).
+// Weights are decoded to fp16 exactly (an E2M1 value times its E4M3 scale has
+// at most 6 significant bits and lies in [2^-10, 2688]): a convert and a
+// packed multiply, one instruction a weight. Activations are scaled by a power
+// of two for each token and wave, so that the largest lies near 2^14, and
+// split into fp16 terms: bf16 inputs are one exact term (values below 2^-31 of
+// the largest lose bits), float32 inputs and the SwiGLU result two (22 bits).
+// v_mfma_f32_16x16x32_f16 sums in float32; the powers of two are taken back
+// before the waves' sums are added, the outer scales and the token's weight
+// after.
+//
+// Which experts occur is read from the ids by every workgroup itself, so the
+// layer is three launches: W13 with SwiGLU, W2 into one row per (token, slot)
+// pair, and the sum over a token's pairs in slot order (no atomics: the same
+// bits every time).
 #include "bsq_device.h"
 #include "bsq_internal.h"
 
@@ -31,233 +40,575 @@ namespace {
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef u32x2 u32x2_a4 __attribute__((aligned(4)));
+typedef __amdgpu_buffer_rsrc_t brsrc_t;
 
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
 constexpr int kMaxPairs = BSQ_MOE_FEW_MAX_PAIRS;
-constexpr int kMT = 4;  // 16-pair tiles that share one decode of the weights
+constexpr int kMaxExperts = 1024;
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
 }
 
-// Two words (16 E2M1 codes) times one E4M3 scale -> 16 bf16 in 8 words.
-__device__ __forceinline__ void decode16(uint32_t w0, uint32_t w1, float s, uint32_t* out) {
-  const uint32_t w[2] = {w0, w1};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    f32x2 v;
-    v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], 1.0f, 0);
-    out[4 * i + 0] = pack_bf16(v[0] * s, v[1] * s);
-    v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], 1.0f, 1);
-    out[4 * i + 1] = pack_bf16(v[0] * s, v[1] * s);
-    v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], 1.0f, 2);
-    out[4 * i + 2] = pack_bf16(v[0] * s, v[1] * s);
-    v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], 1.0f, 3);
-    out[4 * i + 3] = pack_bf16(v[0] * s, v[1] * s);
-  }
-}
+// A value that is the same in every lane, told to the compiler (it goes to a
+// scalar register; descriptors and loop bounds made of it need no lane loops).
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// 16 activations -> NT terms of 8 words each. bf16 rows hold them as they are.
-template <int NT>
-__device__ __forceinline__ void load_terms(const uint16_t* p, uint32_t (&o)[NT][8]) {
-  static_assert(NT == 1, "bf16 rows are one term");
-  const u32x4 a = *reinterpret_cast<const u32x4*>(p), b = *reinterpret_cast<const u32x4*>(p + 8);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[0][i] = a[i], o[0][4 + i] = b[i];
+// Workgroup barrier that completes this wave's LDS operations and leaves its
+// loads in flight.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Operands are read through buffer descriptors: a 32-bit offset per lane, the
+// tile's and step's offset in a scalar register.
+__device__ __forceinline__ brsrc_t buffer(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, 0x00020000);
 }
-// float32 rows: the upper halves of the values' bits are exact bf16 terms whose
-// remainders are exact too; the last term is rounded.
-template <int NT>
-__device__ __forceinline__ void load_terms(const float* p, uint32_t (&o)[NT][8]) {
-  float v[16];
+constexpr uint32_t kPastEnd = 0x80000000u;  // past every buffer here: reads as zero
+
+// ---------------------------------------------------------------- operands
+// A step is 128 values of K: 8 blocks. Lane (c, g) = (lane % 16, lane / 16) of
+// a wave holds blocks 2 g and 2 g + 1 of a step for row c: of the weights 16
+// bytes of codes and two scales. Each of a step's four MFMAs takes 8 values of
+// every lane; the order of K is the same for the activations.
+
+// A step's 32 weights of a lane: four MFMA operands (kept as words: vectors of
+// halves took a register for each half where control flow joins).
+__device__ __forceinline__ uint32_t as_word(f16x2 v) { return __builtin_bit_cast(uint32_t, v); }
+__device__ __forceinline__ void decode(u32x4 codes, uint32_t scales, u32x4 (&o)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const f32x4 a = reinterpret_cast<const f32x4*>(p)[i];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[4 * i + j] = a[j];
+    const float s = i < 2 ? __builtin_amdgcn_cvt_f32_fp8((int)scales, 0) : __builtin_amdgcn_cvt_f32_fp8((int)scales, 1);
+    const f16x2 s2 = {(_Float16)s, (_Float16)s};
+    const uint32_t c = codes[i];
+    o[i] = (u32x4){as_word(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.0f, 0) * s2),
+                   as_word(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.0f, 1) * s2),
+                   as_word(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.0f, 2) * s2),
+                   as_word(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.0f, 3) * s2)};
   }
-#pragma unroll
-  for (int t = 0; t < NT - 1; ++t)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t a = __float_as_uint(v[2 * i]) & 0xFFFF0000u, b = __float_as_uint(v[2 * i + 1]) & 0xFFFF0000u;
-      o[t][i] = (a >> 16) | b;
-      v[2 * i] -= __uint_as_float(a);
-      v[2 * i + 1] -= __uint_as_float(b);
-    }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) o[NT - 1][i] = pack_bf16(v[2 * i], v[2 * i + 1]);
 }
 
-// The slot's expert and the pairs that chose it (ascending), or -1 when fewer
-// experts occur. Every thread calls it; list and bits are LDS.
-__device__ __forceinline__ int find_slot(const int32_t* __restrict__ ids, int pairs, int E, int slot, uint32_t* bits,
-                                         uint16_t* list, int* count) {
-  const int t = threadIdx.x, lane = t & 63;
-  if (t < 32) bits[t] = 0;
-  __syncthreads();
-  for (int p = t; p < pairs; p += kThreads) {
-    const int e = ids[p];
-    if (e >= 0 && e < E) atomicOr(&bits[e >> 5], 1u << (e & 31));
-  }
-  __syncthreads();
-  uint32_t word = lane < 32 ? bits[lane] : 0u;
-  const int mine = __popc(word);
-  int upto = mine;
+// A lane's 32 activations of a step as they lie in memory, blocks b0 and
+// b0 + 1, zeros unless the block is in [first, last). aoff: the lane's row in
+// bytes.
+template <typename T>
+struct Raw {
+  u32x4 v[32 * sizeof(T) / 16];
+};
+template <typename T>
+__device__ __forceinline__ Raw<T> load_raw(brsrc_t act, uint32_t aoff, int b0, int first, int last) {
+  constexpr int Z = (int)sizeof(T), N = 16 * Z / 16;
+  Raw<T> r;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up(upto, o, 64);
-    if (lane >= o) upto += v;
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t at = b0 + i >= first && b0 + i < last ? aoff + (uint32_t)(b0 + i) * (16 * Z) : kPastEnd;
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+      r.v[i * N + q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(act, at, q * 16, 0));
   }
-  const uint64_t hit = __ballot(lane < 32 && upto - mine <= slot && slot < upto);
-  if (!hit) return -1;
-  const int src = __ffsll((unsigned long long)hit) - 1;
-  word = (uint32_t)__shfl((int)word, src, 64);
-  int skip = slot - __shfl(upto - mine, src, 64);
-  for (; skip > 0; --skip) word &= word - 1;
-  const int expert = src * 32 + __ffs((int)word) - 1;
-  if (t < 64) {
-    int n = 0;
-    for (int p0 = 0; p0 < pairs; p0 += 64) {
-      const bool is = p0 + lane < pairs && ids[p0 + lane] == expert;
-      const uint64_t b = __ballot(is);
-      if (is) list[n + __popcll(b & ((1ull << lane) - 1))] = (uint16_t)(p0 + lane);
-      n += __popcll(b);
-    }
-    if (lane == 0) *count = n;
-  }
-  __syncthreads();
-  return expert;
+  return r;
 }
-
-// One 32-row slice of one expert's product. GLU (W13): rows [f0, f0 + 16) of
-// the gate half and of the up half; out[pair, f] = silu(gate) * up. Otherwise
-// (W2): rows [n0, n0 + 32); out[pair, n] = weight[pair] * product.
-// Row of activations of pair p: in + (GLU ? p / k : p) * K.
-template <typename T, int NT, bool GLU>
-__global__ __launch_bounds__(kThreads) void k_moe_part(const T* __restrict__ in, const int32_t* __restrict__ ids,
-                                                      const float* __restrict__ pair_weight, int pairs, int k, int E,
-                                                      int K, int rows, const uint8_t* __restrict__ codes,
-                                                      const uint8_t* __restrict__ scales,
-                                                      const float* __restrict__ outer, float* __restrict__ out) {
-  __shared__ uint32_t bits[32];
-  __shared__ uint16_t list[kMaxPairs];
-  __shared__ int count;
-  __shared__ f32x4 part[kWaves][2][kMT][64];
-  const int expert = find_slot(ids, pairs, E, (int)blockIdx.y, bits, list, &count);
-  if (expert < 0) return;
-  const int np = count;
-  const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
-  const int col = lane & 15, grp = lane >> 4;
-  // weight rows of this lane in the two 16-row tiles (clamped rows are computed and not stored)
-  const int f0 = (int)blockIdx.x * (GLU ? 16 : 32);
-  const int width = GLU ? rows / 2 : rows;  // outputs per pair
-  int r[2];
+__device__ __forceinline__ float raw_get(const Raw<uint16_t>& r, int i) {
+  const uint32_t w = r.v[i / 8][(i % 8) / 2];
+  return i & 1 ? bf16_hi(w) : bf16_lo(w);
+}
+__device__ __forceinline__ float raw_get(const Raw<float>& r, int i) { return __uint_as_float(r.v[i / 4][i % 4]); }
+template <typename T>
+__device__ __forceinline__ float raw_max(const Raw<T>& r, float m) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int f = f0 + (GLU ? 0 : 16 * i) + col;
-    r[i] = (f < width ? f : width - 1) + (GLU ? i * width : 0);
-  }
-  const uint8_t* crow[2];
-  const uint8_t* srow[2];
+  for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(raw_get(r, i)));
+  return m;
+}
+// NT fp16 terms of the activations times `scale`: rounded to nearest, the next
+// term takes the (exact) remainder.
+template <typename T, int NT>
+__device__ __forceinline__ void split(const Raw<T>& r, float scale, u32x4 (&o)[NT][4]) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    crow[i] = codes + ((int64_t)expert * rows + r[i]) * (K / 2);
-    srow[i] = scales + ((int64_t)expert * rows + r[i]) * (K / 16);
-  }
-  const float so = outer[expert];
-  const int nblk = K / 16;                    // blocks of 16 along K
-  const int steps = (nblk + 7) / 8;           // 128 values: two blocks per 16-lane group
-  for (int mt0 = 0; mt0 < np; mt0 += 16 * kMT) {
-    const int tiles = (np - mt0 + 15) / 16 < kMT ? (np - mt0 + 15) / 16 : kMT;
-    const T* arow[kMT];
-    bool have[kMT];
+  for (int q = 0; q < 4; ++q) {
+    float v[8];
 #pragma unroll
-    for (int m = 0; m < kMT; ++m) {
-      const int q = mt0 + 16 * m + col;
-      have[m] = q < np;
-      const int p = list[have[m] ? q : mt0];
-      arow[m] = in + (int64_t)(GLU ? p / k : p) * K;
-    }
-    f32x4 acc[2][kMT] = {};
-    for (int st = wave; st < steps; st += kWaves) {
+    for (int i = 0; i < 8; ++i) v[i] = raw_get(r, 8 * q + i) * scale;
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int blk = st * 8 + grp * 2 + b;
-        const bool in_k = blk < nblk;
-        uint32_t wd[2][8];
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          u32x2 c = {0u, 0u};
-          uint32_t s8 = 0;
-          if (in_k) {
-            c = *reinterpret_cast<const u32x2_a4*>(crow[i] + blk * 8);
-            s8 = srow[i][blk];
-          }
-          decode16(c[0], c[1], e4m3_val(s8), wd[i]);
+      for (int i = 0; i < 4; ++i) {
+        const f16x2 h = __builtin_convertvector((f32x2){v[2 * i], v[2 * i + 1]}, f16x2);
+        o[t][q][i] = as_word(h);
+        if (t + 1 < NT) {
+          v[2 * i] -= (float)h[0];
+          v[2 * i + 1] -= (float)h[1];
         }
+      }
+  }
+}
+
+// The power of two that brings a maximum into [2^14, 2^15), and its inverse,
+// from the exponent bits; below 2^-111 and for infinities the nearest usable.
+struct Scale {
+  float up, down;
+};
+__device__ __forceinline__ Scale scale_for(float amax) {
+  int e = (int)(__float_as_uint(amax) >> 23);
+  e = e < 16 ? 16 : e > 254 ? 254 : e;
+  return {__uint_as_float((uint32_t)(268 - e) << 23), __uint_as_float((uint32_t)(e - 14) << 23)};
+}
+
+template <int NT>
+__device__ __forceinline__ f32x4 multiply(const u32x4 (&w)[4], const u32x4 (&a)[NT][4], f32x4 acc) {
 #pragma unroll
-        for (int m = 0; m < kMT; ++m) {
-          if (m >= tiles) break;
-          uint32_t a[NT][8] = {};
-          if (in_k && have[m]) load_terms<NT>(arow[m] + blk * 16, a);
+  for (int q = 0; q < 4; ++q)
 #pragma unroll
-          for (int q = 0; q < NT; ++q)
+    for (int t = 0; t < NT; ++t)
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, w[q]), __builtin_bit_cast(f16x8, a[t][q]),
+                                                   acc, 0, 0, 0);
+  return acc;
+}
+
+// ---------------------------------------------------------------- which experts
+// The ids of all pairs, spread over the workgroup's registers, and a bitmap of
+// the experts that occur. Slot s is the s-th smallest of them.
+struct RouteLds {
+  uint32_t bits[kMaxExperts / 32];
+  int count[kMaxPairs / kThreads * kWaves];
+  uint16_t list[kMaxPairs];
+};
+struct Route {
+  static constexpr int C = kMaxPairs / kThreads;
+  int id[C];
+  int words;   // lane l holds bitmap word l % 32
+  int active;  // experts that occur
+
+  __device__ __forceinline__ void init(const int32_t* __restrict__ ids, int pairs, int E, RouteLds& lds) {
+    const int t = threadIdx.x, lane = t & 63;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int p = t + c * kThreads;
+      id[c] = -1;
+      if (c * kThreads < pairs) {
+        const int v = ids[p < pairs ? p : 0];
+        id[c] = p < pairs && v < E ? v : -1;
+      }
+    }
+    if (t < kMaxExperts / 32) lds.bits[t] = 0;
+    lds_barrier();
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (id[c] >= 0) atomicOr(&lds.bits[id[c] >> 5], 1u << (id[c] & 31));
+    lds_barrier();
+    words = (int)lds.bits[lane & 31];
+    active = 0;
+    for (int w = 0; w * 32 < E; ++w) active += __popc((uint32_t)__builtin_amdgcn_readlane(words, w));
+  }
+
+  // The expert of a slot below `active`, counted out by the scalar unit.
+  __device__ __forceinline__ int expert_of(int slot) const {
+    int at = 0, before = 0;
+    uint32_t word = 0;
+#pragma unroll 1
+    for (; at < kMaxExperts / 32; ++at) {
+      word = (uint32_t)__builtin_amdgcn_readlane(words, at);
+      const int n = __popc(word);
+      if (before + n > slot) break;
+      before += n;
+    }
+    for (; before < slot; ++before) word &= word - 1;
+    return at * 32 + __ffs((int)word) - 1;
+  }
+
+  // Writes the pairs of an expert into lds.list, ascending, and returns how
+  // many they are. Every wave calls it, after its last use of the list before.
+  __device__ __forceinline__ int list_pairs(int expert, int pairs, RouteLds& lds) const {
+    const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
+    uint64_t mask[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      mask[c] = __ballot(id[c] == expert);
+      if (lane == 0) lds.count[c * kWaves + wave] = __popcll(mask[c]);
+    }
+    lds_barrier();
+    const int counts = lds.count[lane & (C * kWaves - 1)];
+    int n = 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if (c * kThreads < pairs) {
+        int mine = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+          if (w == wave) mine = n;
+          n += __builtin_amdgcn_readlane(counts, c * kWaves + w);
+        }
+        if (id[c] == expert) lds.list[mine + __popcll(mask[c] & ((1ull << lane) - 1))] = (uint16_t)(t + c * kThreads);
+      }
+    }
+    lds_barrier();
+    return n;
+  }
+};
+
+// ---------------------------------------------------------------- the stream
+struct Product {
+  const void* in;         // activations: row of pair p is (GLU ? p / k : p)
+  const int32_t* ids;
+  const float* weight;    // of a pair (not GLU)
+  int pairs, k, E, K;
+  int width;              // outputs of a pair
+  const uint8_t* codes;
+  const uint8_t* scales;
+  const float* outer;
+  float* out;             // [pairs, width]
+};
+
+// The end of a tile: the waves' partial sums of 16 x 16 outputs meet in LDS and
+// are stored. GLU (W13): the tiles are gate rows, then their up rows, and the
+// result is silu(gate) * up. Otherwise (W2) RT * 16 rows, times the pair's
+// weight. One barrier, which leaves loads in flight; the caller alternates
+// between two buffers.
+template <bool GLU, int RT>
+__device__ __forceinline__ void finish(const Product& a, float (&part)[kWaves][RT][256], const f32x4 (&acc)[RT],
+                                       float down, int tile, int mt0, int np, float so, const uint16_t* list) {
+  constexpr int OUT = GLU ? RT * 8 : RT * 16, PER = OUT * 16;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int i = 0; i < RT; ++i) *reinterpret_cast<f32x4*>(&part[wave][i][lane * 4]) = acc[i] * down;
+  lds_barrier();
+  int o0 = threadIdx.x;
+  asm volatile("" : "+v"(o0));  // its addresses are formed here, not kept in registers over the stream
+  // float j of a 16 x 16 tile is row 4 (j / 64) + j % 4 of pair j / 4 % 16
+  for (int o = o0; o < PER; o += kThreads) {
+    const int i = o / 256, j = o % 256;
+    const int q = mt0 + (j >> 2 & 15);
+    const int f = tile * OUT + 16 * i + 4 * (j >> 6) + (j & 3);
+    float v = part[0][i][j];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) v += part[w][i][j];
+    if constexpr (GLU) {
+      float up = part[0][i + RT / 2][j];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) up += part[w][i + RT / 2][j];
+      const float g = v * so;
+      v = g / (1.0f + expf(-g)) * (up * so);
+    }
+    if (q < np && f < a.width) {
+      const int p = list[q];
+      if constexpr (!GLU) v *= a.weight[p] * so;
+      a.out[(int64_t)p * a.width + f] = v;
+    }
+  }
+}
+
+// Any K: weights and activations straight to registers, read again for every
+// tile (rows too long for k_moe_stream's registers, and rows of one block).
+template <typename T, int NT, bool GLU, int RT>
+__global__ __launch_bounds__(kThreads, 2) void k_moe_any(Product a) {
+  constexpr int OUT = GLU ? RT * 8 : RT * 16;  // outputs of a tile
+  __shared__ RouteLds lds;
+  __shared__ float part[2][kWaves][RT][256];
+  const int t = threadIdx.x, wave = uniform(t >> 6), lane = t & 63;
+  const int col = lane & 15, grp = lane >> 4;
+  Route route;
+  route.init(a.ids, a.pairs, a.E, lds);
+  const int tiles = (a.width + OUT - 1) / OUT;
+  const int64_t units = (int64_t)route.active * tiles;
+  int u = uniform((int)(units * blockIdx.x / gridDim.x));
+  const int u1 = uniform((int)(units * (blockIdx.x + 1) / gridDim.x));
+  const int nblk = a.K / 16;
+  const int steps = (nblk + 7) / 8;
+  const int st0 = steps * wave / kWaves, st1 = steps * (wave + 1) / kWaves;
+  const int rows = GLU ? 2 * a.width : a.width;
+  const brsrc_t act = buffer(a.in, (int64_t)(GLU ? a.pairs / a.k : a.pairs) * a.K * (int)sizeof(T));
+  int buf = 0;
+  while (u < u1) {
+    const int slot = u / tiles, tile0 = u - slot * tiles;
+    const int tile1 = tile0 + (u1 - u) < tiles ? tile0 + (u1 - u) : tiles;
+    u += tile1 - tile0;
+    const int expert = uniform(route.expert_of(slot));
+    const int np = uniform(route.list_pairs(expert, a.pairs, lds));
+    const int64_t wrow = (int64_t)expert * rows;
+    const brsrc_t codes = buffer(a.codes + wrow * (a.K / 2), (int64_t)rows * (a.K / 2));
+    const brsrc_t scales = buffer(a.scales + wrow * nblk, (int64_t)rows * nblk);
+    const float so = a.outer[expert];
+#pragma unroll 1
+    for (int mt0 = 0; mt0 < np; mt0 += 16) {
+      const int mine = lds.list[mt0 + col < np ? mt0 + col : mt0];
+      const uint32_t aoff = (uint32_t)((GLU ? mine / a.k : mine) * a.K) * (uint32_t)sizeof(T);
+      auto raw_at = [&](int st) {
+        const int b = st * 8 + grp * 2;
+        return load_raw<T>(act, aoff, b, b, nblk);
+      };
+      float mx = 0.0f;
+      for (int st = st0; st < st1; ++st) mx = raw_max(raw_at(st), mx);
+      mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+      mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+      const Scale sc = scale_for(mx);
+#pragma unroll 1
+      for (int tile = tile0; tile < tile1; ++tile) {
+        f32x4 acc[RT] = {};
+#pragma unroll 1
+        for (int st = st0; st < st1; ++st) {
+          u32x4 x[NT][4];
+          split<T, NT>(raw_at(st), sc.up, x);
+          const int b = st * 8 + grp * 2;
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            const int f = tile * OUT + 16 * (GLU ? i % (RT / 2) : i) + col;
+            const uint32_t r = (uint32_t)((f < a.width ? f : a.width - 1) + (GLU && i >= RT / 2 ? a.width : 0)) * nblk + b;
+            u32x4 c;
+            uint32_t s8 = 0;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const bf16x8 bv = __builtin_bit_cast(
-                  bf16x8, (u32x4){a[q][4 * h], a[q][4 * h + 1], a[q][4 * h + 2], a[q][4 * h + 3]});
+              const bool in = b + h < nblk;
+              const u32x2 w = __builtin_bit_cast(
+                  u32x2, __builtin_amdgcn_raw_buffer_load_b64(codes, in ? (r + h) * 8 : kPastEnd, 0, 0));
+              c[2 * h] = w[0];
+              c[2 * h + 1] = w[1];
+              s8 |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(scales, in ? r + h : kPastEnd, 0, 0) << (8 * h);
+            }
+            u32x4 d[4];
+            decode(c, s8, d);
+            acc[i] = multiply<NT>(d, x, acc[i]);
+          }
+        }
+        finish<GLU, RT>(a, part[buf], acc, sc.down, tile, mt0, np, so, lds.list);
+        buf ^= 1;
+      }
+    }
+    lds_barrier();  // the list is rewritten next
+  }
+}
+
+// ---------------------------------------------------------------- loads to LDS
+// 64 lanes of SIZE bytes (4 or 16) each: lane l's at lds + l * SIZE. Written as
+// asm because the waits are counted here: the compiler would have to take every
+// LDS read for one that may meet the newest load. There is no register to be
+// overwritten in flight; the address registers are read at issue.
+typedef uint32_t rsrc_words __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ rsrc_words descriptor(const void* p, uint32_t bytes) {
+  const uint64_t at = (uint64_t)p;
+  return (rsrc_words){(uint32_t)uniform((int)(uint32_t)at), (uint32_t)uniform((int)(uint32_t)(at >> 32)) & 0xFFFFu,
+                      (uint32_t)uniform((int)bytes), 0x00020000u};
+}
+template <int SIZE>
+__device__ __forceinline__ void load_to_lds(rsrc_words rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
+  static_assert(SIZE == 4 || SIZE == 16, "sizes of the instruction");
+  if constexpr (SIZE == 16)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
+                 "s"(rsrc), "s"(soff)
+                 : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
+                 "s"(rsrc), "s"(soff)
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_loads() {  // all but the N youngest
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return (uint32_t)uniform((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p);
+}
+
+// One place of a wave's ring: a span (256 values of K, 16 blocks) of 32 weight
+// rows. Codes as four loads of 8 rows of 128 bytes, the eight 16-byte pieces of
+// row c in the order piece ^ (c / 2 % 8), so that 16 rows at one piece meet 16
+// different banks. Scales as one load of 16 bytes a row, or, where rows of
+// scales are not aligned, five aligned words a row.
+struct Place {
+  u32x4 codes[4][64];
+  uint32_t scales[256];
+};
+
+// S: spans of a wave. EVEN: K % 256 == 0. A tile is two 16-row tiles (W13: 16
+// gate rows and their up rows; W2: 32 rows), 16 pairs one pass over them.
+template <typename T, int NT, bool GLU, int S, bool EVEN>
+__global__ __launch_bounds__(kThreads, 2) void k_moe_stream(Product a) {
+  constexpr int R = 3;                        // places of the ring
+  constexpr int LOADS = EVEN ? 5 : 7;         // of a span
+  constexpr int OUT = GLU ? 16 : 32;          // outputs of a tile
+  __shared__ RouteLds lds;
+  __shared__ float part[2][kWaves][2][256];
+  __shared__ Place ring[R][kWaves];
+  const int t = threadIdx.x, wave = uniform(t >> 6), lane = t & 63;
+  const int col = lane & 15, grp = lane >> 4;
+  Route route;
+  route.init(a.ids, a.pairs, a.E, lds);
+  const int tiles = (a.width + OUT - 1) / OUT;
+  const int64_t units = (int64_t)route.active * tiles;
+  int u = uniform((int)(units * blockIdx.x / gridDim.x));
+  const int u1 = uniform((int)(units * (blockIdx.x + 1) / gridDim.x));
+  const int nblk = a.K / 16;
+  const int pitch = nblk * 8;  // bytes of a row's codes
+  const int spans = (nblk + 15) / 16;
+  const int sp0 = spans * wave / kWaves, cnt = spans * (wave + 1) / kWaves - sp0;
+  const int rows = GLU ? 2 * a.width : a.width;
+  const int up = GLU ? a.width : 16;  // from a row of the first 16-row tile to the second's
+  const brsrc_t act = buffer(a.in, (int64_t)(GLU ? a.pairs / a.k : a.pairs) * a.K * (int)sizeof(T));
+  // In a last span that is not whole, pieces past the end move back to the
+  // row's last two blocks; the activations are zero where another lane has one.
+  auto block_of = [&](int span, int piece) {
+    const int b = span * 16 + piece * 2;
+    return EVEN || b < nblk - 2 ? b : nblk - 2;
+  };
+  // this lane's share of the loads: codes, rows 8 b + lane / 8 of the tile's 32
+  uint32_t coff[4], piece[2];
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const bf16x8 av = __builtin_bit_cast(
-                    bf16x8, (u32x4){wd[i][4 * h], wd[i][4 * h + 1], wd[i][4 * h + 2], wd[i][4 * h + 3]});
-                acc[i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, bv, acc[i][m], 0, 0, 0);
-              }
+  for (int b = 0; b < 4; ++b) {
+    const int c = (b & 1) * 8 + (lane >> 3);
+    piece[b & 1] = (lane & 7) ^ (c >> 1 & 7);
+    coff[b] = (uint32_t)(c + (b >> 1) * up) * pitch + (EVEN ? piece[b & 1] * 16 : 0);
+  }
+  // its own 16-byte piece of rows col and 16 + col at piece grp, and the same at piece 4 + grp
+  const int mine0 = (col >> 3) * 64 + (col & 7) * 8 + (grp ^ (col >> 1 & 7)), mine1 = mine0 ^ 4;
+  int buf = 0;
+  while (u < u1) {
+    const int slot = u / tiles, tile0 = u - slot * tiles;
+    const int tile1 = tile0 + (u1 - u) < tiles ? tile0 + (u1 - u) : tiles;
+    u += tile1 - tile0;
+    const int expert = uniform(route.expert_of(slot));
+    const int np = uniform(route.list_pairs(expert, a.pairs, lds));
+    const int64_t wrow = (int64_t)expert * rows;
+    const rsrc_words codes = descriptor(a.codes + wrow * pitch, (uint32_t)rows * pitch);
+    const uint8_t* sbase = a.scales + wrow * nblk;
+    const uint32_t phase = EVEN ? 0u : (uint32_t)((uintptr_t)sbase & 15u);  // aligned words from an aligned base
+    const rsrc_words scales = descriptor(sbase - phase, (phase + (uint32_t)rows * nblk + 3u) & ~3u);
+    const float so = a.outer[expert];
+
+    // the loads of span s of this wave for a tile, into one place of the ring; past the last tile, and for a span that
+    // this wave has not, they are issued all the same (the waits count them) but past the buffers' ends
+    auto fetch = [&](int tile, int s, int place) {
+      const bool some = tile < tile1 && s < cnt;
+      const bool both = GLU || tile * 32 + 16 < a.width;
+      const int span = sp0 + s;
+      const uint32_t at = lds_offset(&ring[place][wave]);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const uint32_t v = EVEN ? coff[b] : coff[b] + (uint32_t)block_of(span, piece[b & 1]) * 8;
+        load_to_lds<16>(codes, some && (both || b < 2) ? v : kPastEnd, (uint32_t)(tile * OUT) * pitch + (EVEN ? span * 128 : 0),
+                        at + b * 1024);
+      }
+      if constexpr (EVEN) {
+        const int r = (lane & 15) + (lane >> 4 & 1) * up;
+        load_to_lds<16>(scales, some && lane < 32 && (both || lane < 16) ? (uint32_t)r * nblk : kPastEnd,
+                        (uint32_t)(tile * OUT) * nblk + span * 16, at + 4096);
+      } else {
+        const int w0 = block_of(span, 0);
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+          const int i = j * 64 + lane, rr = i / 5;
+          const uint32_t r = tile * OUT + (rr & 15) + (rr >> 4) * up;
+          load_to_lds<4>(scales, some && i < 160 && (both || rr < 16) ? ((phase + r * nblk + w0) & ~3u) + i % 5 * 4 : kPastEnd,
+                         0, at + 4096 + j * 256);
+        }
+      }
+    };
+
+#pragma unroll 1
+    for (int mt0 = 0; mt0 < np; mt0 += 16) {
+      // lanes past the last pair repeat one and are not stored
+      const int pair = lds.list[mt0 + col < np ? mt0 + col : mt0];
+      const uint32_t aoff = (uint32_t)((GLU ? pair / a.k : pair) * a.K) * (uint32_t)sizeof(T);
+      u32x4 x[S][2][NT][4];
+      Scale sc;
+      {
+        // G spans at a time; where that is not all, they are read once for the maximum and once to be split
+        constexpr int G = S > 2 ? S / 2 : S;
+        Raw<T> raw[G][2];
+        auto read = [&](int g) {
+#pragma unroll
+          for (int s = 0; s < G; ++s)
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+              raw[s][p] = load_raw<T>(act, aoff, block_of(sp0 + g + s, 4 * p + grp),
+                                      g + s < cnt ? (sp0 + g + s) * 16 + 2 * (4 * p + grp) : nblk, nblk);
+          __builtin_amdgcn_sched_barrier(0);
+        };
+        auto start = [&] {
+          wait_loads<0>();  // what was in flight to the ring's places before, too
+#pragma unroll
+          for (int i = 0; i < R; ++i) fetch(tile0 + i / S, i % S, i);
+          __builtin_amdgcn_sched_barrier(0);
+        };
+        float mx = 0.0f;
+#pragma unroll
+        for (int g = 0; g < S; g += G) {
+          read(g);
+          if (G == S) start();
+#pragma unroll
+          for (int s = 0; s < G; ++s)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              mx = raw_max(raw[s][p], mx);
+              __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+        mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+        sc = scale_for(mx);
+#pragma unroll
+        for (int g = 0; g < S; g += G) {
+          if (G < S) read(g);
+          if (G < S && g + G == S) start();
+#pragma unroll
+          for (int s = 0; s < G; ++s)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              split<T, NT>(raw[s][p], sc.up, x[g + s][p]);
+              __builtin_amdgcn_sched_barrier(0);
             }
         }
       }
-    }
+      int place = 0;
+#pragma unroll 1
+      for (int tile = tile0; tile < tile1; ++tile) {
+        f32x4 acc[2] = {};
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+        for (int s = 0; s < S; ++s) {
+          wait_loads<(R - 1) * LOADS>();
+          if (s < cnt) {
+            const Place& pl = ring[place][wave];
+            u32x4 c[2][2];
+            uint32_t s8[2][2];
 #pragma unroll
-      for (int m = 0; m < kMT; ++m)
-        if (m < tiles) part[wave][i][m][lane] = acc[i][m];
-    __syncthreads();
-    // 64 threads per 16-pair tile; a lane holds 4 consecutive rows of one pair
-    for (int j = t; j < tiles * 64; j += kThreads) {
-      const int m = j >> 6, l = j & 63;
-      const int q = mt0 + 16 * m + (l & 15);
-      f32x4 s0 = part[0][0][m][l], s1 = part[0][1][m][l];
+            for (int p = 0; p < 2; ++p)
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) {
-        s0 += part[w][0][m][l];
-        s1 += part[w][1][m][l];
-      }
-      if (q >= np) continue;
-      const int p = list[q];
-      const int fr = f0 + 4 * (l >> 4);
-      float* o = out + (int64_t)p * width;
-      if constexpr (GLU) {
-        f32x4 v;
+              for (int i = 0; i < 2; ++i) {
+                c[p][i] = (&pl.codes[0][0])[i * 128 + (p ? mine1 : mine0)];
+                if constexpr (EVEN) {
+                  s8[p][i] = reinterpret_cast<const uint16_t*>(pl.scales)[(i * 16 + col) * 8 + 4 * p + grp];
+                } else {
+                  const int w0 = block_of(sp0 + s, 0);
+                  const uint32_t r = tile * OUT + col + i * up;
+                  const uint8_t* q = reinterpret_cast<const uint8_t*>(pl.scales) + (i * 16 + col) * 20 +
+                                     ((phase + r * nblk + w0) & 3u) + (block_of(sp0 + s, 4 * p + grp) - w0);
+                  s8[p][i] = (uint32_t)q[0] | (uint32_t)q[1] << 8;
+                }
+              }
+            wait_lds();  // the place may be filled again
+            fetch(tile + (s + R) / S, (s + R) % S, place);
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const float g = s0[z] * so, u = s1[z] * so;
-          v[z] = g / (1.0f + expf(-g)) * u;
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                u32x4 d[4];
+                decode(c[p][i], s8[p][i], d);
+                acc[i] = multiply<NT>(d, x[s][p], acc[i]);
+              }
+          } else {
+            fetch(tile + (s + R) / S, (s + R) % S, place);
+          }
+          place = place == R - 1 ? 0 : place + 1;
+          __builtin_amdgcn_sched_barrier(0);
         }
-        if (fr < width) *reinterpret_cast<f32x4*>(o + fr) = v;  // width % 16 == 0: whole or not at all
-      } else {
-        const float ws = pair_weight[p] * so;
-        if (fr < width) *reinterpret_cast<f32x4*>(o + fr) = s0 * ws;
-        if (fr + 16 < width) *reinterpret_cast<f32x4*>(o + fr + 16) = s1 * ws;
+        finish<GLU, 2>(a, part[buf], acc, sc.down, tile, mt0, np, so, lds.list);
+        buf ^= 1;
       }
     }
-    __syncthreads();
+    lds_barrier();  // the list is rewritten next
   }
 }
 
@@ -281,25 +632,39 @@ __global__ __launch_bounds__(256) void k_moe_sum(const float* __restrict__ z, co
   }
 }
 
-template <typename T, int NT, int NH>
+// Registers hold up to 128 words of activations: 32 for each span of a wave
+// (eight waves to K) and term. Longer rows are read again for every tile.
+template <typename T, int NT, bool GLU, bool EVEN>
+bool launch_stream_k(const Product& a, hipStream_t s) {
+  const int spans = (a.K / 16 + 15) / 16;
+  const dim3 grid((unsigned)bsqh::device_cus()), block(kThreads);
+  if (spans * NT <= 16) hipLaunchKernelGGL((k_moe_stream<T, NT, GLU, 2 / NT, EVEN>), grid, block, 0, s, a);
+  else if (spans * NT <= 32) hipLaunchKernelGGL((k_moe_stream<T, NT, GLU, 4 / NT, EVEN>), grid, block, 0, s, a);
+  else return false;
+  return true;
+}
+template <typename T, int NT, bool GLU>
+void launch_stream(const Product& a, hipStream_t s) {
+  if (a.K >= 32 && (a.K % 256 == 0 ? launch_stream_k<T, NT, GLU, true>(a, s) : launch_stream_k<T, NT, GLU, false>(a, s)))
+    return;
+  hipLaunchKernelGGL((k_moe_any<T, NT, GLU, 2>), dim3((unsigned)bsqh::device_cus()), dim3(kThreads), 0, s, a);
+}
+
+template <typename T, int NT>
 void launch_layer(const T* x, int64_t tokens, int64_t H, int64_t F, int64_t E, int64_t k, const int32_t* ids,
                   const float* weights, const uint8_t* w13c, const uint8_t* w13s, const float* w13o,
                   const uint8_t* w2c, const uint8_t* w2s, const float* w2o, T* out, float* h, float* z,
                   hipStream_t s) {
   const int pairs = (int)(tokens * k);
-  const unsigned slots = (unsigned)(pairs < E ? pairs : E);
-  hipLaunchKernelGGL((k_moe_part<T, NT, true>), dim3((unsigned)((F + 15) / 16), slots), dim3(kThreads), 0, s, x, ids,
-                     weights, pairs, (int)k, (int)E, (int)H, (int)(2 * F), w13c, w13s, w13o, h);
-  hipLaunchKernelGGL((k_moe_part<float, NH, false>), dim3((unsigned)((H + 31) / 32), slots), dim3(kThreads), 0, s,
-                     static_cast<const float*>(h), ids, weights, pairs, (int)k, (int)E, (int)F, (int)H, w2c, w2s, w2o,
-                     z);
+  launch_stream<T, NT, true>({x, ids, weights, pairs, (int)k, (int)E, (int)H, (int)F, w13c, w13s, w13o, h}, s);
+  launch_stream<float, 2, false>({h, ids, weights, pairs, (int)k, (int)E, (int)F, (int)H, w2c, w2s, w2o, z}, s);
   hipLaunchKernelGGL((k_moe_sum<T>), dim3((unsigned)((tokens * (H / 4) + 255) / 256)), dim3(256), 0, s,
                      static_cast<const float*>(z), ids, (int)tokens, (int)k, (int)E, (int)H, out);
 }
 
 bool shape_ok(int64_t tokens, int64_t hidden, int64_t ffn, int64_t E, int64_t k) {
   return tokens >= 0 && hidden >= 16 && hidden % 16 == 0 && hidden <= 32768 && ffn >= 16 && ffn % 16 == 0 &&
-         ffn <= 32768 && E >= 1 && E <= 1024 && k >= 1 && k <= 64 && tokens <= kMaxPairs / k;
+         ffn <= 32768 && E >= 1 && E <= kMaxExperts && k >= 1 && k <= 64 && tokens <= kMaxPairs / k;
 }
 
 }  // namespace
@@ -327,15 +692,14 @@ extern "C" int bsq_moe_few_nvfp4(const void* x, int dtype, int64_t tokens, int64
               BSQ_E_ALIGN);
   BSQ_REQUIRE(ws_bytes >= bsq_moe_few_nvfp4_workspace(tokens, hidden, ffn, E, k), BSQ_E_WORKSPACE);
   hipStream_t s = bsqh::as_stream(stream);
-  float* h = static_cast<float*>(ws);            // [pairs, ffn]
-  float* z = h + tokens * k * ffn;               // [pairs, hidden]
+  float* h = static_cast<float*>(ws);  // [pairs, ffn]
+  float* z = h + tokens * k * ffn;     // [pairs, hidden]
   if (dtype == BSQ_BF16)
-    launch_layer<uint16_t, 1, 2>(static_cast<const uint16_t*>(x), tokens, hidden, ffn, E, k, topk_ids, topk_weights,
-                                 w13_codes, w13_scales, w13_outer, w2_codes, w2_scales, w2_outer,
-                                 static_cast<uint16_t*>(out), h, z, s);
-  else
-    launch_layer<float, 3, 3>(static_cast<const float*>(x), tokens, hidden, ffn, E, k, topk_ids, topk_weights,
+    launch_layer<uint16_t, 1>(static_cast<const uint16_t*>(x), tokens, hidden, ffn, E, k, topk_ids, topk_weights,
                               w13_codes, w13_scales, w13_outer, w2_codes, w2_scales, w2_outer,
-                              static_cast<float*>(out), h, z, s);
+                              static_cast<uint16_t*>(out), h, z, s);
+  else
+    launch_layer<float, 2>(static_cast<const float*>(x), tokens, hidden, ffn, E, k, topk_ids, topk_weights, w13_codes,
+                           w13_scales, w13_outer, w2_codes, w2_scales, w2_outer, static_cast<float*>(out), h, z, s);
   return bsqh::launch_status();
 }

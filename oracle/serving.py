@@ -100,7 +100,7 @@ def moe_few(x, ids, weights, w13, w2, out_terms_eps, out_eps):
 def quantize_int8(x):
     """(codes int8 [R, C], scales float32 [R]), every step in float32."""
     x = np.asarray(x, dtype=np.float32)
-    s = (np.abs(x).max(1) / np.float32(127)).astype(np.float32)
+    s = (np.abs(x).max(1) * (np.float32(1) / np.float32(127))).astype(np.float32)
     s = np.where(s >= np.float32(2.0 ** -126), s, np.float32(1)).astype(np.float32)
     q = np.rint(x * (np.float32(1) / s).astype(np.float32)[:, None])
     return np.clip(q, -127, 127).astype(np.int8), s
