@@ -254,7 +254,6 @@ struct Route {
 struct Product {
   const void* in;         // activations: row of pair p is (GLU ? p / k : p)
   const int32_t* ids;
-  const float* weight;    // of a pair (not GLU)
   int pairs, k, E, K;
   int width;              // outputs of a pair
   const uint8_t* codes;
@@ -265,9 +264,10 @@ struct Product {
 
 // The end of a tile: the waves' partial sums of 16 x 16 outputs meet in LDS and
 // are stored. GLU (W13): the tiles are gate rows, then their up rows, and the
-// result is silu(gate) * up. Otherwise (W2) RT * 16 rows, times the pair's
-// weight. One barrier, which leaves loads in flight; the caller alternates
-// between two buffers.
+// result is silu(gate) * up. Otherwise (W2) RT * 16 rows. One barrier, which
+// leaves loads in flight, and no load of its own, whose wait would be one for
+// all that are in flight (the pairs' weights are left to the last sum); the
+// caller alternates between two buffers.
 template <bool GLU, int RT>
 __device__ __forceinline__ void finish(const Product& a, float (&part)[kWaves][RT][256], const f32x4 (&acc)[RT],
                                        float down, int tile, int mt0, int np, float so, const uint16_t* list) {
@@ -294,9 +294,8 @@ __device__ __forceinline__ void finish(const Product& a, float (&part)[kWaves][R
       v = g / (1.0f + expf(-g)) * (up * so);
     }
     if (q < np && f < a.width) {
-      const int p = list[q];
-      if constexpr (!GLU) v *= a.weight[p] * so;
-      a.out[(int64_t)p * a.width + f] = v;
+      if constexpr (!GLU) v *= so;
+      a.out[(int64_t)list[q] * a.width + f] = v;
     }
   }
 }
@@ -612,10 +611,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_stream(Product a) {
   }
 }
 
-// y[t, n..n+3] = sum over the token's valid pairs, in slot order.
+// y[t, n..n+3] = weighted sum over the token's valid pairs, in slot order.
 template <typename T>
 __global__ __launch_bounds__(256) void k_moe_sum(const float* __restrict__ z, const int32_t* __restrict__ ids,
-                                                 int tokens, int k, int E, int H, T* __restrict__ y) {
+                                                 const float* __restrict__ weights, int tokens, int k, int E, int H, T* __restrict__ y) {
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int per = H / 4;
   if (id >= (int64_t)tokens * per) return;
@@ -623,7 +622,7 @@ __global__ __launch_bounds__(256) void k_moe_sum(const float* __restrict__ z, co
   f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int j = 0; j < k; ++j) {
     const int e = ids[t * k + j];
-    if (e >= 0 && e < E) s += *reinterpret_cast<const f32x4*>(z + ((int64_t)t * k + j) * H + n);
+    if (e >= 0 && e < E) s += weights[t * k + j] * *reinterpret_cast<const f32x4*>(z + ((int64_t)t * k + j) * H + n);
   }
   if constexpr (sizeof(T) == 4) {
     *reinterpret_cast<f32x4*>(y + (int64_t)t * H + n) = s;
@@ -656,10 +655,10 @@ void launch_layer(const T* x, int64_t tokens, int64_t H, int64_t F, int64_t E, i
                   const uint8_t* w2c, const uint8_t* w2s, const float* w2o, T* out, float* h, float* z,
                   hipStream_t s) {
   const int pairs = (int)(tokens * k);
-  launch_stream<T, NT, true>({x, ids, weights, pairs, (int)k, (int)E, (int)H, (int)F, w13c, w13s, w13o, h}, s);
-  launch_stream<float, 2, false>({h, ids, weights, pairs, (int)k, (int)E, (int)F, (int)H, w2c, w2s, w2o, z}, s);
+  launch_stream<T, NT, true>({x, ids, pairs, (int)k, (int)E, (int)H, (int)F, w13c, w13s, w13o, h}, s);
+  launch_stream<float, 2, false>({h, ids, pairs, (int)k, (int)E, (int)F, (int)H, w2c, w2s, w2o, z}, s);
   hipLaunchKernelGGL((k_moe_sum<T>), dim3((unsigned)((tokens * (H / 4) + 255) / 256)), dim3(256), 0, s,
-                     static_cast<const float*>(z), ids, (int)tokens, (int)k, (int)E, (int)H, out);
+                     static_cast<const float*>(z), ids, weights, (int)tokens, (int)k, (int)E, (int)H, out);
 }
 
 bool shape_ok(int64_t tokens, int64_t hidden, int64_t ffn, int64_t E, int64_t k) {
