@@ -209,85 +209,210 @@ __global__ __launch_bounds__(kFThreads) void k_gemm_int8_few(const int8_t* __res
 }
 
 // ---------------------------------------------------------------- many rows
-// 128 x 128 outputs per workgroup of four waves (64 x 64 each), K in steps of
-// 128 staged in LDS. 16-byte pieces of a row are placed at (piece ^ row % 8),
-// so that fragment reads (32 rows at one piece) meet no bank twice.
-constexpr int kTile = 128;
-constexpr int kStep = 128;
+// Tiles of 64 WM rows of activations by 64 WN rows of weights for a workgroup
+// of four waves (32 WM x 32 WN each, v_mfma_i32_32x32x32_i8, one wave a SIMD
+// with all accumulators in registers). K advances in steps of 64 bytes through
+// a ring of four stages in LDS, filled by loads that go straight there; the
+// steps in flight are counted here, so a barrier a step is all that is waited
+// for. A wave reads the next fragments while it multiplies: the barrier stands
+// before the second half of a step, whose fragments are in registers by then,
+// so that its matrix instructions cover the reads of the next step.
+//
+// A stage holds rows of 64 bytes; the 16-byte pieces of row r lie in the order
+// piece ^ (r / 4 % 4), so that 16 rows at one piece meet 16 different banks.
+// Fragments past K (in a last step that is not whole) are set to zero on the
+// weights' side; rows past M or N repeat the last one and are not stored.
+//
+// Weights are the matrix instruction's first operand: a lane then holds four
+// neighbouring outputs of one row, which go through LDS (free by then) and
+// leave as whole 16-byte pieces of rows.
+constexpr int kStages = 4;
+constexpr int kStep = 64;
 
-template <typename T>
-__global__ __launch_bounds__(256) void k_gemm_int8(const int8_t* __restrict__ a, const float* __restrict__ sa,
-                                                  const int8_t* __restrict__ b, const float* __restrict__ sb,
-                                                  const float* __restrict__ bias, int64_t M, int N, int K,
-                                                  T* __restrict__ out) {
-  __shared__ i32x4 la[kTile * 8], lb[kTile * 8];
-  const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
-  const int ntn = (N + kTile - 1) / kTile;
-  const int64_t m0 = (int64_t)(blockIdx.x / ntn) * kTile;
-  const int n0 = (int)(blockIdx.x % ntn) * kTile;
-  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
-  const int piece = t & 7, r0 = t >> 3;  // this thread's piece of rows r0, r0 + 32, ...
-  const int8_t* ap[4];
-  const int8_t* bp[4];
+typedef uint32_t rsrc_words __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ rsrc_words descriptor(const void* p, uint32_t bytes) {
+  const uint64_t at = (uint64_t)p;
+  return (rsrc_words){(uint32_t)uniform((int)(uint32_t)at), (uint32_t)uniform((int)(uint32_t)(at >> 32)) & 0xFFFFu,
+                      (uint32_t)uniform((int)bytes), 0x00020000u};
+}
+// 64 lanes of 16 bytes: lane l's at lds + 16 l. There is no register to be
+// overwritten in flight; the address register is read at issue.
+__device__ __forceinline__ void load_to_lds(rsrc_words rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff), "s"(rsrc),
+               "s"(soff)
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_loads() {  // all but the N youngest
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return (uint32_t)uniform((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
+}
+
+template <typename T, int WM, int WN>
+__global__ __launch_bounds__(256, 1) void k_gemm_int8(const int8_t* __restrict__ a, const float* __restrict__ sa,
+                                                     const int8_t* __restrict__ b, const float* __restrict__ sb,
+                                                     const float* __restrict__ bias, int64_t M, int N, int K,
+                                                     T* __restrict__ out) {
+  constexpr int TM = 64 * WM, TN = 64 * WN;
+  constexpr int STAGE = (TM + TN) * kStep;      // bytes: rows of activations, then of weights
+  constexpr int LA = TM / 64, LB = TN / 64;     // loads of a wave for a step: 16 rows each
+  constexpr int LOADS = LA + LB;
+  // the output of a wave, 32 WM rows of COLS columns at a time
+  constexpr int COLS = sizeof(T) == 2 ? 32 * WN : 16 * WN;
+  constexpr int PITCH = COLS * (int)sizeof(T) + 16;
+  constexpr int OUT = 32 * WM * PITCH;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kStages * STAGE > 4 * OUT ? kStages * STAGE : 4 * OUT];
+  const int t = threadIdx.x, wave = uniform(t >> 6), lane = t & 63;
+  // Workgroups go round the 8 XCDs; each XCD takes a contiguous part of the
+  // tiles, columns first, so that the workgroups it runs at once share rows of
+  // both operands in its L2.
+  const int ntn = (N + TN - 1) / TN;
+  const int64_t ntiles = gridDim.x;
+  const int64_t per = ntiles / 8, extra = ntiles % 8;
+  const int xcd = blockIdx.x % 8;
+  const int64_t tile = xcd * per + (xcd < extra ? xcd : extra) + blockIdx.x / 8;
+  const int64_t m0 = tile / ntn * TM;
+  const int n0 = (int)(tile % ntn) * TN;
+  const int rows_a = M - m0 < TM ? (int)(M - m0) : TM, rows_b = N - n0 < TN ? N - n0 : TN;
+  const rsrc_words ra = descriptor(a + m0 * K, (uint32_t)rows_a * K);
+  const rsrc_words rb = descriptor(b + (int64_t)n0 * K, (uint32_t)rows_b * K);
+  uint32_t va[LA], vb[LB];
+  {
+    const int r = lane >> 2, piece = (lane & 3) ^ (r >> 2 & 3);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t m = m0 + r0 + 32 * i;
-    const int n = n0 + r0 + 32 * i;
-    ap[i] = a + (m < M ? m : M - 1) * K + piece * 16;
-    bp[i] = b + (int64_t)(n < N ? n : N - 1) * K + piece * 16;
-  }
-  i32x16 acc[2][2] = {};
-  i32x4 ra[4], rb[4];
-  auto fetch = [&](int k) {
-    const bool in = k + piece * 16 < K;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      ra[i] = rb[i] = (i32x4){0, 0, 0, 0};
-      if (in) {
-        ra[i] = *reinterpret_cast<const i32x4*>(ap[i] + k);
-        rb[i] = *reinterpret_cast<const i32x4*>(bp[i] + k);
-      }
+    for (int i = 0; i < LA; ++i) {
+      const int row = (wave * LA + i) * 16 + r;
+      va[i] = (uint32_t)(row < rows_a ? row : rows_a - 1) * K + piece * 16;
     }
+#pragma unroll
+    for (int i = 0; i < LB; ++i) {
+      const int row = (wave * LB + i) * 16 + r;
+      vb[i] = (uint32_t)(row < rows_b ? row : rows_b - 1) * K + piece * 16;
+    }
+  }
+  const uint32_t base = lds_offset(lds);
+  const int steps = (K + kStep - 1) / kStep;
+  // steps past the end are issued all the same (the waits count them), to empty buffers
+  auto fetch = [&](int step, int stage) {
+    const uint32_t at = base + stage * STAGE;
+    rsrc_words da = ra, db = rb;
+    if (step >= steps) da[2] = db[2] = 0u;
+#pragma unroll
+    for (int i = 0; i < LA; ++i) load_to_lds(da, va[i] + step * kStep, 0, at + (wave * LA + i) * 1024);
+#pragma unroll
+    for (int i = 0; i < LB; ++i) load_to_lds(db, vb[i] + step * kStep, 0, at + TM * kStep + (wave * LB + i) * 1024);
   };
-  fetch(0);
-  for (int k = 0; k < K; k += kStep) {
-    __syncthreads();
+  const int wm = wave >> 1, wn = wave & 1;
+  const int mine = (lane & 31) * kStep + ((lane >> 5) ^ (lane >> 2 & 3)) * 16;  // row lane % 32, piece lane / 32
+  i32x4 fa[2][WM], fb[2][WN];
+  auto read = [&](int stage, int q) {
+    const uint8_t* pa = lds + stage * STAGE + wm * (32 * WM) * kStep + (mine ^ (q * 32));
+    const uint8_t* pb = lds + stage * STAGE + TM * kStep + wn * (32 * WN) * kStep + (mine ^ (q * 32));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = r0 + 32 * i;
-      la[r * 8 + (piece ^ (r & 7))] = ra[i];
-      lb[r * 8 + (piece ^ (r & 7))] = rb[i];
+    for (int i = 0; i < WN; ++i) fb[q][i] = *reinterpret_cast<const i32x4*>(pb + i * 32 * kStep);
+#pragma unroll
+    for (int i = 0; i < WM; ++i) fa[q][i] = *reinterpret_cast<const i32x4*>(pa + i * 32 * kStep);
+  };
+  i32x16 acc[WN][WM] = {};
+  auto products = [&](int step, int q) {
+    if (step * kStep + kStep > K) {  // a last step that is not whole
+      const bool in = step * kStep + (2 * q + (lane >> 5)) * 16 < K;
+#pragma unroll
+      for (int i = 0; i < WN; ++i) fb[q][i] = in ? fb[q][i] : (i32x4){0, 0, 0, 0};
     }
-    __syncthreads();
-    if (k + kStep < K) fetch(k + kStep);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      i32x4 fa[2], fb[2];
+    for (int i = 0; i < WN; ++i)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int ar = wm + 32 * i + (lane & 31), br = wn + 32 * i + (lane & 31);
-        const int pc = 2 * q + (lane >> 5);
-        fa[i] = la[ar * 8 + (pc ^ (ar & 7))];
-        fb[i] = lb[br * 8 + (pc ^ (br & 7))];
-      }
+      for (int j = 0; j < WM; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[q][i], fa[q][j], acc[i][j], 0, 0, 0);
+  };
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[i], fb[j], acc[i][j], 0, 0, 0);
-    }
+  for (int s = 0; s < kStages; ++s) fetch(s, s);
+  wait_loads<(kStages - 1) * LOADS>();
+  lds_barrier();
+  read(0, 0);
+  int stage = 0;
+#pragma unroll 1
+  for (int step = 0; step < steps; ++step) {
+    read(stage, 1);
+    products(step, 0);
+    __builtin_amdgcn_sched_barrier(0);  // they run while the barrier is waited for
+    const int next = stage == kStages - 1 ? 0 : stage + 1;
+    wait_loads<(kStages - 2) * LOADS>();  // the next stage has come
+    lds_barrier();                        // for every wave, and this one is read
+    fetch(step + kStages, stage);
+    read(next, 0);
+    products(step, 1);
+    stage = next;
   }
+  wait_loads<0>();
+  lds_barrier();
+
+  // outputs: lane holds row lane % 32 of the 32 x 32 tile (i, j) and columns 8 (r / 4) + 4 (lane / 32) + r % 4
+  uint8_t* mylds = lds + wave * OUT;
+  const bool whole = (N * (int)sizeof(T)) % 16 == 0;
+  const int64_t mw = m0 + wm * 32 * WM;
+  float ma[WM];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int n = n0 + wn + 32 * j + (lane & 31);
-    if (n >= N) continue;
-    const float fb = sb[n], add = bias ? bias[n] : 0.0f;
+  for (int j = 0; j < WM; ++j) {
+    const int64_t m = mw + 32 * j + (lane & 31);
+    ma[j] = sa[m < M ? m : M - 1];
+  }
+  constexpr int HALVES = 32 * WN / COLS;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+  for (int h = 0; h < HALVES; ++h) {
+    const int nw = n0 + wn * 32 * WN + h * COLS;
 #pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        const int64_t m = m0 + wm + 32 * i + 8 * (q >> 2) + 4 * (lane >> 5) + (q & 3);
-        if (m < M) store1(out + m * N + n, (float)acc[i][j][q] * sa[m] * fb + add);
+    for (int i = 0; i < COLS / 32; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int c = 32 * i + 8 * r + 4 * (lane >> 5);
+        f32x4 s, add;
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const int n = nw + c + z < N ? nw + c + z : N - 1;
+          s[z] = sb[n];
+          add[z] = bias ? bias[n] : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < WM; ++j) {
+          const i32x16& v = acc[h * (COLS / 32) + i][j];
+          f32x4 y;
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            y[z] = (float)v[4 * r + z] * ma[j] * s[z];
+            if (bias) y[z] += add[z];
+          }
+          uint8_t* at = mylds + (32 * j + (lane & 31)) * PITCH + c * (int)sizeof(T);
+          if constexpr (sizeof(T) == 2) *reinterpret_cast<u32x2*>(at) = (u32x2){pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+          else *reinterpret_cast<f32x4*>(at) = y;
+        }
       }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the wave reads what its own lanes wrote
+    if (whole) {
+      constexpr int PR = COLS * (int)sizeof(T) / 16;  // pieces of a row
+#pragma unroll 4
+      for (int o = lane; o < 32 * WM * PR; o += 64) {
+        const int row = o / PR, pc = o % PR;
+        const int n = nw + pc * (16 / (int)sizeof(T));
+        if (mw + row < M && n < N)
+          *reinterpret_cast<u32x4*>(out + (mw + row) * N + n) = *reinterpret_cast<const u32x4*>(mylds + row * PITCH + pc * 16);
+      }
+    } else {
+#pragma unroll 4
+      for (int o = lane; o < 32 * WM * COLS; o += 64) {
+        const int row = o / COLS, n = nw + o % COLS;
+        if (mw + row < M && n < N) out[(mw + row) * N + n] = *reinterpret_cast<const T*>(mylds + row * PITCH + o % COLS * (int)sizeof(T));
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
 }
 
@@ -305,8 +430,16 @@ void launch_gemm(const int8_t* a, const float* sa, const int8_t* b, const float*
 #undef BSQ_F
     return;
   }
-  const int64_t tiles = ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
-  hipLaunchKernelGGL((k_gemm_int8<T>), dim3((unsigned)tiles), dim3(256), 0, s, a, sa, b, sb, bias, M, (int)N, (int)K,
+  // 256 x 256 tiles move half as many bytes through LDS for each product as
+  // 128 x 128 ones; the small ones serve shapes whose large tiles leave CUs idle.
+  const int64_t big = ((M + 255) / 256) * ((N + 255) / 256);
+  if (big >= bsqh::device_cus()) {
+    hipLaunchKernelGGL((k_gemm_int8<T, 4, 4>), dim3((unsigned)big), dim3(256), 0, s, a, sa, b, sb, bias, M, (int)N, (int)K,
+                       out);
+    return;
+  }
+  const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
+  hipLaunchKernelGGL((k_gemm_int8<T, 2, 2>), dim3((unsigned)tiles), dim3(256), 0, s, a, sa, b, sb, bias, M, (int)N, (int)K,
                      out);
 }
 
@@ -315,7 +448,7 @@ int check_gemm(int64_t M, int64_t N, int64_t K, int out_dtype) {
   // 128 * 128 * K stays below 2^31; fewer than 2^31 tiles
   BSQ_REQUIRE(M >= 0 && M < (int64_t)1 << 31 && N >= 0 && N < (int64_t)1 << 31 && K >= 16 && K % 16 == 0 && K < 131072,
               BSQ_E_SHAPE);
-  BSQ_REQUIRE(((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile) < (int64_t)1 << 31, BSQ_E_SHAPE);
+  BSQ_REQUIRE(((M + 127) / 128) * ((N + 127) / 128) < (int64_t)1 << 31, BSQ_E_SHAPE);
   return BSQ_OK;
 }
 
