@@ -144,67 +144,171 @@ int check_quant(const void* x, int dtype, int64_t rows, int64_t cols, const void
   return BSQ_OK;
 }
 
+// ---------------------------------------------------------------- loads to LDS
+// Loads that go straight to LDS, as asm because the waits are counted here: the
+// compiler would have to take every LDS read for one that may meet the newest
+// load.
+typedef uint32_t rsrc_words __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ rsrc_words descriptor(const void* p, uint32_t bytes) {
+  const uint64_t at = (uint64_t)p;
+  return (rsrc_words){(uint32_t)uniform((int)(uint32_t)at), (uint32_t)uniform((int)(uint32_t)(at >> 32)) & 0xFFFFu,
+                      (uint32_t)uniform((int)bytes), 0x00020000u};
+}
+// 64 lanes of 16 bytes: lane l's at lds + 16 l. There is no register to be
+// overwritten in flight; the address register is read at issue.
+__device__ __forceinline__ void load_to_lds(rsrc_words rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff), "s"(rsrc),
+               "s"(soff)
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_loads() {  // all but the N youngest
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return (uint32_t)uniform((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p);
+}
+
 // ---------------------------------------------------------------- epilogue
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
 
 // ---------------------------------------------------------------- few rows
-// Up to 64 rows of activations: bound by reading the weights once. A workgroup
-// owns 16 weight rows for all M, its eight waves share K, and the exact
-// integer partial sums meet in LDS.
+// Up to 64 rows of activations: bound by reading the weights once, and by how
+// soon. A workgroup owns 16 weight rows for all M; its eight waves share K, each
+// with a ring of R steps of 64 bytes in LDS of its own (no barriers), filled
+// by loads that go straight there: four lanes side by side read 64 bytes of a
+// row, where a load in the matrix instruction's own layout (a lane, a row)
+// costs the address unit four times as long. Pieces of row r lie in the order
+// piece ^ (r / 4 % 4) as in the large tiles. The exact integer partial sums meet
+// in LDS.
+//
+// FUSED: the activations come unquantized, few enough to lie in LDS (kFuseBytes);
+// every workgroup quantizes them itself, while the first weights are on their
+// way, and one launch is the whole layer. The codes are those of
+// k_quant_int8: the same steps in the same order.
 constexpr int kFThreads = 512;
 constexpr int kFWaves = kFThreads / 64;
+constexpr int kFuseBytes = 32768;
+constexpr int kFuseCodes = 16384;
 
-template <typename T, int MT>
-__global__ __launch_bounds__(kFThreads) void k_gemm_int8_few(const int8_t* __restrict__ a, const float* __restrict__ sa,
+template <typename X, typename T, int MT, bool FUSED>
+__global__ __launch_bounds__(kFThreads) void k_gemm_int8_few(const X* __restrict__ a, const float* __restrict__ sa,
                                                             const int8_t* __restrict__ b, const float* __restrict__ sb,
                                                             const float* __restrict__ bias, int M, int N, int K,
                                                             T* __restrict__ out) {
+  constexpr int LOADS = FUSED ? 1 : 1 + MT;               // of a step: 16 rows of 64 bytes each
+  constexpr int R = FUSED ? 8 : MT == 1 ? 6 : MT == 2 ? 5 : 3;
+  constexpr int XLOADS = FUSED ? kFuseBytes / 1024 / kFWaves : 0;
+  __shared__ __attribute__((aligned(16))) uint8_t ring[kFWaves][R][LOADS * 1024];
   __shared__ i32x4 part[kFWaves][MT][64];
-  const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
-  const int col = lane & 15, grp = lane >> 4;
+  __shared__ __attribute__((aligned(16))) uint8_t raw[FUSED ? kFuseBytes : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t code[FUSED ? kFuseCodes + 16 * 16 + 64 : 16];
+  __shared__ uint32_t rmax[16];
+  const int t = threadIdx.x, wave = uniform(t >> 6), lane = t & 63;
   const int n0 = (int)blockIdx.x * 16;
-  const int8_t* brow = b + (int64_t)(n0 + col < N ? n0 + col : N - 1) * K;
-  const int8_t* arow[MT];
-  bool have[MT];
+  const int rows_b = N - n0 < 16 ? N - n0 : 16;
+  const int steps = (K + 63) / 64;
+  const int st0 = steps * wave / kFWaves, st1 = steps * (wave + 1) / kFWaves;
+  // what the epilogue will need, ahead of the stream
+  constexpr int PER = (MT * 256 + kFThreads - 1) / kFThreads;
+  float ea[PER], eb[PER], ec[PER];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    have[m] = 16 * m + col < M;
-    arow[m] = a + (int64_t)(have[m] ? 16 * m + col : 0) * K;
+  for (int i = 0; i < PER; ++i) {
+    const int j = t + i * kFThreads, row = j / 256 * 16 + (j >> 2 & 15), n = n0 + (j % 256 >> 6) * 4 + (j & 3);
+    ea[i] = !FUSED ? sa[row < M ? row : M - 1] : 0.0f;
+    eb[i] = sb[n < N ? n : N - 1];
+    ec[i] = bias ? bias[n < N ? n : N - 1] : 0.0f;
   }
-  i32x4 acc[MT] = {};
-  for (int k0 = wave * 64; k0 < K; k0 += kFWaves * 64) {
-    const int k = k0 + grp * 16;
-    const bool in = k < K;  // K % 16 == 0: a lane's 16 values are whole or past the end
-    i32x4 w = {0, 0, 0, 0};
-    if (in) w = *reinterpret_cast<const i32x4*>(brow + k);
+  const int r = lane >> 2, piece = (lane & 3) ^ (r >> 2 & 3);
+  const rsrc_words db = descriptor(b + (int64_t)n0 * K, (uint32_t)rows_b * K);
+  const rsrc_words da = descriptor(a, FUSED ? (uint32_t)(M * K) * (uint32_t)sizeof(X) : (uint32_t)M * K);
+  const uint32_t vb = (uint32_t)(r < rows_b ? r : rows_b - 1) * K + piece * 16;
+  uint32_t va[MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      i32x4 v = {0, 0, 0, 0};
-      if (in && have[m]) v = *reinterpret_cast<const i32x4*>(arow[m] + k);
-      acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, v, acc[m], 0, 0, 0);
+  for (int m = 0; m < MT; ++m) va[m] = (uint32_t)(16 * m + r < M ? 16 * m + r : M - 1) * K + piece * 16;
+  const uint32_t base = lds_offset(&ring[wave][0][0]);
+  constexpr uint32_t kPastEnd = 0x80000000u;
+  auto fetch = [&](int st, int place) {  // past the last step: issued all the same (the waits count them), past the end
+    const uint32_t k = st < st1 ? (uint32_t)st * 64 : kPastEnd;
+    load_to_lds(db, vb + k, 0, base + place * (LOADS * 1024));
+    if constexpr (!FUSED) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) load_to_lds(da, va[m] + k, 0, base + place * (LOADS * 1024) + (1 + m) * 1024);
     }
+  };
+  if constexpr (FUSED) {
+    const uint32_t at = lds_offset(raw);
+#pragma unroll
+    for (int i = 0; i < XLOADS; ++i) {
+      const int c = i * kFWaves + wave;
+      load_to_lds(da, c * 1024 + lane * 16, 0, at + c * 1024);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) fetch(st0 + i, i);
+  const int pitch = K + 16;
+  if constexpr (FUSED) {
+    if (t < 16) rmax[t] = 0u;
+    wait_loads<R * LOADS>();
+    lds_barrier();
+    const int per = K / 16, units = M * per;
+    for (int u = t; u < units; u += kFThreads) {
+      float v[16], mx = 0.0f;
+      load16(reinterpret_cast<const X*>(raw) + u * 16, v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, fabsf(v[i]));
+      atomicMax(&rmax[u / per], __float_as_uint(mx));
+    }
+    lds_barrier();
+    for (int u = t; u < units; u += kFThreads) {
+      const int row = u / per;
+      const float inv = 1.0f / row_scale(__uint_as_float(rmax[row]));
+      float v[16];
+      load16(reinterpret_cast<const X*>(raw) + u * 16, v);
+      *reinterpret_cast<u32x4*>(code + row * pitch + (u - row * per) * 16) =
+          (u32x4){codes4(&v[0], inv), codes4(&v[4], inv), codes4(&v[8], inv), codes4(&v[12], inv)};
+    }
+    lds_barrier();
+  }
+  const int col = lane & 15, grp = lane >> 4;
+  const int mine = col * 64 + (grp ^ (col >> 2 & 3)) * 16;
+  const uint8_t* crow = code + (FUSED && col < M ? col : 0) * pitch + grp * 16;  // lanes past M repeat row 0
+  i32x4 acc[MT] = {};
+  int place = 0;
+#pragma unroll 1
+  for (int st = st0; st < st1; ++st) {
+    wait_loads<(R - 1) * LOADS>();
+    const uint8_t* p = &ring[wave][place][0] + mine;
+    i32x4 w = *reinterpret_cast<const i32x4*>(p), v[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+      v[m] = *reinterpret_cast<const i32x4*>(FUSED ? crow + st * 64 : p + (1 + m) * 1024);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the place may be filled again
+    fetch(st + R, place);
+    if (st * 64 + 64 > K && st * 64 + grp * 16 >= K) w = (i32x4){0, 0, 0, 0};  // past the end of K
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, v[m], acc[m], 0, 0, 0);
+    place = place == R - 1 ? 0 : place + 1;
   }
 #pragma unroll
   for (int m = 0; m < MT; ++m) part[wave][m][lane] = acc[m];
-  __syncthreads();
-  for (int j = t; j < MT * 64; j += kFThreads) {
-    const int m = j >> 6, l = j & 63;
-    i32x4 s = part[0][m][l];
+  lds_barrier();
 #pragma unroll
-    for (int w = 1; w < kFWaves; ++w) s += part[w][m][l];
-    const int row = 16 * m + (l & 15);
-    if (row >= M) continue;
-    const float fa = sa[row];
+  for (int i = 0; i < PER; ++i) {
+    const int j = t + i * kFThreads;
+    if (j >= MT * 256) break;
+    int s = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = n0 + 4 * (l >> 4) + i;
-      if (n < N) {
-        float y = (float)s[i] * fa * sb[n];
-        if (bias) y += bias[n];
-        store1(out + (int64_t)row * N + n, y);
-      }
-    }
+    for (int w = 0; w < kFWaves; ++w) s += reinterpret_cast<const int*>(&part[w][0][0])[j];
+    const int row = j / 256 * 16 + (j >> 2 & 15), n = n0 + (j % 256 >> 6) * 4 + (j & 3);
+    if (row >= M || n >= N) continue;
+    if constexpr (FUSED) ea[i] = row_scale(__uint_as_float(rmax[row]));
+    float y = (float)s * ea[i] * eb[i];
+    if (bias) y += ec[i];
+    store1(out + (int64_t)row * N + n, y);
   }
 }
 
@@ -228,29 +332,6 @@ __global__ __launch_bounds__(kFThreads) void k_gemm_int8_few(const int8_t* __res
 // leave as whole 16-byte pieces of rows.
 constexpr int kStages = 4;
 constexpr int kStep = 64;
-
-typedef uint32_t rsrc_words __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ rsrc_words descriptor(const void* p, uint32_t bytes) {
-  const uint64_t at = (uint64_t)p;
-  return (rsrc_words){(uint32_t)uniform((int)(uint32_t)at), (uint32_t)uniform((int)(uint32_t)(at >> 32)) & 0xFFFFu,
-                      (uint32_t)uniform((int)bytes), 0x00020000u};
-}
-// 64 lanes of 16 bytes: lane l's at lds + 16 l. There is no register to be
-// overwritten in flight; the address register is read at issue.
-__device__ __forceinline__ void load_to_lds(rsrc_words rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff), "s"(rsrc),
-               "s"(soff)
-               : "memory");
-}
-template <int N>
-__device__ __forceinline__ void wait_loads() {  // all but the N youngest
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-__device__ __forceinline__ uint32_t lds_offset(const void* p) {
-  return (uint32_t)uniform((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p);
-}
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
@@ -300,56 +381,76 @@ __global__ __launch_bounds__(256, 1) void k_gemm_int8(const int8_t* __restrict__
   }
   const uint32_t base = lds_offset(lds);
   const int steps = (K + kStep - 1) / kStep;
-  // steps past the end are issued all the same (the waits count them), to empty buffers
-  auto fetch = [&](int step, int stage) {
-    const uint32_t at = base + stage * STAGE;
-    rsrc_words da = ra, db = rb;
-    if (step >= steps) da[2] = db[2] = 0u;
-#pragma unroll
-    for (int i = 0; i < LA; ++i) load_to_lds(da, va[i] + step * kStep, 0, at + (wave * LA + i) * 1024);
-#pragma unroll
-    for (int i = 0; i < LB; ++i) load_to_lds(db, vb[i] + step * kStep, 0, at + TM * kStep + (wave * LB + i) * 1024);
+  // Steps past the end are issued all the same (the waits count them), to empty
+  // buffers. A stage's loads of activations and of weights go out in different
+  // halves of a step, one before each row of matrix instructions: issued
+  // together they fill the address unit's queue and the wave stands behind it.
+  auto fetch_a = [&](int step, int stage, int i) {
+    rsrc_words d = ra;
+    if (step >= steps) d[2] = 0u;
+    load_to_lds(d, va[i] + step * kStep, 0, base + stage * STAGE + (wave * LA + i) * 1024);
+  };
+  auto fetch_b = [&](int step, int stage, int i) {
+    rsrc_words d = rb;
+    if (step >= steps) d[2] = 0u;
+    load_to_lds(d, vb[i] + step * kStep, 0, base + stage * STAGE + TM * kStep + (wave * LB + i) * 1024);
   };
   const int wm = wave >> 1, wn = wave & 1;
   const int mine = (lane & 31) * kStep + ((lane >> 5) ^ (lane >> 2 & 3)) * 16;  // row lane % 32, piece lane / 32
   i32x4 fa[2][WM], fb[2][WN];
-  auto read = [&](int stage, int q) {
-    const uint8_t* pa = lds + stage * STAGE + wm * (32 * WM) * kStep + (mine ^ (q * 32));
-    const uint8_t* pb = lds + stage * STAGE + TM * kStep + wn * (32 * WN) * kStep + (mine ^ (q * 32));
-#pragma unroll
-    for (int i = 0; i < WN; ++i) fb[q][i] = *reinterpret_cast<const i32x4*>(pb + i * 32 * kStep);
-#pragma unroll
-    for (int i = 0; i < WM; ++i) fa[q][i] = *reinterpret_cast<const i32x4*>(pa + i * 32 * kStep);
+  auto read = [&](int stage, int q, int i) {
+    const uint8_t* p = lds + stage * STAGE + (mine ^ (q * 32)) + i * 32 * kStep;
+    if (i < WN) fb[q][i < WN ? i : 0] = *reinterpret_cast<const i32x4*>(p + (TM + wn * 32 * WN) * kStep);
+    if (i < WM) fa[q][i < WM ? i : 0] = *reinterpret_cast<const i32x4*>(p + wm * (32 * WM) * kStep);
   };
   i32x16 acc[WN][WM] = {};
-  auto products = [&](int step, int q) {
+  auto mask = [&](int step, int q) {
     if (step * kStep + kStep > K) {  // a last step that is not whole
       const bool in = step * kStep + (2 * q + (lane >> 5)) * 16 < K;
 #pragma unroll
       for (int i = 0; i < WN; ++i) fb[q][i] = in ? fb[q][i] : (i32x4){0, 0, 0, 0};
     }
-#pragma unroll
-    for (int i = 0; i < WN; ++i)
-#pragma unroll
-      for (int j = 0; j < WM; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[q][i], fa[q][j], acc[i][j], 0, 0, 0);
   };
+  auto products = [&](int q, int i) {
 #pragma unroll
-  for (int s = 0; s < kStages; ++s) fetch(s, s);
-  wait_loads<(kStages - 1) * LOADS>();
+    for (int j = 0; j < WM; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[q][i], fa[q][j], acc[i][j], 0, 0, 0);
+  };
+  static_assert(WM == WN, "a row of matrix instructions for each load of a half");
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) {
+#pragma unroll
+    for (int i = 0; i < LA; ++i) fetch_a(s, s, i);
+    if (s < kStages - 1) {
+#pragma unroll
+      for (int i = 0; i < LB; ++i) fetch_b(s, s, i);
+    }
+  }
+  wait_loads<(kStages - 2) * LOADS + LA>();
   lds_barrier();
-  read(0, 0);
+#pragma unroll
+  for (int i = 0; i < WN; ++i) read(0, 0, i);
   int stage = 0;
 #pragma unroll 1
   for (int step = 0; step < steps; ++step) {
-    read(stage, 1);
-    products(step, 0);
-    __builtin_amdgcn_sched_barrier(0);  // they run while the barrier is waited for
-    const int next = stage == kStages - 1 ? 0 : stage + 1;
+    const int next = (stage + 1) & (kStages - 1), last = (stage + kStages - 1) & (kStages - 1);
+    mask(step, 0);
+#pragma unroll
+    for (int i = 0; i < WN; ++i) {
+      fetch_b(step + kStages - 1, last, i);
+      read(stage, 1, i);
+      products(0, i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     wait_loads<(kStages - 2) * LOADS>();  // the next stage has come
     lds_barrier();                        // for every wave, and this one is read
-    fetch(step + kStages, stage);
-    read(next, 0);
-    products(step, 1);
+    mask(step, 1);
+#pragma unroll
+    for (int i = 0; i < WN; ++i) {
+      fetch_a(step + kStages, stage, i);
+      read(next, 0, i);
+      products(1, i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     stage = next;
   }
   wait_loads<0>();
@@ -422,8 +523,8 @@ void launch_gemm(const int8_t* a, const float* sa, const int8_t* b, const float*
   if (M <= 64) {
     const dim3 grid((unsigned)((N + 15) / 16));
 #define BSQ_F(MT)                                                                                                     \
-  hipLaunchKernelGGL((k_gemm_int8_few<T, MT>), grid, dim3(kFThreads), 0, s, a, sa, b, sb, bias, (int)M, (int)N, (int)K, \
-                     out)
+  hipLaunchKernelGGL((k_gemm_int8_few<int8_t, T, MT, false>), grid, dim3(kFThreads), 0, s, a, sa, b, sb, bias, (int)M, \
+                     (int)N, (int)K, out)
     if (M <= 16) BSQ_F(1);
     else if (M <= 32) BSQ_F(2);
     else BSQ_F(4);
@@ -514,6 +615,21 @@ extern "C" int bsq_linear_int8(const void* x, int dtype, const int8_t* b_codes, 
                   (((uintptr_t)b_scales | (uintptr_t)bias) & 3) == 0,
               BSQ_E_ALIGN);
   BSQ_REQUIRE(ws_bytes >= bsq_linear_int8_workspace(M, K), BSQ_E_WORKSPACE);
+  // One launch where the workgroups can quantize the few activations themselves.
+  const int64_t fuse = (M * K <= kFuseCodes && M * K * (dtype == BSQ_F32 ? 4 : 2) <= kFuseBytes && M <= 16) ? 1 : 0;
+  if (fuse) {
+    const dim3 grid((unsigned)((N + 15) / 16));
+#define BSQ_FUSED(X, T)                                                                                          \
+  hipLaunchKernelGGL((k_gemm_int8_few<X, T, 1, true>), grid, dim3(kFThreads), 0, bsqh::as_stream(stream),        \
+                     static_cast<const X*>(x), static_cast<const float*>(nullptr), b_codes, b_scales, bias, (int)M, \
+                     (int)N, (int)K, static_cast<T*>(out))
+    if (dtype == BSQ_BF16 && out_dtype == BSQ_BF16) BSQ_FUSED(uint16_t, uint16_t);
+    else if (dtype == BSQ_BF16) BSQ_FUSED(uint16_t, float);
+    else if (out_dtype == BSQ_BF16) BSQ_FUSED(float, uint16_t);
+    else BSQ_FUSED(float, float);
+#undef BSQ_FUSED
+    return bsqh::launch_status();
+  }
   int8_t* codes = static_cast<int8_t*>(ws);
   float* scales = reinterpret_cast<float*>(codes + M * K);  // K % 16 == 0: aligned
   st = bsq_quantize_int8(x, dtype, M, K, codes, scales, stream);

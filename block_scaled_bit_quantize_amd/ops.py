@@ -23,8 +23,15 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# the current stream's handle without a Stream object: 0.2 us where current_stream() takes 2.8
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream():
-    return torch.cuda.current_stream().cuda_stream
+    if _raw_stream is None or _raw_device is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(_raw_device())
 
 
 def _dev(*ts):
