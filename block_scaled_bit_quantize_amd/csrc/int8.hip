@@ -42,6 +42,14 @@ __device__ __forceinline__ void load16(const uint16_t* p, float (&v)[16]) {
   }
 }
 
+// silu(g) * u by the hardware's exponential and reciprocal: within a few units
+// in the last place, |g| 2^-24 more from the exponent's rounding (expf and an
+// exact division made the kernel bound by the vector ALU).
+__device__ __forceinline__ float swiglu(float g, float u) {
+  const float e = __builtin_amdgcn_exp2f(g * -1.44269504088896340736f);
+  return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
+}
+
 // Four values -> four int8 codes in a word: rint(v * inv), clamped.
 __device__ __forceinline__ uint32_t codes4(const float* v, float inv) {
   uint32_t w = 0;
@@ -81,7 +89,7 @@ __global__ __launch_bounds__(kQThreads) void k_quant_int8(const T* __restrict__ 
         load16(x + row * 2 * C + j * 16, v[b]);
         load16(x + row * 2 * C + C + j * 16, u);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[b][i] = v[b][i] / (1.0f + expf(-v[b][i])) * u[i];
+        for (int i = 0; i < 16; ++i) v[b][i] = swiglu(v[b][i], u[i]);
       } else {
         load16(x + row * C + j * 16, v[b]);
       }
@@ -314,43 +322,50 @@ __global__ __launch_bounds__(kFThreads) void k_gemm_int8_few(const X* __restrict
 
 // ---------------------------------------------------------------- many rows
 // Tiles of 64 WM rows of activations by 64 WN rows of weights for a workgroup
-// of four waves (32 WM x 32 WN each, v_mfma_i32_32x32x32_i8, one wave a SIMD
-// with all accumulators in registers). K advances in steps of 64 bytes through
-// a ring of four stages in LDS, filled by loads that go straight there; the
-// steps in flight are counted here, so a barrier a step is all that is waited
-// for. A wave reads the next fragments while it multiplies: the barrier stands
-// before the second half of a step, whose fragments are in registers by then,
-// so that its matrix instructions cover the reads of the next step.
+// of four waves (32 WM x 32 WN each, v_mfma_i32_32x32x32_i8, all accumulators
+// in registers). K advances in steps of KS bytes through a ring of ST stages in
+// LDS, filled by loads that go straight there; the steps in flight are counted
+// here, so a barrier a step is all that is waited for. A wave reads the next
+// fragments while it multiplies: the barrier stands before the last
+// instructions along a step, whose fragments are in registers by then, so that
+// they cover the reads of the next step.
 //
-// A stage holds rows of 64 bytes; the 16-byte pieces of row r lie in the order
-// piece ^ (r / 4 % 4), so that 16 rows at one piece meet 16 different banks.
-// Fragments past K (in a last step that is not whole) are set to zero on the
+// 256 x 256 tiles are bound by the chip's power: the matrix instructions alone
+// reach 3.4 POP/s on random codes (4.8 on zeros), and with them 62% of the
+// cycles at a clock that sinks to 1.45 GHz the kernel runs at 1.9 to 2.2 POP/s
+// (65536 x 2048 x 7168: 0.88 to 1.0 ms, with the loads left out 0.79). Small
+// tiles are bound by the latency of their loads: 128 bytes a row and step
+// (L2 serves twice the bytes with whole lines), 96 KB of them in flight a CU.
+//
+// A stage's rows hold their 16-byte pieces in an order that depends on the row,
+// so that 16 rows at one piece meet 16 different banks. Fragments past K (in a last step that is not whole) are set to zero on the
 // weights' side; rows past M or N repeat the last one and are not stored.
 //
 // Weights are the matrix instruction's first operand: a lane then holds four
 // neighbouring outputs of one row, which go through LDS (free by then) and
 // leave as whole 16-byte pieces of rows.
-constexpr int kStages = 4;
-constexpr int kStep = 64;
-
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
 }
 
-template <typename T, int WM, int WN>
+// KS bytes of K a step (64 or 128), ST stages.
+template <typename T, int WM, int WN, int KS, int ST>
 __global__ __launch_bounds__(256, 1) void k_gemm_int8(const int8_t* __restrict__ a, const float* __restrict__ sa,
                                                      const int8_t* __restrict__ b, const float* __restrict__ sb,
                                                      const float* __restrict__ bias, int64_t M, int N, int K,
                                                      T* __restrict__ out) {
   constexpr int TM = 64 * WM, TN = 64 * WN;
-  constexpr int STAGE = (TM + TN) * kStep;      // bytes: rows of activations, then of weights
-  constexpr int LA = TM / 64, LB = TN / 64;     // loads of a wave for a step: 16 rows each
+  constexpr int STAGE = (TM + TN) * KS;         // bytes: rows of activations, then of weights
+  constexpr int PR = KS / 16, RL = 64 / PR;     // pieces of a row, rows of a load
+  constexpr int LA = TM / RL / 4, LB = TN / RL / 4;  // loads of a wave for a step
   constexpr int LOADS = LA + LB;
+  constexpr int Q = KS / 32;                    // matrix instructions along a step
+  constexpr int SLOTS = Q * WN;                 // rows of matrix instructions in a step
   // the output of a wave, 32 WM rows of COLS columns at a time
   constexpr int COLS = sizeof(T) == 2 ? 32 * WN : 16 * WN;
   constexpr int PITCH = COLS * (int)sizeof(T) + 16;
   constexpr int OUT = 32 * WM * PITCH;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kStages * STAGE > 4 * OUT ? kStages * STAGE : 4 * OUT];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[ST * STAGE > 4 * OUT ? ST * STAGE : 4 * OUT];
   const int t = threadIdx.x, wave = uniform(t >> 6), lane = t & 63;
   // Workgroups go round the 8 XCDs; each XCD takes a contiguous part of the
   // tiles, columns first, so that the workgroups it runs at once share rows of
@@ -365,91 +380,92 @@ __global__ __launch_bounds__(256, 1) void k_gemm_int8(const int8_t* __restrict__
   const int rows_a = M - m0 < TM ? (int)(M - m0) : TM, rows_b = N - n0 < TN ? N - n0 : TN;
   const rsrc_words ra = descriptor(a + m0 * K, (uint32_t)rows_a * K);
   const rsrc_words rb = descriptor(b + (int64_t)n0 * K, (uint32_t)rows_b * K);
+  // piece p of row r lies at p ^ swizzle(r), so that 16 rows at one piece meet 16 different banks
+  auto swizzle = [](int r) { return r / (16 / PR) & (PR - 1); };
   uint32_t va[LA], vb[LB];
   {
-    const int r = lane >> 2, piece = (lane & 3) ^ (r >> 2 & 3);
+    const int r = lane / PR;
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
-      const int row = (wave * LA + i) * 16 + r;
-      va[i] = (uint32_t)(row < rows_a ? row : rows_a - 1) * K + piece * 16;
+      const int row = (wave * LA + i) * RL + r;
+      va[i] = (uint32_t)(row < rows_a ? row : rows_a - 1) * K + ((lane % PR) ^ swizzle(row)) * 16;
     }
 #pragma unroll
     for (int i = 0; i < LB; ++i) {
-      const int row = (wave * LB + i) * 16 + r;
-      vb[i] = (uint32_t)(row < rows_b ? row : rows_b - 1) * K + piece * 16;
+      const int row = (wave * LB + i) * RL + r;
+      vb[i] = (uint32_t)(row < rows_b ? row : rows_b - 1) * K + ((lane % PR) ^ swizzle(row)) * 16;
     }
   }
   const uint32_t base = lds_offset(lds);
-  const int steps = (K + kStep - 1) / kStep;
+  const int steps = (K + KS - 1) / KS;
   // Steps past the end are issued all the same (the waits count them), to empty
-  // buffers. A stage's loads of activations and of weights go out in different
-  // halves of a step, one before each row of matrix instructions: issued
-  // together they fill the address unit's queue and the wave stands behind it.
-  auto fetch_a = [&](int step, int stage, int i) {
-    rsrc_words d = ra;
-    if (step >= steps) d[2] = 0u;
-    load_to_lds(d, va[i] + step * kStep, 0, base + stage * STAGE + (wave * LA + i) * 1024);
-  };
-  auto fetch_b = [&](int step, int stage, int i) {
-    rsrc_words d = rb;
-    if (step >= steps) d[2] = 0u;
-    load_to_lds(d, vb[i] + step * kStep, 0, base + stage * STAGE + TM * kStep + (wave * LB + i) * 1024);
+  // buffers. A stage's loads go out over a whole step, before the rows of matrix
+  // instructions: issued together they fill the address unit's queue and the
+  // wave stands behind it.
+  auto fetch = [&](int step, int stage, int i) {
+    if (i < LA) {
+      rsrc_words d = ra;
+      if (step >= steps) d[2] = 0u;
+      load_to_lds(d, va[i < LA ? i : 0] + step * KS, 0, base + stage * STAGE + (wave * LA + i) * 1024);
+    } else {
+      rsrc_words d = rb;
+      if (step >= steps) d[2] = 0u;
+      load_to_lds(d, vb[i < LA ? 0 : i - LA] + step * KS, 0, base + stage * STAGE + TM * KS + (wave * LB + i - LA) * 1024);
+    }
   };
   const int wm = wave >> 1, wn = wave & 1;
-  const int mine = (lane & 31) * kStep + ((lane >> 5) ^ (lane >> 2 & 3)) * 16;  // row lane % 32, piece lane / 32
-  i32x4 fa[2][WM], fb[2][WN];
+  i32x4 fa[2][WM], fb[2][WN];  // fragments of even and odd instructions along K
+  // row lane % 32 of a 32-row fragment, piece 2 q + lane / 32
+  const int myrow = (lane & 31) * KS, mysw = swizzle(lane & 31);
   auto read = [&](int stage, int q, int i) {
-    const uint8_t* p = lds + stage * STAGE + (mine ^ (q * 32)) + i * 32 * kStep;
-    if (i < WN) fb[q][i < WN ? i : 0] = *reinterpret_cast<const i32x4*>(p + (TM + wn * 32 * WN) * kStep);
-    if (i < WM) fa[q][i < WM ? i : 0] = *reinterpret_cast<const i32x4*>(p + wm * (32 * WM) * kStep);
+    const uint8_t* p = lds + stage * STAGE + myrow + ((2 * q + (lane >> 5)) ^ mysw) * 16 + i * 32 * KS;
+    if (i < WN) fb[q & 1][i < WN ? i : 0] = *reinterpret_cast<const i32x4*>(p + (TM + wn * 32 * WN) * KS);
+    if (i < WM) fa[q & 1][i < WM ? i : 0] = *reinterpret_cast<const i32x4*>(p + wm * (32 * WM) * KS);
   };
   i32x16 acc[WN][WM] = {};
   auto mask = [&](int step, int q) {
-    if (step * kStep + kStep > K) {  // a last step that is not whole
-      const bool in = step * kStep + (2 * q + (lane >> 5)) * 16 < K;
+    if (step * KS + KS > K) {  // a last step that is not whole
+      const bool in = step * KS + (2 * q + (lane >> 5)) * 16 < K;
 #pragma unroll
-      for (int i = 0; i < WN; ++i) fb[q][i] = in ? fb[q][i] : (i32x4){0, 0, 0, 0};
+      for (int i = 0; i < WN; ++i) fb[q & 1][i] = in ? fb[q & 1][i] : (i32x4){0, 0, 0, 0};
     }
   };
-  auto products = [&](int q, int i) {
+  constexpr int RD = (WM > WN ? WM : WN);  // fragment pairs to read for an instruction along K
+  // slot k of the loads that fill one stage: the last WN rows of a step begin, the others end in the next step
+  auto slot_of = [&](int step, int stage, int k) {
 #pragma unroll
-    for (int j = 0; j < WM; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[q][i], fa[q][j], acc[i][j], 0, 0, 0);
+    for (int i = k * LOADS / SLOTS; i < (k + 1) * LOADS / SLOTS; ++i) fetch(step, stage, i);
   };
-  static_assert(WM == WN, "a row of matrix instructions for each load of a half");
 #pragma unroll
-  for (int s = 0; s < kStages; ++s) {
+  for (int s = 0; s < ST; ++s)
 #pragma unroll
-    for (int i = 0; i < LA; ++i) fetch_a(s, s, i);
-    if (s < kStages - 1) {
-#pragma unroll
-      for (int i = 0; i < LB; ++i) fetch_b(s, s, i);
-    }
-  }
-  wait_loads<(kStages - 2) * LOADS + LA>();
+    for (int k = 0; k < (s < ST - 1 ? SLOTS : WN); ++k) slot_of(s, s, k);
+  wait_loads<(ST - 2) * LOADS + WN * LOADS / SLOTS>();
   lds_barrier();
 #pragma unroll
-  for (int i = 0; i < WN; ++i) read(0, 0, i);
+  for (int i = 0; i < RD; ++i) read(0, 0, i);
   int stage = 0;
 #pragma unroll 1
   for (int step = 0; step < steps; ++step) {
-    const int next = (stage + 1) & (kStages - 1), last = (stage + kStages - 1) & (kStages - 1);
-    mask(step, 0);
+    const int next = stage == ST - 1 ? 0 : stage + 1, last = stage == 0 ? ST - 1 : stage - 1;
 #pragma unroll
-    for (int i = 0; i < WN; ++i) {
-      fetch_b(step + kStages - 1, last, i);
-      read(stage, 1, i);
-      products(0, i);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    wait_loads<(kStages - 2) * LOADS>();  // the next stage has come
-    lds_barrier();                        // for every wave, and this one is read
-    mask(step, 1);
+    for (int q = 0; q < Q; ++q) {
+      if (q == Q - 1) {
+        wait_loads<(ST - 2) * LOADS>();  // the next stage has come
+        lds_barrier();                   // for every wave, and this one is read
+      }
+      mask(step, q);
 #pragma unroll
-    for (int i = 0; i < WN; ++i) {
-      fetch_a(step + kStages, stage, i);
-      read(next, 0, i);
-      products(1, i);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int i = 0; i < WN; ++i) {
+        if (q == Q - 1) slot_of(step + ST, stage, i);
+        else slot_of(step + ST - 1, last, (q + 1) * WN + i);
+#pragma unroll
+        for (int z = i * RD / WN; z < (i + 1) * RD / WN; ++z) read(q == Q - 1 ? next : stage, (q + 1) % Q, z);
+#pragma unroll
+        for (int j = 0; j < WM; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[q & 1][i], fa[q & 1][j], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
     stage = next;
   }
@@ -498,10 +514,10 @@ __global__ __launch_bounds__(256, 1) void k_gemm_int8(const int8_t* __restrict__
       }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the wave reads what its own lanes wrote
     if (whole) {
-      constexpr int PR = COLS * (int)sizeof(T) / 16;  // pieces of a row
+      constexpr int OP = COLS * (int)sizeof(T) / 16;  // pieces of a row
 #pragma unroll 4
-      for (int o = lane; o < 32 * WM * PR; o += 64) {
-        const int row = o / PR, pc = o % PR;
+      for (int o = lane; o < 32 * WM * OP; o += 64) {
+        const int row = o / OP, pc = o % OP;
         const int n = nw + pc * (16 / (int)sizeof(T));
         if (mw + row < M && n < N)
           *reinterpret_cast<u32x4*>(out + (mw + row) * N + n) = *reinterpret_cast<const u32x4*>(mylds + row * PITCH + pc * 16);
@@ -531,17 +547,23 @@ void launch_gemm(const int8_t* a, const float* sa, const int8_t* b, const float*
 #undef BSQ_F
     return;
   }
-  // 256 x 256 tiles move half as many bytes through LDS for each product as
-  // 128 x 128 ones; the small ones serve shapes whose large tiles leave CUs idle.
-  const int64_t big = ((M + 255) / 256) * ((N + 255) / 256);
-  if (big >= bsqh::device_cus()) {
-    hipLaunchKernelGGL((k_gemm_int8<T, 4, 4>), dim3((unsigned)big), dim3(256), 0, s, a, sa, b, sb, bias, M, (int)N, (int)K,
-                       out);
-    return;
-  }
-  const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
-  hipLaunchKernelGGL((k_gemm_int8<T, 2, 2>), dim3((unsigned)tiles), dim3(256), 0, s, a, sa, b, sb, bias, M, (int)N, (int)K,
-                     out);
+  // Large tiles move fewer bytes for each product, small ones leave no CU idle.
+  // Compared by the time of their rounds, in quarters of a 256 x 256 round (one
+  // tile a CU): a round of one 128 x 128 tile a CU takes 1.15, of two 2.1.
+  // Measured, 256 x 256 against 128 x 128: 1024 x 4096 x 4096 52 and 37 us (64
+  // and 256 tiles), 2048 x 4096 x 4096 57 and 44 us, 3000 x 4096 x 4096 66 and
+  // 63 us, 8192 x 1536 x 1536 34 and 35 us, 4096 x 4096 x 4096 74 and 77 us.
+  const int64_t cus = bsqh::device_cus();
+  const int64_t big = ((M + 255) / 256) * ((N + 255) / 256), small = ((M + 127) / 128) * ((N + 127) / 128);
+  const double tb = 4.0 * (double)((big + cus - 1) / cus);
+  const double ts = small <= cus ? 1.15 : 2.1 * (double)((small + 2 * cus - 1) / (2 * cus));
+#define BSQ_G(W, KS, ST, TILES)                                                                                    \
+  hipLaunchKernelGGL((k_gemm_int8<T, W, W, KS, ST>), dim3((unsigned)(TILES)), dim3(256), 0, s, a, sa, b, sb, bias, M, \
+                     (int)N, (int)K, out)
+  if (tb <= ts) BSQ_G(4, 64, 4, big);
+  else if (small <= cus) BSQ_G(2, 128, 3, small);  // one workgroup a CU: more in flight each
+  else BSQ_G(2, 128, 2, small);                    // two a CU
+#undef BSQ_G
 }
 
 int check_gemm(int64_t M, int64_t N, int64_t K, int out_dtype) {
