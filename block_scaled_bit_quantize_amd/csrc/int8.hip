@@ -366,6 +366,7 @@ __global__ __launch_bounds__(256, 1) void k_gemm_int8(const int8_t* __restrict__
   constexpr int PITCH = COLS * (int)sizeof(T) + 16;
   constexpr int OUT = 32 * WM * PITCH;
   __shared__ __attribute__((aligned(16))) uint8_t lds[ST * STAGE > 4 * OUT ? ST * STAGE : 4 * OUT];
+  __shared__ __attribute__((aligned(16))) float esa[TM], esb[TN], ebias[TN];
   const int t = threadIdx.x, wave = uniform(t >> 6), lane = t & 63;
   // Workgroups go round the 8 XCDs; each XCD takes a contiguous part of the
   // tiles, columns first, so that the workgroups it runs at once share rows of
@@ -380,6 +381,11 @@ __global__ __launch_bounds__(256, 1) void k_gemm_int8(const int8_t* __restrict__
   const int rows_a = M - m0 < TM ? (int)(M - m0) : TM, rows_b = N - n0 < TN ? N - n0 : TN;
   const rsrc_words ra = descriptor(a + m0 * K, (uint32_t)rows_a * K);
   const rsrc_words rb = descriptor(b + (int64_t)n0 * K, (uint32_t)rows_b * K);
+  // the tile's scales and bias, asked for before the products (loads in the
+  // epilogue, each waited for, took 8 us a tile)
+  const float ga = t < TM ? sa[m0 + (t < rows_a ? t : rows_a - 1)] : 0.0f;
+  const float gb = t < TN ? sb[n0 + (t < rows_b ? t : rows_b - 1)] : 0.0f;
+  const float gc = t < TN && bias ? bias[n0 + (t < rows_b ? t : rows_b - 1)] : 0.0f;
   // piece p of row r lies at p ^ swizzle(r), so that 16 rows at one piece meet 16 different banks
   auto swizzle = [](int r) { return r / (16 / PR) & (PR - 1); };
   uint32_t va[LA], vb[LB];
@@ -470,6 +476,8 @@ __global__ __launch_bounds__(256, 1) void k_gemm_int8(const int8_t* __restrict__
     stage = next;
   }
   wait_loads<0>();
+  if (t < TM) esa[t] = ga;
+  if (t < TN) esb[t] = gb, ebias[t] = gc;
   lds_barrier();
 
   // outputs: lane holds row lane % 32 of the 32 x 32 tile (i, j) and columns 8 (r / 4) + 4 (lane / 32) + r % 4
@@ -478,10 +486,7 @@ __global__ __launch_bounds__(256, 1) void k_gemm_int8(const int8_t* __restrict__
   const int64_t mw = m0 + wm * 32 * WM;
   float ma[WM];
 #pragma unroll
-  for (int j = 0; j < WM; ++j) {
-    const int64_t m = mw + 32 * j + (lane & 31);
-    ma[j] = sa[m < M ? m : M - 1];
-  }
+  for (int j = 0; j < WM; ++j) ma[j] = esa[wm * 32 * WM + 32 * j + (lane & 31)];
   constexpr int HALVES = 32 * WN / COLS;
 #pragma unroll
   for (int h = 0; h < HALVES; ++h) {
@@ -491,13 +496,8 @@ __global__ __launch_bounds__(256, 1) void k_gemm_int8(const int8_t* __restrict__
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int c = 32 * i + 8 * r + 4 * (lane >> 5);
-        f32x4 s, add;
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const int n = nw + c + z < N ? nw + c + z : N - 1;
-          s[z] = sb[n];
-          add[z] = bias ? bias[n] : 0.0f;
-        }
+        const int cn = wn * 32 * WN + h * COLS + c;
+        const f32x4 s = *reinterpret_cast<const f32x4*>(esb + cn), add = *reinterpret_cast<const f32x4*>(ebias + cn);
 #pragma unroll
         for (int j = 0; j < WM; ++j) {
           const i32x16& v = acc[h * (COLS / 32) + i][j];
