@@ -170,8 +170,11 @@ __device__ __forceinline__ f32x4 multiply(const u32x4 (&w)[4], const u32x4 (&a)[
 }
 
 // ---------------------------------------------------------------- which experts
-// The ids of all pairs, spread over the workgroup's registers, and a bitmap of
-// the experts that occur. Slot s is the s-th smallest of them.
+// The ids of all pairs, and the experts that occur, in slots 0 .. active - 1.
+// Up to 64 pairs: every wave holds all ids, a lane each; a slot is a pair whose
+// expert no earlier pair has, seen by ballots (no barrier). More: the ids are
+// spread over the workgroup's registers, and slot s is the s-th smallest expert
+// of a bitmap in LDS.
 struct RouteLds {
   uint32_t bits[kMaxExperts / 32];
   int count[kMaxPairs / kThreads * kWaves];
@@ -180,11 +183,24 @@ struct RouteLds {
 struct Route {
   static constexpr int C = kMaxPairs / kThreads;
   int id[C];
-  int words;   // lane l holds bitmap word l % 32
-  int active;  // experts that occur
+  int words;      // lane l holds bitmap word l % 32
+  uint64_t first;  // up to 64 pairs: those that own a slot
+  int active;     // experts that occur
 
   __device__ __forceinline__ void init(const int32_t* __restrict__ ids, int pairs, int E, RouteLds& lds) {
     const int t = threadIdx.x, lane = t & 63;
+    active = 0;
+    first = 0;
+    if (pairs <= 64) {
+      const int v = ids[lane < pairs ? lane : 0];
+      id[0] = lane < pairs && v < E ? v : -1;
+      for (uint64_t rem = __ballot(id[0] >= 0); rem; ++active) {
+        const int p = __ffsll((unsigned long long)rem) - 1;
+        first |= 1ull << p;
+        rem &= ~__ballot(id[0] == __builtin_amdgcn_readlane(id[0], p));
+      }
+      return;
+    }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int p = t + c * kThreads;
@@ -201,12 +217,16 @@ struct Route {
       if (id[c] >= 0) atomicOr(&lds.bits[id[c] >> 5], 1u << (id[c] & 31));
     lds_barrier();
     words = (int)lds.bits[lane & 31];
-    active = 0;
     for (int w = 0; w * 32 < E; ++w) active += __popc((uint32_t)__builtin_amdgcn_readlane(words, w));
   }
 
   // The expert of a slot below `active`, counted out by the scalar unit.
   __device__ __forceinline__ int expert_of(int slot) const {
+    if (first) {
+      uint64_t m = first;
+      for (; slot > 0; --slot) m &= m - 1;
+      return __builtin_amdgcn_readlane(id[0], __ffsll((unsigned long long)m) - 1);
+    }
     int at = 0, before = 0;
     uint32_t word = 0;
 #pragma unroll 1
@@ -224,6 +244,12 @@ struct Route {
   // many they are. Every wave calls it, after its last use of the list before.
   __device__ __forceinline__ int list_pairs(int expert, int pairs, RouteLds& lds) const {
     const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
+    if (first) {
+      const uint64_t m = __ballot(id[0] == expert);
+      if (wave == 0 && id[0] == expert) lds.list[__popcll(m & ((1ull << lane) - 1))] = (uint16_t)lane;
+      lds_barrier();
+      return __popcll(m);
+    }
     uint64_t mask[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -620,9 +646,20 @@ __global__ __launch_bounds__(256) void k_moe_sum(const float* __restrict__ z, co
   if (id >= (int64_t)tokens * per) return;
   const int t = (int)(id / per), n = (int)(id % per) * 4;
   f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int j = 0; j < k; ++j) {
-    const int e = ids[t * k + j];
-    if (e >= 0 && e < E) s += weights[t * k + j] * *reinterpret_cast<const f32x4*>(z + ((int64_t)t * k + j) * H + n);
+  const float* zt = z + (int64_t)t * k * H + n;
+  for (int j0 = 0; j0 < k; j0 += 8) {  // eight rows' loads at once; an invalid pair's row holds anything
+    f32x4 v[8];
+    float w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int q = j0 + j < k ? j0 + j : k - 1;
+      const int e = ids[t * k + q];
+      w[j] = weights[t * k + q];
+      v[j] = *reinterpret_cast<const f32x4*>(zt + (int64_t)q * H);
+      if (j0 + j >= k || e < 0 || e >= E) v[j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f}, w[j] = 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += w[j] * v[j];
   }
   if constexpr (sizeof(T) == 4) {
     *reinterpret_cast<f32x4*>(y + (int64_t)t * H + n) = s;
