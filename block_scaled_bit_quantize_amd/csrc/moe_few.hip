@@ -170,34 +170,52 @@ __device__ __forceinline__ f32x4 multiply(const u32x4 (&w)[4], const u32x4 (&a)[
 }
 
 // ---------------------------------------------------------------- which experts
-// The ids of all pairs, and the experts that occur, in slots 0 .. active - 1.
-// Up to 64 pairs: every wave holds all ids, a lane each; a slot is a pair whose
-// expert no earlier pair has, seen by ballots (no barrier). More: the ids are
-// spread over the workgroup's registers, and slot s is the s-th smallest expert
-// of a bitmap in LDS.
+// The experts that occur, as slots 0 .. slots - 1: a slot is an expert and 16
+// (or the last few) of the pairs that chose it, which is one pass over its
+// weights. (Slots, and not experts, are what the workgroups share out: where a
+// few experts take most tokens, shares of experts left the others waiting.)
+// Up to 64 pairs: every wave holds all ids, a lane each, and sees an expert's
+// first pair and its number of pairs by ballots (no barrier). More: the ids are
+// spread over the workgroup's registers and the pairs of each expert counted
+// in LDS; lane l of every wave holds the running sums of the slots of experts
+// [16 l, 16 l + 16).
 struct RouteLds {
-  uint32_t bits[kMaxExperts / 32];
+  uint32_t pairs[kMaxExperts / 2];  // of two experts a word (at most kMaxPairs each)
   int count[kMaxPairs / kThreads * kWaves];
   uint16_t list[kMaxPairs];
 };
+struct Slot {
+  int expert, part;  // pairs [16 part, 16 part + 16) of the expert's
+};
 struct Route {
   static constexpr int C = kMaxPairs / kThreads;
+  static constexpr int G = kMaxExperts / 64;  // experts of a lane
   int id[C];
-  int words;      // lane l holds bitmap word l % 32
-  uint64_t first;  // up to 64 pairs: those that own a slot
-  int active;     // experts that occur
+  bool few;
+  uint64_t first;  // few: the first pair of each expert
+  int upto;        // else: slots of this lane's experts and of all before
+  int slots;
+
+  __device__ __forceinline__ static int slots_of(uint32_t n) { return (int)((n + 15) / 16); }
+  __device__ __forceinline__ static int pairs_of(const RouteLds& lds, int e) {
+    return (int)(lds.pairs[e >> 1] >> (16 * (e & 1)) & 0xFFFFu);
+  }
 
   __device__ __forceinline__ void init(const int32_t* __restrict__ ids, int pairs, int E, RouteLds& lds) {
     const int t = threadIdx.x, lane = t & 63;
-    active = 0;
+    slots = 0;
     first = 0;
-    if (pairs <= 64) {
+    upto = 0;
+    few = pairs <= 64;
+    if (few) {
       const int v = ids[lane < pairs ? lane : 0];
       id[0] = lane < pairs && v < E ? v : -1;
-      for (uint64_t rem = __ballot(id[0] >= 0); rem; ++active) {
+      for (uint64_t rem = __ballot(id[0] >= 0); rem;) {
         const int p = __ffsll((unsigned long long)rem) - 1;
+        const uint64_t m = __ballot(id[0] == __builtin_amdgcn_readlane(id[0], p));
         first |= 1ull << p;
-        rem &= ~__ballot(id[0] == __builtin_amdgcn_readlane(id[0], p));
+        slots += slots_of(__popcll(m));
+        rem &= ~m;
       }
       return;
     }
@@ -210,41 +228,53 @@ struct Route {
         id[c] = p < pairs && v < E ? v : -1;
       }
     }
-    if (t < kMaxExperts / 32) lds.bits[t] = 0;
+    static_assert(kMaxExperts / 2 == kThreads, "a word each");
+    lds.pairs[t] = 0;
     lds_barrier();
 #pragma unroll
     for (int c = 0; c < C; ++c)
-      if (id[c] >= 0) atomicOr(&lds.bits[id[c] >> 5], 1u << (id[c] & 31));
+      if (id[c] >= 0) atomicAdd(&lds.pairs[id[c] >> 1], 1u << (16 * (id[c] & 1)));
     lds_barrier();
-    words = (int)lds.bits[lane & 31];
-    for (int w = 0; w * 32 < E; ++w) active += __popc((uint32_t)__builtin_amdgcn_readlane(words, w));
+#pragma unroll
+    for (int w = 0; w < G / 2; ++w) {
+      const uint32_t n = lds.pairs[lane * (G / 2) + w];
+      upto += slots_of(n & 0xFFFFu) + slots_of(n >> 16);
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(upto, o, 64);
+      if (lane >= o) upto += v;
+    }
+    slots = __builtin_amdgcn_readlane(upto, 63);
   }
 
-  // The expert of a slot below `active`, counted out by the scalar unit.
-  __device__ __forceinline__ int expert_of(int slot) const {
-    if (first) {
-      uint64_t m = first;
-      for (; slot > 0; --slot) m &= m - 1;
-      return __builtin_amdgcn_readlane(id[0], __ffsll((unsigned long long)m) - 1);
+  // A slot below `slots`, counted out by the scalar unit.
+  __device__ __forceinline__ Slot slot(int s, const RouteLds& lds) const {
+    if (few) {
+      uint64_t rem = first;
+      for (;; rem &= rem - 1) {
+        const int e = __builtin_amdgcn_readlane(id[0], __ffsll((unsigned long long)rem) - 1);
+        const int n = slots_of(__popcll(__ballot(id[0] == e)));
+        if (s < n) return {e, s};
+        s -= n;
+      }
     }
-    int at = 0, before = 0;
-    uint32_t word = 0;
+    const int src = __ffsll((unsigned long long)__ballot(s < upto)) - 1;
+    if (src > 0) s -= __builtin_amdgcn_readlane(upto, src - 1);
+    int e = src * G;
 #pragma unroll 1
-    for (; at < kMaxExperts / 32; ++at) {
-      word = (uint32_t)__builtin_amdgcn_readlane(words, at);
-      const int n = __popc(word);
-      if (before + n > slot) break;
-      before += n;
+    for (;; ++e) {
+      const int n = slots_of(uniform(pairs_of(lds, e)));
+      if (s < n) return {e, s};
+      s -= n;
     }
-    for (; before < slot; ++before) word &= word - 1;
-    return at * 32 + __ffs((int)word) - 1;
   }
 
   // Writes the pairs of an expert into lds.list, ascending, and returns how
   // many they are. Every wave calls it, after its last use of the list before.
   __device__ __forceinline__ int list_pairs(int expert, int pairs, RouteLds& lds) const {
     const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
-    if (first) {
+    if (few) {
       const uint64_t m = __ballot(id[0] == expert);
       if (wave == 0 && id[0] == expert) lds.list[__popcll(m & ((1ull << lane) - 1))] = (uint16_t)lane;
       lds_barrier();
@@ -338,7 +368,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_any(Product a) {
   Route route;
   route.init(a.ids, a.pairs, a.E, lds);
   const int tiles = (a.width + OUT - 1) / OUT;
-  const int64_t units = (int64_t)route.active * tiles;
+  const int64_t units = (int64_t)route.slots * tiles;
   int u = uniform((int)(units * blockIdx.x / gridDim.x));
   const int u1 = uniform((int)(units * (blockIdx.x + 1) / gridDim.x));
   const int nblk = a.K / 16;
@@ -348,17 +378,17 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_any(Product a) {
   const brsrc_t act = buffer(a.in, (int64_t)(GLU ? a.pairs / a.k : a.pairs) * a.K * (int)sizeof(T));
   int buf = 0;
   while (u < u1) {
-    const int slot = u / tiles, tile0 = u - slot * tiles;
+    const int at = u / tiles, tile0 = u - at * tiles;
     const int tile1 = tile0 + (u1 - u) < tiles ? tile0 + (u1 - u) : tiles;
     u += tile1 - tile0;
-    const int expert = uniform(route.expert_of(slot));
+    const Slot slot = route.slot(at, lds);
+    const int expert = uniform(slot.expert), mt0 = uniform(slot.part) * 16;
     const int np = uniform(route.list_pairs(expert, a.pairs, lds));
     const int64_t wrow = (int64_t)expert * rows;
     const brsrc_t codes = buffer(a.codes + wrow * (a.K / 2), (int64_t)rows * (a.K / 2));
     const brsrc_t scales = buffer(a.scales + wrow * nblk, (int64_t)rows * nblk);
     const float so = a.outer[expert];
-#pragma unroll 1
-    for (int mt0 = 0; mt0 < np; mt0 += 16) {
+    {
       const int mine = lds.list[mt0 + col < np ? mt0 + col : mt0];
       const uint32_t aoff = (uint32_t)((GLU ? mine / a.k : mine) * a.K) * (uint32_t)sizeof(T);
       auto raw_at = [&](int st) {
@@ -463,7 +493,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_stream(Product a) {
   Route route;
   route.init(a.ids, a.pairs, a.E, lds);
   const int tiles = (a.width + OUT - 1) / OUT;
-  const int64_t units = (int64_t)route.active * tiles;
+  const int64_t units = (int64_t)route.slots * tiles;
   int u = uniform((int)(units * blockIdx.x / gridDim.x));
   const int u1 = uniform((int)(units * (blockIdx.x + 1) / gridDim.x));
   const int nblk = a.K / 16;
@@ -491,10 +521,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_stream(Product a) {
   const int mine0 = (col >> 3) * 64 + (col & 7) * 8 + (grp ^ (col >> 1 & 7)), mine1 = mine0 ^ 4;
   int buf = 0;
   while (u < u1) {
-    const int slot = u / tiles, tile0 = u - slot * tiles;
+    const int at = u / tiles, tile0 = u - at * tiles;
     const int tile1 = tile0 + (u1 - u) < tiles ? tile0 + (u1 - u) : tiles;
     u += tile1 - tile0;
-    const int expert = uniform(route.expert_of(slot));
+    const Slot slot = route.slot(at, lds);
+    const int expert = uniform(slot.expert), mt0 = uniform(slot.part) * 16;
     const int np = uniform(route.list_pairs(expert, a.pairs, lds));
     const int64_t wrow = (int64_t)expert * rows;
     const rsrc_words codes = descriptor(a.codes + wrow * pitch, (uint32_t)rows * pitch);
@@ -532,8 +563,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_stream(Product a) {
       }
     };
 
-#pragma unroll 1
-    for (int mt0 = 0; mt0 < np; mt0 += 16) {
+    {
       // lanes past the last pair repeat one and are not stored
       const int pair = lds.list[mt0 + col < np ? mt0 + col : mt0];
       const uint32_t aoff = (uint32_t)((GLU ? pair / a.k : pair) * a.K) * (uint32_t)sizeof(T);
