@@ -526,7 +526,6 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_stream(Product a) {
     u += tile1 - tile0;
     const Slot slot = route.slot(at, lds);
     const int expert = uniform(slot.expert), mt0 = uniform(slot.part) * 16;
-    const int np = uniform(route.list_pairs(expert, a.pairs, lds));
     const int64_t wrow = (int64_t)expert * rows;
     const rsrc_words codes = descriptor(a.codes + wrow * pitch, (uint32_t)rows * pitch);
     const uint8_t* sbase = a.scales + wrow * nblk;
@@ -563,6 +562,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_stream(Product a) {
       }
     };
 
+    // the ring starts before the activations are looked for
+    wait_loads<0>();  // what was in flight to its places before
+#pragma unroll
+    for (int i = 0; i < R; ++i) fetch(tile0 + i / S, i % S, i);
+    const int np = uniform(route.list_pairs(expert, a.pairs, lds));
+
     {
       // lanes past the last pair repeat one and are not stored
       const int pair = lds.list[mt0 + col < np ? mt0 + col : mt0];
@@ -582,17 +587,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_stream(Product a) {
                                       g + s < cnt ? (sp0 + g + s) * 16 + 2 * (4 * p + grp) : nblk, nblk);
           __builtin_amdgcn_sched_barrier(0);
         };
-        auto start = [&] {
-          wait_loads<0>();  // what was in flight to the ring's places before, too
-#pragma unroll
-          for (int i = 0; i < R; ++i) fetch(tile0 + i / S, i % S, i);
-          __builtin_amdgcn_sched_barrier(0);
-        };
         float mx = 0.0f;
 #pragma unroll
         for (int g = 0; g < S; g += G) {
           read(g);
-          if (G == S) start();
 #pragma unroll
           for (int s = 0; s < G; ++s)
 #pragma unroll
@@ -607,7 +605,6 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_stream(Product a) {
 #pragma unroll
         for (int g = 0; g < S; g += G) {
           if (G < S) read(g);
-          if (G < S && g + G == S) start();
 #pragma unroll
           for (int s = 0; s < G; ++s)
 #pragma unroll
