@@ -19,6 +19,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 
@@ -362,7 +363,7 @@ __global__ __launch_bounds__(256, 1) void k_gemm_int8(const int8_t* __restrict__
   constexpr int Q = KS / 32;                    // matrix instructions along a step
   constexpr int SLOTS = Q * WN;                 // rows of matrix instructions in a step
   // the output of a wave, 32 WM rows of COLS columns at a time
-  constexpr int COLS = sizeof(T) == 2 ? 32 * WN : 16 * WN;
+  constexpr int COLS = sizeof(T) == 2 || WN == 1 ? 32 * WN : 16 * WN;
   constexpr int PITCH = COLS * (int)sizeof(T) + 16;
   constexpr int OUT = 32 * WM * PITCH;
   __shared__ __attribute__((aligned(16))) uint8_t lds[ST * STAGE > 4 * OUT ? ST * STAGE : 4 * OUT];
@@ -482,7 +483,6 @@ __global__ __launch_bounds__(256, 1) void k_gemm_int8(const int8_t* __restrict__
 
   // outputs: lane holds row lane % 32 of the 32 x 32 tile (i, j) and columns 8 (r / 4) + 4 (lane / 32) + r % 4
   uint8_t* mylds = lds + wave * OUT;
-  const bool whole = (N * (int)sizeof(T)) % 16 == 0;
   const int64_t mw = m0 + wm * 32 * WM;
   float ma[WM];
 #pragma unroll
@@ -513,20 +513,21 @@ __global__ __launch_bounds__(256, 1) void k_gemm_int8(const int8_t* __restrict__
         }
       }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the wave reads what its own lanes wrote
-    if (whole) {
-      constexpr int OP = COLS * (int)sizeof(T) / 16;  // pieces of a row
+    // 16-byte pieces of rows; rows of another pitch than 16 bytes take them unaligned, and the last piece of a row
+    // that is not whole goes element by element
+    constexpr int OP = COLS * (int)sizeof(T) / 16, EP = 16 / (int)sizeof(T);  // pieces of a row, elements of a piece
 #pragma unroll 4
-      for (int o = lane; o < 32 * WM * OP; o += 64) {
-        const int row = o / OP, pc = o % OP;
-        const int n = nw + pc * (16 / (int)sizeof(T));
-        if (mw + row < M && n < N)
-          *reinterpret_cast<u32x4*>(out + (mw + row) * N + n) = *reinterpret_cast<const u32x4*>(mylds + row * PITCH + pc * 16);
-      }
-    } else {
-#pragma unroll 4
-      for (int o = lane; o < 32 * WM * COLS; o += 64) {
-        const int row = o / COLS, n = nw + o % COLS;
-        if (mw + row < M && n < N) out[(mw + row) * N + n] = *reinterpret_cast<const T*>(mylds + row * PITCH + o % COLS * (int)sizeof(T));
+    for (int o = lane; o < 32 * WM * OP; o += 64) {
+      const int row = o / OP, pc = o % OP;
+      const int n = nw + pc * EP;
+      if (mw + row < M && n < N) {
+        T* to = out + (mw + row) * N + n;
+        const T* from = reinterpret_cast<const T*>(mylds + row * PITCH + pc * 16);
+        if (n + EP <= N) {
+          *reinterpret_cast<u32x4_a2*>(to) = *reinterpret_cast<const u32x4*>(from);
+        } else {
+          for (int i = 0; n + i < N; ++i) to[i] = from[i];
+        }
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -553,6 +554,9 @@ void launch_gemm(const int8_t* a, const float* sa, const int8_t* b, const float*
   // Measured, 256 x 256 against 128 x 128: 1024 x 4096 x 4096 52 and 37 us (64
   // and 256 tiles), 2048 x 4096 x 4096 57 and 44 us, 3000 x 4096 x 4096 66 and
   // 63 us, 8192 x 1536 x 1536 34 and 35 us, 4096 x 4096 x 4096 74 and 77 us.
+  // Where 128 x 128 tiles leave three CUs of four idle, 64 x 64 ones: 128 x 2048
+  // x 7168 30 and 23 us, 256 x 4096 x 4096 21 and 17 us (64 tiles of 128 x 128;
+  // with 128 of them, 512 x 4096 x 4096, 23 and 25 us).
   const int64_t cus = bsqh::device_cus();
   const int64_t big = ((M + 255) / 256) * ((N + 255) / 256), small = ((M + 127) / 128) * ((N + 127) / 128);
   const double tb = 4.0 * (double)((big + cus - 1) / cus);
@@ -560,7 +564,8 @@ void launch_gemm(const int8_t* a, const float* sa, const int8_t* b, const float*
 #define BSQ_G(W, KS, ST, TILES)                                                                                    \
   hipLaunchKernelGGL((k_gemm_int8<T, W, W, KS, ST>), dim3((unsigned)(TILES)), dim3(256), 0, s, a, sa, b, sb, bias, M, \
                      (int)N, (int)K, out)
-  if (tb <= ts) BSQ_G(4, 64, 4, big);
+  if (4 * small <= cus) BSQ_G(1, 128, 4, ((M + 63) / 64) * ((N + 63) / 64));
+  else if (tb <= ts) BSQ_G(4, 64, 4, big);
   else if (small <= cus) BSQ_G(2, 128, 3, small);  // one workgroup a CU: more in flight each
   else BSQ_G(2, 128, 2, small);                    // two a CU
 #undef BSQ_G

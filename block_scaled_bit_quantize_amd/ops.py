@@ -464,8 +464,9 @@ def swiglu_quantize_int8(h13):
 
 
 def _int8_operand(codes, scales, what):
-    _need(codes.dim() == 2 and codes.dtype == torch.int8 and scales.dtype == torch.float32
-          and scales.numel() == codes.shape[0], f"{what}: int8 codes [rows, K] with float32 scales [rows]")
+    if not (codes.dim() == 2 and codes.dtype == torch.int8 and scales.dtype == torch.float32
+            and scales.numel() == codes.shape[0]):
+        raise BsqError(what + ": int8 codes [rows, K] with float32 scales [rows]")
 
 
 def gemm_int8(a_codes, a_scales, b_codes, b_scales, bias=None, out_dtype=torch.bfloat16):

@@ -362,3 +362,27 @@ def test_bindings_refuse():
         with pytest.raises(bsq.BsqError):
             bsq.moe_few_tokens_nvfp4(**{**good, name: v})
             pytest.fail(f"{name} was accepted")
+
+
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+@pytest.mark.parametrize("M,N,K", [(66, 70, 528), (300, 65, 2064), (130, 1030, 384), (2050, 1026, 208), (4100, 4099, 80),
+                                   (4096, 4096, 128), (8200, 515, 96)])
+def test_gemm_int8_tiles(M, N, K, out_dtype):
+    """Every tile size, with rows of outputs that are not whole 16-byte pieces."""
+    int8_case(M, N, K, out_dtype, bias=N % 2 == 1, seed=K)
+
+
+@pytest.mark.parametrize("T,H,F,E,k", [(3, 4096, 1536, 16, 4), (2, 7168, 64, 4, 2), (2, 8208, 48, 4, 2), (5, 6160, 2064, 4, 2),
+                                       (1, 64, 8208, 3, 1), (128, 64, 64, 8, 8)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_moe_few_long_rows(T, H, F, E, k, dtype):
+    """Rows at and past what the streams keep in registers."""
+    moe_case(T, H, F, E, k, dtype, seed=H + F)
+
+
+def test_moe_few_skewed_experts():
+    """Some experts take several passes, most one, some none."""
+    rng = np.random.default_rng(4)
+    ids = np.stack([rng.choice(40, size=6, replace=False, p=(lambda p: p / p.sum())(np.arange(1, 41) ** -1.5))
+                    for _ in range(150)])
+    moe_case(150, 96, 80, 40, 6, BF16, seed=4, ids=ids)
