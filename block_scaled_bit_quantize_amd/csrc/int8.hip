@@ -165,7 +165,8 @@ __device__ __forceinline__ rsrc_words descriptor(const void* p, uint32_t bytes) 
                       (uint32_t)uniform((int)bytes), 0x00020000u};
 }
 // 64 lanes of 16 bytes: lane l's at lds + 16 l. There is no register to be
-// overwritten in flight; the address register is read at issue.
+// overwritten in flight; the address register is read at issue, and m0 is one
+// that the compiler sets anew before each use of its own.
 __device__ __forceinline__ void load_to_lds(rsrc_words rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff), "s"(rsrc),
                "s"(soff)

@@ -440,14 +440,18 @@ int bsq_moe_gate_backward(const float* dweights, const float* weights, const int
  * w13_*    codes [E, 2*ffn, hidden/2], scales [E, 2*ffn, hidden/16], outer [E]:
  *          gate rows [0, ffn), then up rows; w2_* [E, hidden, ffn/2], ... as
  *          bsq_quantize_nvfp4 writes them with BSQ_OUTER_TENSOR.
- * Products of exactly decoded weights with x in float32 sums; silu(G) * U is
- * kept to 16 significant bits or more; a token's experts are added in slot
- * order in float32 (the same bits on every call).
+ * Products of exactly decoded weights in float32 sums; BF16 x is multiplied as
+ * it is, F32 x and silu(G) * U to 22 significant bits (all after scaling by a
+ * power of two; values below 2^-31 of a token's largest lose bits). A token's
+ * experts are added in slot order in float32: the same bits on every call.
  * hidden % 16 == 0, ffn % 16 == 0, both in [16, 32768]; 1 <= E <= 1024,
  * 1 <= k <= 64, tokens * k <= BSQ_MOE_FEW_MAX_PAIRS (more tokens: the grouped
  * GEMMs).
  * ws       bsq_moe_few_nvfp4_workspace() bytes.
- * x, out, codes, scales and ws 16-byte aligned, the others 4.
+ * x, out, codes, scales and ws 16-byte aligned, the others 4. Where hidden or
+ * ffn is no multiple of 256 its scales are read in aligned 4-byte words: that
+ * array must stay readable up to the next 4-byte boundary past its end, as any
+ * allocation of whole 4-byte words is.
  * Errors: NULL, SHAPE, ALIGN, DTYPE, WORKSPACE, LAUNCH.
  * ---------------------------------------------------------------------- */
 #define BSQ_MOE_FEW_MAX_PAIRS 2048
@@ -468,7 +472,9 @@ int bsq_moe_few_nvfp4(const void* x, int dtype, int64_t tokens, int64_t hidden, 
  *   below 2^-126 (all codes are then 0); code = rint(f32(x * f32(1/s))), half to
  *   even, within [-127, 127].
  * bsq_swiglu_quantize_int8: the same of silu(g) * u in float32, h13
- *   [rows, 2*ffn] with gate columns [0, ffn), then up columns.
+ *   [rows, 2*ffn] with gate columns [0, ffn), then up columns; silu(g) is
+ *   g / (1 + e^-g) by the hardware's base-2 exponential and reciprocal (a few
+ *   units in the last place, |g| 2^-24 more).
  * bsq_gemm_int8: out[m, n] = (sum_k a[m, k] b[n, k]) a_scales[m] b_scales[n]
  *   + bias[n]; a_codes int8 [M, K], b_codes int8 [N, K] (any codes, -128
  *   included), exact integer sums; bias FP32 [N] or NULL; out [M, N] of
