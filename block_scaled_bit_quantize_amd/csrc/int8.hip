@@ -70,7 +70,9 @@ __device__ __forceinline__ float row_scale(float amax) {
 }
 
 // TPR threads share a row and keep it in registers, up to MAXB blocks of 16
-// values each: one read of x. GLU: a row of x holds 2C values, gate then up,
+// values each: one read of x, bound by the memory. [65536, 7168] bf16 takes
+// 246 us (5.7 TB/s), [16384, 4096] 43 us; the GLU form of [16384, 2 x 1536]
+// 25 us. GLU: a row of x holds 2C values, gate then up,
 // and what is quantized is silu(gate) * up.
 template <typename T, int TPR, int MAXB, bool GLU>
 __global__ __launch_bounds__(kQThreads) void k_quant_int8(const T* __restrict__ x, int64_t rows, int64_t C,
@@ -187,40 +189,41 @@ __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = __builtin_bi
 
 // ---------------------------------------------------------------- few rows
 // Up to 64 rows of activations: bound by reading the weights once, and by how
-// soon. A workgroup owns 16 weight rows for all M; its eight waves share K, each
-// with a ring of R steps of 64 bytes in LDS of its own (no barriers), filled
-// by loads that go straight there: four lanes side by side read 64 bytes of a
-// row, where a load in the matrix instruction's own layout (a lane, a row)
-// costs the address unit four times as long. Pieces of row r lie in the order
-// piece ^ (r / 4 % 4) as in the large tiles. The exact integer partial sums meet
-// in LDS.
+// soon. A workgroup owns 16 weight rows for all M; its waves share K, each
+// with a ring of R steps of 128 bytes in LDS of its own (no barriers), filled
+// by loads that go straight there: eight lanes side by side read a whole line
+// of a row (64 bytes a row took the address unit twice as long, a lane a row as
+// in the matrix instruction's own layout four times). Piece p of row r lies at
+// p ^ (r / 2 % 8), so that 16 rows at one piece meet 16 different banks. The
+// exact integer partial sums meet in LDS. 50 x 2048 x 7168 takes 9.4 us (11.6
+// with 64 bytes of a row a load), 64 x 8192 x 4096 15.9 us.
 //
 // FUSED: the activations come unquantized, few enough to lie in LDS (kFuseBytes);
 // every workgroup quantizes them itself, while the first weights are on their
 // way, and one launch is the whole layer. The codes are those of
 // k_quant_int8: the same steps in the same order.
-constexpr int kFThreads = 512;
-constexpr int kFWaves = kFThreads / 64;
 constexpr int kFuseBytes = 32768;
 constexpr int kFuseCodes = 16384;
+// Waves: as many as leave each of them a ring of three steps or more in 160 KB.
+constexpr int few_waves(bool fused) { return fused ? 8 : 4; }
 
 template <typename X, typename T, int MT, bool FUSED>
-__global__ __launch_bounds__(kFThreads) void k_gemm_int8_few(const X* __restrict__ a, const float* __restrict__ sa,
-                                                            const int8_t* __restrict__ b, const float* __restrict__ sb,
-                                                            const float* __restrict__ bias, int M, int N, int K,
-                                                            T* __restrict__ out) {
-  constexpr int LOADS = FUSED ? 1 : 1 + MT;               // of a step: 16 rows of 64 bytes each
-  constexpr int R = FUSED ? 8 : MT == 1 ? 6 : MT == 2 ? 5 : 3;
+__global__ __launch_bounds__(64 * few_waves(FUSED)) void k_gemm_int8_few(
+    const X* __restrict__ a, const float* __restrict__ sa, const int8_t* __restrict__ b, const float* __restrict__ sb,
+    const float* __restrict__ bias, int M, int N, int K, T* __restrict__ out) {
+  constexpr int kFWaves = few_waves(FUSED), kFThreads = 64 * kFWaves;
+  constexpr int LOADS = FUSED ? 2 : 2 + 2 * MT;           // of a step: 8 rows of 128 bytes each
+  constexpr int R = FUSED ? 4 : MT == 1 ? 8 : MT == 2 ? 5 : 3;
   constexpr int XLOADS = FUSED ? kFuseBytes / 1024 / kFWaves : 0;
   __shared__ __attribute__((aligned(16))) uint8_t ring[kFWaves][R][LOADS * 1024];
   __shared__ i32x4 part[kFWaves][MT][64];
   __shared__ __attribute__((aligned(16))) uint8_t raw[FUSED ? kFuseBytes : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t code[FUSED ? kFuseCodes + 16 * 16 + 64 : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t code[FUSED ? kFuseCodes + 16 * 16 + 128 : 16];
   __shared__ uint32_t rmax[16];
   const int t = threadIdx.x, wave = uniform(t >> 6), lane = t & 63;
   const int n0 = (int)blockIdx.x * 16;
   const int rows_b = N - n0 < 16 ? N - n0 : 16;
-  const int steps = (K + 63) / 64;
+  const int steps = (K + 127) / 128;
   const int st0 = steps * wave / kFWaves, st1 = steps * (wave + 1) / kFWaves;
   // what the epilogue will need, ahead of the stream
   constexpr int PER = (MT * 256 + kFThreads - 1) / kFThreads;
@@ -232,21 +235,26 @@ __global__ __launch_bounds__(kFThreads) void k_gemm_int8_few(const X* __restrict
     eb[i] = sb[n < N ? n : N - 1];
     ec[i] = bias ? bias[n < N ? n : N - 1] : 0.0f;
   }
-  const int r = lane >> 2, piece = (lane & 3) ^ (r >> 2 & 3);
   const rsrc_words db = descriptor(b + (int64_t)n0 * K, (uint32_t)rows_b * K);
   const rsrc_words da = descriptor(a, FUSED ? (uint32_t)(M * K) * (uint32_t)sizeof(X) : (uint32_t)M * K);
-  const uint32_t vb = (uint32_t)(r < rows_b ? r : rows_b - 1) * K + piece * 16;
-  uint32_t va[MT];
+  constexpr uint32_t kPastEnd = 0x40000000u;  // past every buffer here, once or twice
+  // Rows past N or M are not fetched: what lies in their place meets outputs that are not stored.
+  uint32_t vb[2], va[2 * MT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) va[m] = (uint32_t)(16 * m + r < M ? 16 * m + r : M - 1) * K + piece * 16;
+  for (int i = 0; i < 2 * MT; ++i) {
+    const int r = 8 * i + (lane >> 3);
+    const uint32_t piece = (uint32_t)((lane & 7) ^ (r >> 1 & 7)) * 16;
+    if (i < 2) vb[i < 2 ? i : 0] = r < rows_b ? (uint32_t)r * K + piece : kPastEnd;
+    va[i] = r < M ? (uint32_t)r * K + piece : kPastEnd;
+  }
   const uint32_t base = lds_offset(&ring[wave][0][0]);
-  constexpr uint32_t kPastEnd = 0x80000000u;
   auto fetch = [&](int st, int place) {  // past the last step: issued all the same (the waits count them), past the end
-    const uint32_t k = st < st1 ? (uint32_t)st * 64 : kPastEnd;
-    load_to_lds(db, vb + k, 0, base + place * (LOADS * 1024));
+    const uint32_t k = st < st1 ? (uint32_t)st * 128 : kPastEnd, at = base + place * (LOADS * 1024);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) load_to_lds(db, vb[i] + k, 0, at + i * 1024);
     if constexpr (!FUSED) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m) load_to_lds(da, va[m] + k, 0, base + place * (LOADS * 1024) + (1 + m) * 1024);
+      for (int i = 0; i < 2 * MT; ++i) load_to_lds(da, va[i] + k, 0, at + (2 + i) * 1024);
     }
   };
   if constexpr (FUSED) {
@@ -284,23 +292,29 @@ __global__ __launch_bounds__(kFThreads) void k_gemm_int8_few(const X* __restrict
     lds_barrier();
   }
   const int col = lane & 15, grp = lane >> 4;
-  const int mine = col * 64 + (grp ^ (col >> 2 & 3)) * 16;
   const uint8_t* crow = code + (FUSED && col < M ? col : 0) * pitch + grp * 16;  // lanes past M repeat row 0
   i32x4 acc[MT] = {};
   int place = 0;
 #pragma unroll 1
   for (int st = st0; st < st1; ++st) {
     wait_loads<(R - 1) * LOADS>();
-    const uint8_t* p = &ring[wave][place][0] + mine;
-    i32x4 w = *reinterpret_cast<const i32x4*>(p), v[MT];
+    i32x4 w[2], v[2][MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-      v[m] = *reinterpret_cast<const i32x4*>(FUSED ? crow + st * 64 : p + (1 + m) * 1024);
+    for (int h = 0; h < 2; ++h) {  // 64 values of K each
+      const uint8_t* p = &ring[wave][place][0] + col * 128 + ((4 * h + grp) ^ (col >> 1)) * 16;
+      w[h] = *reinterpret_cast<const i32x4*>(p);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        v[h][m] = *reinterpret_cast<const i32x4*>(FUSED ? crow + st * 128 + h * 64 : p + (1 + m) * 2048);
+    }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the place may be filled again
     fetch(st + R, place);
-    if (st * 64 + 64 > K && st * 64 + grp * 16 >= K) w = (i32x4){0, 0, 0, 0};  // past the end of K
 #pragma unroll
-    for (int m = 0; m < MT; ++m) acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, v[m], acc[m], 0, 0, 0);
+    for (int h = 0; h < 2; ++h) {
+      if (st * 128 + 128 > K && st * 128 + h * 64 + grp * 16 >= K) w[h] = (i32x4){0, 0, 0, 0};  // past the end of K
+#pragma unroll
+      for (int m = 0; m < MT; ++m) acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[h], v[h][m], acc[m], 0, 0, 0);
+    }
     place = place == R - 1 ? 0 : place + 1;
   }
 #pragma unroll
@@ -541,7 +555,7 @@ void launch_gemm(const int8_t* a, const float* sa, const int8_t* b, const float*
   if (M <= 64) {
     const dim3 grid((unsigned)((N + 15) / 16));
 #define BSQ_F(MT)                                                                                                     \
-  hipLaunchKernelGGL((k_gemm_int8_few<int8_t, T, MT, false>), grid, dim3(kFThreads), 0, s, a, sa, b, sb, bias, (int)M, \
+  hipLaunchKernelGGL((k_gemm_int8_few<int8_t, T, MT, false>), grid, dim3(64 * few_waves(false)), 0, s, a, sa, b, sb, bias, (int)M, \
                      (int)N, (int)K, out)
     if (M <= 16) BSQ_F(1);
     else if (M <= 32) BSQ_F(2);
@@ -648,7 +662,7 @@ extern "C" int bsq_linear_int8(const void* x, int dtype, const int8_t* b_codes, 
   if (fuse) {
     const dim3 grid((unsigned)((N + 15) / 16));
 #define BSQ_FUSED(X, T)                                                                                          \
-  hipLaunchKernelGGL((k_gemm_int8_few<X, T, 1, true>), grid, dim3(kFThreads), 0, bsqh::as_stream(stream),        \
+  hipLaunchKernelGGL((k_gemm_int8_few<X, T, 1, true>), grid, dim3(64 * few_waves(true)), 0, bsqh::as_stream(stream),        \
                      static_cast<const X*>(x), static_cast<const float*>(nullptr), b_codes, b_scales, bias, (int)M, \
                      (int)N, (int)K, static_cast<T*>(out))
     if (dtype == BSQ_BF16 && out_dtype == BSQ_BF16) BSQ_FUSED(uint16_t, uint16_t);
