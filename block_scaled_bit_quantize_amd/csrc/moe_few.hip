@@ -670,6 +670,199 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_stream(Product a) {
   }
 }
 
+// ---------------------------------------------------------------- few pairs
+// W2 and the weighted sum in one launch where all pairs fit the 16 columns of a
+// matrix instruction (one token with its 8 experts, two with theirs): every
+// pair's activations lie in a column, each expert's weights are multiplied by
+// all of them, and a column keeps the sums of its own expert. A workgroup owns
+// 16 outputs of every token and streams those rows of all experts that occur,
+// so a token's experts meet in it, in slot order, and nothing is left to another
+// launch. A wave has one or two spans of K, its activations stay in registers;
+// where K has fewer spans than there are waves, groups of waves take the
+// experts in turn. One token of 4096 x 1536, top 8: W2SUM us against 14 for W2
+// and 4 for the sum.
+struct SmallPlace {  // a span of 16 weight rows; as Place
+  u32x4 codes[2][64];
+  uint32_t scales[128];
+};
+
+template <typename T, int S, bool EVEN>
+__global__ __launch_bounds__(kThreads, 2) void k_moe_last(Product a, const float* __restrict__ weights,
+                                                         T* __restrict__ y) {
+  constexpr int NT = 2, R = 6;
+  constexpr int LOADS = EVEN ? 3 : 4;  // of a span
+  __shared__ RouteLds lds;
+  __shared__ float part[2][kWaves][256];
+  __shared__ float val[256], wlds[16];
+  __shared__ SmallPlace ring[R][kWaves];
+  const int t = threadIdx.x, wave = uniform(t >> 6), lane = t & 63;
+  const int col = lane & 15, grp = lane >> 4;
+  Route route;
+  route.init(a.ids, a.pairs, a.E, lds);
+  const int tiles = a.width / 16;
+  const int tile0 = uniform((int)((int64_t)tiles * blockIdx.x / gridDim.x));
+  const int tile1 = uniform((int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x));
+  if (tile0 == tile1) return;
+  const int nblk = a.K / 16;
+  const int pitch = nblk * 8;
+  const int spans = (nblk + 15) / 16;
+  const int nw = spans < kWaves ? spans : kWaves, groups = kWaves / nw;
+  const int gi = uniform(wave / nw), wi = wave - gi * nw;
+  const int sp0 = uniform(spans * wi / nw), cnt = uniform(spans * (wi + 1) / nw) - sp0;
+  // the bits of `first` that this wave's group takes, from one to the next
+  auto skip = [](uint64_t m, int n) {
+    for (int i = 0; i < n; ++i) m &= m - 1;  // (0 stays 0)
+    return m;
+  };
+  const uint64_t start = gi < groups ? skip(route.first, gi) : 0;
+  auto expert_of = [&](uint64_t rem) { return __builtin_amdgcn_readlane(route.id[0], __ffsll((unsigned long long)rem) - 1); };
+  auto block_of = [&](int span, int piece) {
+    const int b = span * 16 + piece * 2;
+    return EVEN || b < nblk - 2 ? b : nblk - 2;
+  };
+  uint32_t coff[2], piece[2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const int c = b * 8 + (lane >> 3);
+    piece[b] = (lane & 7) ^ (c >> 1 & 7);
+    coff[b] = (uint32_t)c * pitch + (EVEN ? piece[b] * 16 : 0);
+  }
+  const int mine0 = (col >> 3) * 64 + (col & 7) * 8 + (grp ^ (col >> 1 & 7)), mine1 = mine0 ^ 4;
+
+  // the next span to be asked for
+  uint64_t nrem = start;
+  int ntile = tile0, ns = 0;
+  auto fetch = [&](int place) {  // past the last tile: issued all the same (the waits count them), past the end
+    const bool some = ntile < tile1;
+    const int expert = expert_of(nrem), span = sp0 + ns;
+    const int64_t wrow = (int64_t)expert * a.width + (some ? ntile : tile0) * 16;
+    const rsrc_words codes = descriptor(a.codes + wrow * pitch, 16u * pitch);
+    const uint8_t* sbase = a.scales + wrow * nblk;
+    const uint32_t phase = EVEN ? 0u : (uint32_t)((uintptr_t)sbase & 3u);
+    const rsrc_words scales = descriptor(sbase - phase, (phase + 16u * nblk + 3u) & ~3u);
+    const uint32_t at = lds_offset(&ring[place][wave]);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const uint32_t v = EVEN ? coff[b] : coff[b] + (uint32_t)block_of(span, piece[b]) * 8;
+      load_to_lds<16>(codes, some ? v : kPastEnd, EVEN ? span * 128 : 0, at + b * 1024);
+    }
+    if constexpr (EVEN) {
+      load_to_lds<4>(scales, some ? (uint32_t)(lane >> 2) * nblk + (lane & 3) * 4 : kPastEnd, span * 16, at + 2048);
+    } else {
+      const int w0 = block_of(span, 0);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int i = j * 64 + lane;
+        load_to_lds<4>(scales, some && i < 80 ? ((phase + (uint32_t)(i / 5) * nblk + w0) & ~3u) + i % 5 * 4 : kPastEnd, 0,
+                       at + 2048 + j * 256);
+      }
+    }
+    if (++ns == cnt) {
+      ns = 0;
+      nrem = skip(nrem, groups);
+      if (!nrem) nrem = start, ++ntile;
+    }
+  };
+  if (start) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) fetch(i);
+  }
+
+  // this lane's column, and this thread's output in the tile: row 4 (t / 64) + t % 4 of pair t / 4 % 16
+  const int mine = __shfl(route.id[0], col, 64);  // -1 past the last pair
+  const int tp = t >> 2 & 15, te = __shfl(route.id[0], tp, 64);
+  float so = te >= 0 ? a.outer[te] : 0.0f;
+  if (t < 16) wlds[t] = route.id[0] >= 0 ? weights[t] : 0.0f;
+  asm volatile("" : "+v"(so));  // waited for here, not in the stream
+  u32x4 x[S][2][NT][4];
+  Scale sc;
+  {
+    const brsrc_t act = buffer(a.in, (int64_t)a.pairs * a.K * 4);
+    const uint32_t aoff = (uint32_t)((col < a.pairs ? col : 0) * a.K) * 4u;
+    Raw<float> raw[S][2];
+    float mx = 0.0f;
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        raw[s][p] = load_raw<float>(act, aoff, block_of(sp0 + s, 4 * p + grp),
+                                    s < cnt ? (sp0 + s) * 16 + 2 * (4 * p + grp) : nblk, nblk);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) mx = raw_max(raw[s][p], mx);
+    mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+    sc = scale_for(mx);
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) split<float, NT>(raw[s][p], sc.up, x[s][p]);
+  }
+
+  int place = 0, buf = 0;
+#pragma unroll 1
+  for (int tile = tile0; tile < tile1; ++tile) {
+    f32x4 total = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+    for (uint64_t rem = start; rem; rem = skip(rem, groups)) {
+      const int expert = expert_of(rem);
+      f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        if (s < cnt) {
+          wait_loads<(R - 1) * LOADS>();
+          const SmallPlace& pl = ring[place][wave];
+          u32x4 c[2];
+          uint32_t s8[2];
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            c[p] = (&pl.codes[0][0])[p ? mine1 : mine0];
+            if constexpr (EVEN) {
+              s8[p] = reinterpret_cast<const uint16_t*>(pl.scales)[col * 8 + 4 * p + grp];
+            } else {
+              const int w0 = block_of(sp0 + s, 0);
+              const uint32_t at = (uint32_t)(uintptr_t)(a.scales + ((int64_t)expert * a.width + tile * 16 + col) * nblk + w0);
+              const uint8_t* q = reinterpret_cast<const uint8_t*>(pl.scales) + col * 20 + (at & 3u) +
+                                 (block_of(sp0 + s, 4 * p + grp) - w0);
+              s8[p] = (uint32_t)q[0] | (uint32_t)q[1] << 8;
+            }
+          }
+          wait_lds();  // the place may be filled again
+          fetch(place);
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            u32x4 d[4];
+            decode(c[p], s8[p], d);
+            acc = multiply<NT>(d, x[s][p], acc);
+          }
+          place = place == R - 1 ? 0 : place + 1;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) total[i] = mine == expert ? acc[i] : total[i];
+    }
+    *reinterpret_cast<f32x4*>(&part[buf][wave][lane * 4]) = total * sc.down;
+    lds_barrier();
+    if (wave < 4) {
+      float v = part[buf][0][t];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) v += part[buf][w][t];
+      val[t] = v * so;
+      wait_lds();  // the pairs of a row lie in one wave
+      if (tp < a.pairs && tp % a.k == 0) {
+        float sum = 0.0f;
+        for (int j = 0; j < a.k; ++j) sum += wlds[tp + j] * val[t + 4 * j];
+        const int64_t o = (int64_t)(tp / a.k) * a.width + tile * 16 + (t >> 6) * 4 + (t & 3);
+        if constexpr (sizeof(T) == 4) y[o] = sum;
+        else y[o] = (T)(pack_bf16(sum, 0.0f) & 0xFFFFu);
+      }
+    }
+    buf ^= 1;
+  }
+}
+
 // y[t, n..n+3] = weighted sum over the token's valid pairs, in slot order.
 template <typename T>
 __global__ __launch_bounds__(256) void k_moe_sum(const float* __restrict__ z, const int32_t* __restrict__ ids,
@@ -719,6 +912,24 @@ void launch_stream(const Product& a, hipStream_t s) {
   hipLaunchKernelGGL((k_moe_any<T, NT, GLU, 2>), dim3((unsigned)bsqh::device_cus()), dim3(kThreads), 0, s, a);
 }
 
+// W2 and the sum: one launch for up to 16 pairs with K in registers (two spans
+// a wave). Both ways measured: one token LAST1; two tokens LAST2.
+template <typename T>
+bool launch_last(const Product& a, const float* weights, T* y, hipStream_t s) {
+  const int spans = (a.K / 16 + 15) / 16;
+  if (a.pairs > 16 || a.K < 32 || spans > 2 * kWaves) return false;
+  const int tiles = a.width / 16, cus = bsqh::device_cus();
+  const dim3 grid((unsigned)(tiles < cus ? tiles : cus)), block(kThreads);
+  if (a.K % 256 == 0) {
+    if (spans <= kWaves) hipLaunchKernelGGL((k_moe_last<T, 1, true>), grid, block, 0, s, a, weights, y);
+    else hipLaunchKernelGGL((k_moe_last<T, 2, true>), grid, block, 0, s, a, weights, y);
+  } else {
+    if (spans <= kWaves) hipLaunchKernelGGL((k_moe_last<T, 1, false>), grid, block, 0, s, a, weights, y);
+    else hipLaunchKernelGGL((k_moe_last<T, 2, false>), grid, block, 0, s, a, weights, y);
+  }
+  return true;
+}
+
 template <typename T, int NT>
 void launch_layer(const T* x, int64_t tokens, int64_t H, int64_t F, int64_t E, int64_t k, const int32_t* ids,
                   const float* weights, const uint8_t* w13c, const uint8_t* w13s, const float* w13o,
@@ -726,7 +937,9 @@ void launch_layer(const T* x, int64_t tokens, int64_t H, int64_t F, int64_t E, i
                   hipStream_t s) {
   const int pairs = (int)(tokens * k);
   launch_stream<T, NT, true>({x, ids, pairs, (int)k, (int)E, (int)H, (int)F, w13c, w13s, w13o, h}, s);
-  launch_stream<float, 2, false>({h, ids, pairs, (int)k, (int)E, (int)F, (int)H, w2c, w2s, w2o, z}, s);
+  const Product down{h, ids, pairs, (int)k, (int)E, (int)F, (int)H, w2c, w2s, w2o, z};
+  if (launch_last<T>(down, weights, out, s)) return;
+  launch_stream<float, 2, false>(down, s);
   hipLaunchKernelGGL((k_moe_sum<T>), dim3((unsigned)((tokens * (H / 4) + 255) / 256)), dim3(256), 0, s,
                      static_cast<const float*>(z), ids, weights, (int)tokens, (int)k, (int)E, (int)H, out);
 }

@@ -178,6 +178,27 @@ def test_moe_few_one_expert_takes_all(n, dtype):
     moe_case(n, 80, 48, 6, 2, dtype, seed=n, ids=ids)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,k", [(1, 16), (1, 17), (2, 8), (5, 3), (16, 1), (17, 1)])
+@pytest.mark.parametrize("H,F", [(16, 32), (4112, 48), (80, 256), (48, 272), (32, 1536), (64, 2048), (48, 2064),
+                                 (32, 4096), (16, 4112)])
+def test_moe_few_up_to_sixteen_pairs(T, k, H, F, dtype):
+    """At and past 16 pairs, with inner lengths of one to eight spans of 256, of
+    up to sixteen, and beyond; one id in five adds nothing."""
+    rng = np.random.default_rng(T * k + F)
+    E = 20 if H * F < 1 << 17 else 4
+    ids = rng.integers(0, E, (T, k))
+    ids[rng.random((T, k)) < 0.2] = -1
+    moe_case(T, H, F, E, k, dtype, seed=H + F, ids=ids)
+
+
+def test_moe_few_small_repeats_bit_for_bit():
+    _, args = moe_case(2, 528, 400, 16, 4, BF16, seed=8)
+    y = bsq.moe_few_tokens_nvfp4(*args)
+    for _ in range(3):
+        assert torch.equal(y, bsq.moe_few_tokens_nvfp4(*args))
+
+
 def test_moe_few_masked_pairs():
     ids = np.array([[-1, -1, -1], [2, -1, 7], [1 << 30, 0, 6], [6, 6, 6], [-5, 5, 64]])
     y, _ = moe_case(5, 96, 64, 8, 3, F32, seed=3, ids=ids)
