@@ -215,6 +215,14 @@ struct Route {
     if (few) {
       const int v = ids[lane < pairs ? lane : 0];
       id[0] = lane < pairs && v < E ? v : -1;
+      if (pairs <= 16) {  // no loop over experts, whose turns each wait for the one before
+        bool again = id[0] < 0;
+#pragma unroll
+        for (int p = 0; p < 15; ++p) again |= lane > p && id[0] == __builtin_amdgcn_readlane(id[0], p);
+        first = __ballot(!again);
+        slots = __popcll(first);
+        return;
+      }
       for (uint64_t rem = __ballot(id[0] >= 0); rem;) {
         const int p = __ffsll((unsigned long long)rem) - 1;
         const uint64_t m = __ballot(id[0] == __builtin_amdgcn_readlane(id[0], p));
@@ -697,8 +705,6 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_last(Product a, const float
   __shared__ SmallPlace ring[R][kWaves];
   const int t = threadIdx.x, wave = uniform(t >> 6), lane = t & 63;
   const int col = lane & 15, grp = lane >> 4;
-  Route route;
-  route.init(a.ids, a.pairs, a.E, lds);
   const int tiles = a.width / 16;
   const int tile0 = uniform((int)((int64_t)tiles * blockIdx.x / gridDim.x));
   const int tile1 = uniform((int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x));
@@ -709,6 +715,25 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_last(Product a, const float
   const int nw = spans < kWaves ? spans : kWaves, groups = kWaves / nw;
   const int gi = uniform(wave / nw), wi = wave - gi * nw;
   const int sp0 = uniform(spans * wi / nw), cnt = uniform(spans * (wi + 1) / nw) - sp0;
+  auto block_of = [&](int span, int piece) {
+    const int b = span * 16 + piece * 2;
+    return EVEN || b < nblk - 2 ? b : nblk - 2;
+  };
+  // the activations, which wait for no id
+  Raw<float> raw[S][2];
+  {
+    const brsrc_t act = buffer(a.in, (int64_t)a.pairs * a.K * 4);
+    const uint32_t aoff = (uint32_t)((col < a.pairs ? col : 0) * a.K) * 4u;
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        raw[s][p] = load_raw<float>(act, aoff, block_of(sp0 + s, 4 * p + grp),
+                                    s < cnt ? (sp0 + s) * 16 + 2 * (4 * p + grp) : nblk, nblk);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  Route route;
+  route.init(a.ids, a.pairs, a.E, lds);
   // the bits of `first` that this wave's group takes, from one to the next
   auto skip = [](uint64_t m, int n) {
     for (int i = 0; i < n; ++i) m &= m - 1;  // (0 stays 0)
@@ -716,10 +741,6 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_last(Product a, const float
   };
   const uint64_t start = gi < groups ? skip(route.first, gi) : 0;
   auto expert_of = [&](uint64_t rem) { return __builtin_amdgcn_readlane(route.id[0], __ffsll((unsigned long long)rem) - 1); };
-  auto block_of = [&](int span, int piece) {
-    const int b = span * 16 + piece * 2;
-    return EVEN || b < nblk - 2 ? b : nblk - 2;
-  };
   uint32_t coff[2], piece[2];
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
@@ -729,31 +750,38 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_last(Product a, const float
   }
   const int mine0 = (col >> 3) * 64 + (col & 7) * 8 + (grp ^ (col >> 1 & 7)), mine1 = mine0 ^ 4;
 
+  // where the weights of this lane's pair begin (scalar products for every span took longer than the span)
+  const uint64_t e64 = (uint64_t)(route.id[0] < 0 ? 0 : route.id[0]);
+  const uint64_t cbase = (uint64_t)a.codes + e64 * (uint64_t)((uint32_t)a.width * pitch);
+  const uint64_t sbase = (uint64_t)a.scales + e64 * (uint64_t)((uint32_t)a.width * nblk);
+  const uint32_t clo = (uint32_t)cbase, chi = (uint32_t)(cbase >> 32) & 0xFFFFu;
+  const uint32_t slo = (uint32_t)sbase, shi = (uint32_t)(sbase >> 32) & 0xFFFFu;
   // the next span to be asked for
   uint64_t nrem = start;
   int ntile = tile0, ns = 0;
   auto fetch = [&](int place) {  // past the last tile: issued all the same (the waits count them), past the end
     const bool some = ntile < tile1;
-    const int expert = expert_of(nrem), span = sp0 + ns;
-    const int64_t wrow = (int64_t)expert * a.width + (some ? ntile : tile0) * 16;
-    const rsrc_words codes = descriptor(a.codes + wrow * pitch, 16u * pitch);
-    const uint8_t* sbase = a.scales + wrow * nblk;
-    const uint32_t phase = EVEN ? 0u : (uint32_t)((uintptr_t)sbase & 3u);
-    const rsrc_words scales = descriptor(sbase - phase, (phase + 16u * nblk + 3u) & ~3u);
+    const int src = __ffsll((unsigned long long)nrem) - 1, span = sp0 + ns;
+    const uint32_t row0 = (uint32_t)ntile * 16;
+    const rsrc_words codes = {(uint32_t)__builtin_amdgcn_readlane((int)clo, src),
+                              (uint32_t)__builtin_amdgcn_readlane((int)chi, src), (uint32_t)a.width * pitch, 0x00020000u};
+    const uint32_t slow = (uint32_t)__builtin_amdgcn_readlane((int)slo, src), phase = EVEN ? 0u : slow & 3u;
+    const rsrc_words scales = {slow - phase, (uint32_t)__builtin_amdgcn_readlane((int)shi, src),
+                               (phase + (uint32_t)a.width * nblk + 3u) & ~3u, 0x00020000u};
     const uint32_t at = lds_offset(&ring[place][wave]);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const uint32_t v = EVEN ? coff[b] : coff[b] + (uint32_t)block_of(span, piece[b]) * 8;
-      load_to_lds<16>(codes, some ? v : kPastEnd, EVEN ? span * 128 : 0, at + b * 1024);
+      load_to_lds<16>(codes, some ? v : kPastEnd, row0 * pitch + (EVEN ? span * 128 : 0), at + b * 1024);
     }
     if constexpr (EVEN) {
-      load_to_lds<4>(scales, some ? (uint32_t)(lane >> 2) * nblk + (lane & 3) * 4 : kPastEnd, span * 16, at + 2048);
+      load_to_lds<4>(scales, some ? (uint32_t)(lane >> 2) * nblk + (lane & 3) * 4 : kPastEnd, row0 * nblk + span * 16, at + 2048);
     } else {
       const int w0 = block_of(span, 0);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int i = j * 64 + lane;
-        load_to_lds<4>(scales, some && i < 80 ? ((phase + (uint32_t)(i / 5) * nblk + w0) & ~3u) + i % 5 * 4 : kPastEnd, 0,
+        load_to_lds<4>(scales, some && i < 80 ? ((phase + (row0 + i / 5) * nblk + w0) & ~3u) + i % 5 * 4 : kPastEnd, 0,
                        at + 2048 + j * 256);
       }
     }
@@ -773,21 +801,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_last(Product a, const float
   const int tp = t >> 2 & 15, te = __shfl(route.id[0], tp, 64);
   float so = te >= 0 ? a.outer[te] : 0.0f;
   if (t < 16) wlds[t] = route.id[0] >= 0 ? weights[t] : 0.0f;
-  asm volatile("" : "+v"(so));  // waited for here, not in the stream
   u32x4 x[S][2][NT][4];
   Scale sc;
   {
-    const brsrc_t act = buffer(a.in, (int64_t)a.pairs * a.K * 4);
-    const uint32_t aoff = (uint32_t)((col < a.pairs ? col : 0) * a.K) * 4u;
-    Raw<float> raw[S][2];
     float mx = 0.0f;
-#pragma unroll
-    for (int s = 0; s < S; ++s)
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-        raw[s][p] = load_raw<float>(act, aoff, block_of(sp0 + s, 4 * p + grp),
-                                    s < cnt ? (sp0 + s) * 16 + 2 * (4 * p + grp) : nblk, nblk);
-    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int s = 0; s < S; ++s)
 #pragma unroll
@@ -800,6 +817,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_last(Product a, const float
 #pragma unroll
       for (int p = 0; p < 2; ++p) split<float, NT>(raw[s][p], sc.up, x[s][p]);
   }
+  asm volatile("" : "+v"(so));  // waited for here, not in the stream
 
   int place = 0, buf = 0;
 #pragma unroll 1
