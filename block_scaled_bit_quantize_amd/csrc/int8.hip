@@ -354,7 +354,8 @@ __global__ __launch_bounds__(64 * few_waves(FUSED)) void k_gemm_int8_few(
 // (L2 serves twice the bytes with whole lines), 96 KB of them in flight a CU.
 //
 // A stage's rows hold their 16-byte pieces in an order that depends on the row,
-// so that 16 rows at one piece meet 16 different banks. Fragments past K (in a last step that is not whole) are set to zero on the
+// so that 16 rows at one piece meet 16 different banks. Fragments past K (in a
+// last step that is not whole) are set to zero on the
 // weights' side; rows past M or N repeat the last one and are not stored.
 //
 // Weights are the matrix instruction's first operand: a lane then holds four
@@ -378,7 +379,7 @@ __global__ __launch_bounds__(256, 1) void k_gemm_int8(const int8_t* __restrict__
   constexpr int Q = KS / 32;                    // matrix instructions along a step
   constexpr int SLOTS = Q * WN;                 // rows of matrix instructions in a step
   // the output of a wave, 32 WM rows of COLS columns at a time
-  constexpr int COLS = sizeof(T) == 2 || WN == 1 ? 32 * WN : 16 * WN;
+  constexpr int COLS = sizeof(T) == 2 ? 32 * WN : WN % 2 ? 32 : 16 * WN;
   constexpr int PITCH = COLS * (int)sizeof(T) + 16;
   constexpr int OUT = 32 * WM * PITCH;
   __shared__ __attribute__((aligned(16))) uint8_t lds[ST * STAGE > 4 * OUT ? ST * STAGE : 4 * OUT];
@@ -571,18 +572,22 @@ void launch_gemm(const int8_t* a, const float* sa, const int8_t* b, const float*
   // 63 us, 8192 x 1536 x 1536 34 and 35 us, 4096 x 4096 x 4096 74 and 77 us.
   // Where 128 x 128 tiles leave three CUs of four idle, 64 x 64 ones: 128 x 2048
   // x 7168 30 and 23 us, 256 x 4096 x 4096 21 and 17 us (64 tiles of 128 x 128;
-  // with 128 of them, 512 x 4096 x 4096, 23 and 25 us).
+  // with 128 of them, 512 x 4096 x 4096, 23 and 25 us). Where 128 x 128 tiles
+  // are a few more than the CUs, 192 x 128 ones that are not: 384 x 12288 x 4096
+  // 39 and 31 us, 3000 x 1536 x 4096 34 and 31 us, 1001 x 4099 x 1536 21 and 19 us.
   const int64_t cus = bsqh::device_cus();
   const int64_t big = ((M + 255) / 256) * ((N + 255) / 256), small = ((M + 127) / 128) * ((N + 127) / 128);
+  const int64_t mid = ((M + 191) / 192) * ((N + 127) / 128);
   const double tb = 4.0 * (double)((big + cus - 1) / cus);
   const double ts = small <= cus ? 1.15 : 2.1 * (double)((small + 2 * cus - 1) / (2 * cus));
-#define BSQ_G(W, KS, ST, TILES)                                                                                    \
-  hipLaunchKernelGGL((k_gemm_int8<T, W, W, KS, ST>), dim3((unsigned)(TILES)), dim3(256), 0, s, a, sa, b, sb, bias, M, \
+#define BSQ_G(WM, WN, KS, ST, TILES)                                                                                \
+  hipLaunchKernelGGL((k_gemm_int8<T, WM, WN, KS, ST>), dim3((unsigned)(TILES)), dim3(256), 0, s, a, sa, b, sb, bias, M, \
                      (int)N, (int)K, out)
-  if (4 * small <= cus) BSQ_G(1, 128, 4, ((M + 63) / 64) * ((N + 63) / 64));
-  else if (tb <= ts) BSQ_G(4, 64, 4, big);
-  else if (small <= cus) BSQ_G(2, 128, 3, small);  // one workgroup a CU: more in flight each
-  else BSQ_G(2, 128, 2, small);                    // two a CU
+  if (4 * small <= cus) BSQ_G(1, 1, 128, 4, ((M + 63) / 64) * ((N + 63) / 64));
+  else if (small <= cus) BSQ_G(2, 2, 128, 3, small);  // one workgroup a CU: more in flight each
+  else if (mid <= cus) BSQ_G(3, 2, 128, 3, mid);
+  else if (tb <= ts) BSQ_G(4, 4, 64, 4, big);
+  else BSQ_G(2, 2, 128, 2, small);                    // two a CU
 #undef BSQ_G
 }
 

@@ -407,3 +407,9 @@ def test_moe_few_skewed_experts():
     ids = np.stack([rng.choice(40, size=6, replace=False, p=(lambda p: p / p.sum())(np.arange(1, 41) ** -1.5))
                     for _ in range(150)])
     moe_case(150, 96, 80, 40, 6, BF16, seed=4, ids=ids)
+
+
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+@pytest.mark.parametrize("M,N,K", [(1540, 2570, 48), (1001, 4099, 144), (385, 12160, 272), (4600, 900, 1040)])
+def test_gemm_int8_a_few_more_tiles_than_cus(M, N, K, out_dtype):
+    int8_case(M, N, K, out_dtype, bias=K > 200, seed=M + K)
