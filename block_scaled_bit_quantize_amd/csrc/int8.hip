@@ -644,8 +644,13 @@ extern "C" int bsq_gemm_int8(const int8_t* a_codes, const float* a_scales, const
   return run_gemm(a_codes, a_scales, b_codes, b_scales, bias, M, N, K, out, out_dtype, stream);
 }
 
+// Whether the workgroups quantize the activations themselves: one launch, and no workspace.
+static bool fused(int64_t M, int64_t K, int64_t bytes) {
+  return M <= 16 && M * K <= kFuseCodes && M * K * bytes <= kFuseBytes;
+}
+
 extern "C" size_t bsq_linear_int8_workspace(int64_t M, int64_t K) {
-  if (M <= 0 || K <= 0) return 0;
+  if (M <= 0 || K <= 0 || fused(M, K, 4)) return 0;
   return (size_t)M * (size_t)K + ((size_t)M * 4 + 15) / 16 * 16;
 }
 
@@ -657,14 +662,13 @@ extern "C" int bsq_linear_int8(const void* x, int dtype, const int8_t* b_codes, 
   if (st != BSQ_OK) return st;
   BSQ_REQUIRE(K <= 32768, BSQ_E_SHAPE);
   if (M == 0 || N == 0) return BSQ_OK;
-  BSQ_REQUIRE(x && b_codes && b_scales && out && ws, BSQ_E_NULL);
+  const size_t need = bsq_linear_int8_workspace(M, K);
+  BSQ_REQUIRE(x && b_codes && b_scales && out && (ws || need == 0), BSQ_E_NULL);
   BSQ_REQUIRE(bsqh::aligned16(x) && bsqh::aligned16(b_codes) && bsqh::aligned16(ws) && out_aligned(out, out_dtype) &&
                   (((uintptr_t)b_scales | (uintptr_t)bias) & 3) == 0,
               BSQ_E_ALIGN);
-  BSQ_REQUIRE(ws_bytes >= bsq_linear_int8_workspace(M, K), BSQ_E_WORKSPACE);
-  // One launch where the workgroups can quantize the few activations themselves.
-  const int64_t fuse = (M * K <= kFuseCodes && M * K * (dtype == BSQ_F32 ? 4 : 2) <= kFuseBytes && M <= 16) ? 1 : 0;
-  if (fuse) {
+  BSQ_REQUIRE(ws_bytes >= need, BSQ_E_WORKSPACE);
+  if (fused(M, K, dtype == BSQ_F32 ? 4 : 2)) {
     const dim3 grid((unsigned)((N + 15) / 16));
 #define BSQ_FUSED(X, T)                                                                                          \
   hipLaunchKernelGGL((k_gemm_int8_few<X, T, 1, true>), grid, dim3(64 * few_waves(true)), 0, bsqh::as_stream(stream),        \

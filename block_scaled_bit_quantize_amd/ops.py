@@ -505,9 +505,9 @@ def linear_int8(x, b_codes, b_scales, bias=None, out_dtype=None):
     _need(out_dtype in _OUT, "out_dtype must be float32 or bfloat16")
     out = torch.empty((M, N), dtype=out_dtype, device=x.device)
     wsb = lib.bsq_linear_int8_workspace(M, K)
-    ws = _ws(wsb, x.device)
+    ws = _ws(wsb, x.device) if wsb else None
     check(lib.bsq_linear_int8(x.data_ptr(), dt, b_codes.data_ptr(), b_scales.data_ptr(), _ptr(bias), M, N, K,
-                              out.data_ptr(), _OUT[out_dtype], ws.data_ptr(), wsb, _stream()), "bsq_linear_int8")
+                              out.data_ptr(), _OUT[out_dtype], _ptr(ws), wsb, _stream()), "bsq_linear_int8")
     return out
 
 

@@ -106,8 +106,9 @@ def test_int8(lib):
     assert g(a5=0, a0=None) == OK
     assert g(a6=0, a2=None) == OK
     # x, dtype, b, sb, bias, M, N, K, out, out_dtype, ws, bytes, stream
-    need = lib.bsq_linear_int8_workspace(4, 32)
-    l = caller(lib.bsq_linear_int8, [FAKE, 1, FAKE, FAKE, None, 4, 8, 32, FAKE, 1, FAKE, need, None])
+    need = lib.bsq_linear_int8_workspace(20, 32)
+    assert need > 0 and lib.bsq_linear_int8_workspace(1, 4096) == 0
+    l = caller(lib.bsq_linear_int8, [FAKE, 1, FAKE, FAKE, None, 20, 8, 32, FAKE, 1, FAKE, need, None])
     assert l(a1=2) == E_DTYPE
     assert l(a9=2) == E_DTYPE
     assert l(a7=32784) == E_SHAPE
