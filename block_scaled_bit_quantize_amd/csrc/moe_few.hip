@@ -19,7 +19,7 @@
 // loads in flight. 64 tokens, top 8 of 64 experts of 1536, hidden 4096: W13
 // 92 us (453 MB, 4.9 TB/s; 84 us with the barrier and the stores left out), W2
 // 60 us (226 MB, 3.8 TB/s; 47 us with nothing but the stream), where plain
-// reads reach 5.9 TB/s. One token: 17 and 14 us, of which the first bytes'
+// reads reach 5.9 TB/s. One token: 16 and 14 us, of which the first bytes'
 // way (ids, expert, descriptor, latency) is about 5 each.
 //
 // Weights are decoded to fp16 exactly (an E2M1 value times its E4M3 scale has
@@ -35,7 +35,7 @@
 // Which experts occur is read from the ids by every workgroup itself, so the
 // layer is three launches: W13 with SwiGLU, W2 into one row per (token, slot)
 // pair, and the sum over a token's pairs in slot order (no atomics: the same
-// bits every time).
+// bits every time). Up to 16 pairs W2 and the sum are one (k_moe_last).
 #include "bsq_device.h"
 #include "bsq_internal.h"
 
@@ -321,14 +321,16 @@ struct Route {
 
 // ---------------------------------------------------------------- the stream
 struct Product {
-  const void* in;         // activations: row of pair p is (GLU ? p / k : p)
+  const void* in;         // activations: row of pair p is p / share
   const int32_t* ids;
   int pairs, k, E, K;
   int width;              // outputs of a pair
+  int share;              // k for W13, 1 for W2
   const uint8_t* codes;
   const uint8_t* scales;
   const float* outer;
   float* out;             // [pairs, width]
+  int span0, spans;       // k_moe_stream: the part of K, in spans of 256 values
 };
 
 // The end of a tile: the waves' partial sums of 16 x 16 outputs meet in LDS and
@@ -369,8 +371,8 @@ __device__ __forceinline__ void finish(const Product& a, float (&part)[kWaves][R
   }
 }
 
-// Any K: weights and activations straight to registers, read again for every
-// tile (rows too long for k_moe_stream's registers, and rows of one block).
+// Rows of one block (K = 16), which k_moe_stream's loads do not take: weights
+// and activations straight to registers, read again for every tile.
 template <typename T, int NT, bool GLU, int RT>
 __global__ __launch_bounds__(kThreads, 2) void k_moe_any(Product a) {
   constexpr int OUT = GLU ? RT * 8 : RT * 16;  // outputs of a tile
@@ -388,7 +390,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_any(Product a) {
   const int steps = (nblk + 7) / 8;
   const int st0 = steps * wave / kWaves, st1 = steps * (wave + 1) / kWaves;
   const int rows = GLU ? 2 * a.width : a.width;
-  const brsrc_t act = buffer(a.in, (int64_t)(GLU ? a.pairs / a.k : a.pairs) * a.K * (int)sizeof(T));
+  const brsrc_t act = buffer(a.in, (int64_t)(a.pairs / a.share) * a.K * (int)sizeof(T));
   int buf = 0;
   while (u < u1) {
     const int at = u / tiles, tile0 = u - at * tiles;
@@ -403,7 +405,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_any(Product a) {
     const float so = a.outer[expert];
     {
       const int mine = lds.list[mt0 + col < np ? mt0 + col : mt0];
-      const uint32_t aoff = (uint32_t)((GLU ? mine / a.k : mine) * a.K) * (uint32_t)sizeof(T);
+      const uint32_t aoff = (uint32_t)(mine / a.share * a.K) * (uint32_t)sizeof(T);
       auto raw_at = [&](int st) {
         const int b = st * 8 + grp * 2;
         return load_raw<T>(act, aoff, b, b, nblk);
@@ -512,11 +514,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_stream(Product a) {
   const int u1 = uniform((int)(units * (blockIdx.x + 1) / gridDim.x));
   const int nblk = a.K / 16;
   const int pitch = nblk * 8;  // bytes of a row's codes
-  const int spans = (nblk + 15) / 16;
-  const int sp0 = spans * wave / kWaves, cnt = spans * (wave + 1) / kWaves - sp0;
+  const int sp0 = a.span0 + a.spans * wave / kWaves, cnt = a.span0 + a.spans * (wave + 1) / kWaves - sp0;
   const int rows = GLU ? 2 * a.width : a.width;
   const int up = GLU ? a.width : 16;  // from a row of the first 16-row tile to the second's
-  const brsrc_t act = buffer(a.in, (int64_t)(GLU ? a.pairs / a.k : a.pairs) * a.K * (int)sizeof(T));
+  const brsrc_t act = buffer(a.in, (int64_t)(a.pairs / a.share) * a.K * (int)sizeof(T));
   // In a last span that is not whole, pieces past the end move back to the
   // row's last two blocks; the activations are zero where another lane has one.
   auto block_of = [&](int span, int piece) {
@@ -585,7 +586,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_stream(Product a) {
     {
       // lanes past the last pair repeat one and are not stored
       const int pair = lds.list[mt0 + col < np ? mt0 + col : mt0];
-      const uint32_t aoff = (uint32_t)((GLU ? pair / a.k : pair) * a.K) * (uint32_t)sizeof(T);
+      const uint32_t aoff = (uint32_t)(pair / a.share * a.K) * (uint32_t)sizeof(T);
       u32x4 x[S][2][NT][4];
       Scale sc;
       {
@@ -687,8 +688,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_stream(Product a) {
 // so a token's experts meet in it, in slot order, and nothing is left to another
 // launch. A wave has one or two spans of K, its activations stay in registers;
 // where K has fewer spans than there are waves, groups of waves take the
-// experts in turn. One token of 4096 x 1536, top 8: W2SUM us against 14 for W2
-// and 4 for the sum.
+// experts in turn. One token of 4096 x 1536, top 8: 14 us against 14 for W2 and 4 for
+// the sum; 10 of them are latency (28 MB take 5).
 struct SmallPlace {  // a span of 16 weight rows; as Place
   u32x4 codes[2][64];
   uint32_t scales[128];
@@ -881,10 +882,24 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_last(Product a, const float
   }
 }
 
-// y[t, n..n+3] = weighted sum over the token's valid pairs, in slot order.
+// h[p, f] = silu(gate) * up from the parts' sums [parts, pairs, 2 F] of W13.
+// (Rows of pairs without an expert hold anything, and are read by nobody.)
+__global__ __launch_bounds__(256) void k_moe_act(const float* __restrict__ raw, int64_t pairs, int F, int parts,
+                                                 float* __restrict__ h) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= pairs * F) return;
+  const float* at = raw + id / F * 2 * F + id % F;
+  float g = 0.0f, u = 0.0f;
+  for (int c = 0; c < parts; ++c) g += at[c * pairs * 2 * F], u += at[c * pairs * 2 * F + F];
+  h[id] = g / (1.0f + expf(-g)) * u;
+}
+
+// y[t, n..n+3] = weighted sum over the token's valid pairs, in slot order, of
+// the parts' sums [parts, tokens k, H].
 template <typename T>
 __global__ __launch_bounds__(256) void k_moe_sum(const float* __restrict__ z, const int32_t* __restrict__ ids,
-                                                 const float* __restrict__ weights, int tokens, int k, int E, int H, T* __restrict__ y) {
+                                                 const float* __restrict__ weights, int tokens, int k, int E, int H,
+                                                 int parts, T* __restrict__ y) {
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int per = H / 4;
   if (id >= (int64_t)tokens * per) return;
@@ -900,6 +915,8 @@ __global__ __launch_bounds__(256) void k_moe_sum(const float* __restrict__ z, co
       const int e = ids[t * k + q];
       w[j] = weights[t * k + q];
       v[j] = *reinterpret_cast<const f32x4*>(zt + (int64_t)q * H);
+      for (int c = 1; c < parts; ++c)
+        v[j] += *reinterpret_cast<const f32x4*>(zt + ((int64_t)c * tokens * k + q) * H);
       if (j0 + j >= k || e < 0 || e >= E) v[j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f}, w[j] = 0.0f;
     }
 #pragma unroll
@@ -913,25 +930,42 @@ __global__ __launch_bounds__(256) void k_moe_sum(const float* __restrict__ z, co
 }
 
 // Registers hold up to 128 words of activations: 32 for each span of a wave
-// (eight waves to K) and term. Longer rows are read again for every tile.
-template <typename T, int NT, bool GLU, bool EVEN>
-bool launch_stream_k(const Product& a, hipStream_t s) {
-  const int spans = (a.K / 16 + 15) / 16;
+// (eight waves to K) and term. Longer K goes in parts, each a product of its
+// own, whose sums meet in k_moe_act and k_moe_sum (16 tokens, 2 of 4 experts of
+// 10240 x 10240: 210 us, where reading the activations again for every tile
+// took 465; 2 of 8 experts of 4096 x 14336 195 and 289 us).
+int parts_of(int64_t K, int NT) { return (int)(((K + 255) / 256 * NT + 31) / 32); }
+
+template <typename T, int NT, bool GLU, int S>
+void launch_stream(const Product& a, hipStream_t s) {
   const dim3 grid((unsigned)bsqh::device_cus()), block(kThreads);
-  if (spans * NT <= 16) hipLaunchKernelGGL((k_moe_stream<T, NT, GLU, 2 / NT, EVEN>), grid, block, 0, s, a);
-  else if (spans * NT <= 32) hipLaunchKernelGGL((k_moe_stream<T, NT, GLU, 4 / NT, EVEN>), grid, block, 0, s, a);
-  else return false;
-  return true;
+  if (a.K % 256 == 0) hipLaunchKernelGGL((k_moe_stream<T, NT, GLU, S, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_moe_stream<T, NT, GLU, S, false>), grid, block, 0, s, a);
 }
 template <typename T, int NT, bool GLU>
-void launch_stream(const Product& a, hipStream_t s) {
-  if (a.K >= 32 && (a.K % 256 == 0 ? launch_stream_k<T, NT, GLU, true>(a, s) : launch_stream_k<T, NT, GLU, false>(a, s)))
-    return;
-  hipLaunchKernelGGL((k_moe_any<T, NT, GLU, 2>), dim3((unsigned)bsqh::device_cus()), dim3(kThreads), 0, s, a);
+void launch_product(Product a, hipStream_t s) {
+  a.span0 = 0;
+  a.spans = (a.K + 255) / 256;
+  if (a.K < 32)
+    hipLaunchKernelGGL((k_moe_any<T, NT, GLU, 2>), dim3((unsigned)bsqh::device_cus()), dim3(kThreads), 0, s, a);
+  else if (a.spans * NT <= 16) launch_stream<T, NT, GLU, 2 / NT>(a, s);
+  else launch_stream<T, NT, GLU, 4 / NT>(a, s);
+}
+// The part sums [parts, pairs, width], from a.out on.
+template <typename T, int NT>
+void launch_parts(Product a, int parts, hipStream_t s) {
+  const int spans = (a.K + 255) / 256;
+  for (int c = 0; c < parts; ++c) {
+    a.span0 = (int)((int64_t)spans * c / parts);
+    a.spans = (int)((int64_t)spans * (c + 1) / parts) - a.span0;
+    launch_stream<T, NT, false, 4 / NT>(a, s);
+    a.out += (int64_t)a.pairs * a.width;
+  }
 }
 
 // W2 and the sum: one launch for up to 16 pairs with K in registers (two spans
-// a wave). Both ways measured: one token LAST1; two tokens LAST2.
+// a wave). Whole layers this way and with the sum apart: one token of 4096 x 1536,
+// top 8, 31 and 34 us, two 49 and 52 us; two of 7168 x 2048 90 and 92 us.
 template <typename T>
 bool launch_last(const Product& a, const float* weights, T* y, hipStream_t s) {
   const int spans = (a.K / 16 + 15) / 16;
@@ -951,15 +985,26 @@ bool launch_last(const Product& a, const float* weights, T* y, hipStream_t s) {
 template <typename T, int NT>
 void launch_layer(const T* x, int64_t tokens, int64_t H, int64_t F, int64_t E, int64_t k, const int32_t* ids,
                   const float* weights, const uint8_t* w13c, const uint8_t* w13s, const float* w13o,
-                  const uint8_t* w2c, const uint8_t* w2s, const float* w2o, T* out, float* h, float* z,
-                  hipStream_t s) {
+                  const uint8_t* w2c, const uint8_t* w2s, const float* w2o, T* out, float* ws, hipStream_t s) {
   const int pairs = (int)(tokens * k);
-  launch_stream<T, NT, true>({x, ids, pairs, (int)k, (int)E, (int)H, (int)F, w13c, w13s, w13o, h}, s);
-  const Product down{h, ids, pairs, (int)k, (int)E, (int)F, (int)H, w2c, w2s, w2o, z};
+  const int n13 = parts_of(H, NT), n2 = parts_of(F, 2);
+  float* h = ws;                          // [pairs, F]
+  float* z = h + tokens * k * F;          // [n2, pairs, H]
+  float* raw = z + n2 * tokens * k * H;   // [n13, pairs, 2 F] where n13 > 1
+  const int w = (int)F, w2 = 2 * (int)F;
+  if (n13 == 1) {
+    launch_product<T, NT, true>({x, ids, pairs, (int)k, (int)E, (int)H, w, (int)k, w13c, w13s, w13o, h, 0, 0}, s);
+  } else {
+    launch_parts<T, NT>({x, ids, pairs, (int)k, (int)E, (int)H, w2, (int)k, w13c, w13s, w13o, raw, 0, 0}, n13, s);
+    hipLaunchKernelGGL(k_moe_act, dim3((unsigned)((tokens * k * F + 255) / 256)), dim3(256), 0, s,
+                       static_cast<const float*>(raw), tokens * k, (int)F, n13, h);
+  }
+  const Product down{h, ids, pairs, (int)k, (int)E, (int)F, (int)H, 1, w2c, w2s, w2o, z, 0, 0};
   if (launch_last<T>(down, weights, out, s)) return;
-  launch_stream<float, 2, false>(down, s);
+  if (n2 == 1) launch_product<float, 2, false>(down, s);
+  else launch_parts<float, 2>(down, n2, s);
   hipLaunchKernelGGL((k_moe_sum<T>), dim3((unsigned)((tokens * (H / 4) + 255) / 256)), dim3(256), 0, s,
-                     static_cast<const float*>(z), ids, weights, (int)tokens, (int)k, (int)E, (int)H, out);
+                     static_cast<const float*>(z), ids, weights, (int)tokens, (int)k, (int)E, (int)H, n2, out);
 }
 
 bool shape_ok(int64_t tokens, int64_t hidden, int64_t ffn, int64_t E, int64_t k) {
@@ -971,7 +1016,8 @@ bool shape_ok(int64_t tokens, int64_t hidden, int64_t ffn, int64_t E, int64_t k)
 
 extern "C" size_t bsq_moe_few_nvfp4_workspace(int64_t tokens, int64_t hidden, int64_t ffn, int64_t E, int64_t k) {
   if (!shape_ok(tokens, hidden, ffn, E, k)) return 0;
-  return (size_t)(tokens * k) * (size_t)(hidden + ffn) * 4;
+  const int n13 = parts_of(hidden, 2), n2 = parts_of(ffn, 2);  // of float32 x; of bfloat16 n13 may be less
+  return (size_t)(tokens * k) * (size_t)(ffn + n2 * hidden + (n13 > 1 ? n13 * 2 * ffn : 0)) * 4;
 }
 
 extern "C" int bsq_moe_few_nvfp4(const void* x, int dtype, int64_t tokens, int64_t hidden, int64_t ffn, int64_t E,
@@ -992,14 +1038,13 @@ extern "C" int bsq_moe_few_nvfp4(const void* x, int dtype, int64_t tokens, int64
               BSQ_E_ALIGN);
   BSQ_REQUIRE(ws_bytes >= bsq_moe_few_nvfp4_workspace(tokens, hidden, ffn, E, k), BSQ_E_WORKSPACE);
   hipStream_t s = bsqh::as_stream(stream);
-  float* h = static_cast<float*>(ws);  // [pairs, ffn]
-  float* z = h + tokens * k * ffn;     // [pairs, hidden]
+  float* sums = static_cast<float*>(ws);
   if (dtype == BSQ_BF16)
     launch_layer<uint16_t, 1>(static_cast<const uint16_t*>(x), tokens, hidden, ffn, E, k, topk_ids, topk_weights,
                               w13_codes, w13_scales, w13_outer, w2_codes, w2_scales, w2_outer,
-                              static_cast<uint16_t*>(out), h, z, s);
+                              static_cast<uint16_t*>(out), sums, s);
   else
     launch_layer<float, 2>(static_cast<const float*>(x), tokens, hidden, ffn, E, k, topk_ids, topk_weights, w13_codes,
-                           w13_scales, w13_outer, w2_codes, w2_scales, w2_outer, static_cast<float*>(out), h, z, s);
+                           w13_scales, w13_outer, w2_codes, w2_scales, w2_outer, static_cast<float*>(out), sums, s);
   return bsqh::launch_status();
 }

@@ -433,7 +433,7 @@ int bsq_moe_gate_backward(const float* dweights, const float* weights, const int
  * activations unquantized:
  *   out[t] = sum_j topk_weights[t, j] W2_e (silu(G) * U),  (G; U) = W13_e x[t],
  *   e = topk_ids[t, j];  silu(g) = g / (1 + e^-g).
- * Only the experts that occur are read, each once.
+ * Only the experts that occur are read, each once for every 16 pairs that chose it.
  * x, out   [tokens, hidden] of `dtype` (F32 or BF16).
  * topk_ids int32 [tokens, k]; an id outside [0, E) (as bsq_moe_gate's -1) adds
  *          nothing, a token without a valid id gets zeros. topk_weights FP32.

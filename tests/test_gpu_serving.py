@@ -192,6 +192,13 @@ def test_moe_few_up_to_sixteen_pairs(T, k, H, F, dtype):
     moe_case(T, H, F, E, k, dtype, seed=H + F, ids=ids)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,H,F,E,k", [(2, 4112, 48, 3, 2), (9, 8208, 32, 4, 2), (1, 32, 8240, 4, 3), (20, 48, 4352, 3, 1),
+                                       (40, 8448, 4128, 2, 1), (3, 16, 12304, 5, 2), (18, 16640, 16, 4, 1)])
+def test_moe_few_rows_longer_than_the_registers(T, H, F, E, k, dtype):
+    moe_case(T, H, F, E, k, dtype, seed=H + F)
+
+
 def test_moe_few_small_repeats_bit_for_bit():
     _, args = moe_case(2, 528, 400, 16, 4, BF16, seed=8)
     y = bsq.moe_few_tokens_nvfp4(*args)
