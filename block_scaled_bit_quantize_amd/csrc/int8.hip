@@ -646,7 +646,7 @@ extern "C" int bsq_gemm_int8(const int8_t* a_codes, const float* a_scales, const
 
 // Whether the workgroups quantize the activations themselves: one launch, and no workspace.
 static bool fused(int64_t M, int64_t K, int64_t bytes) {
-  return M <= 16 && M * K <= kFuseCodes && M * K * bytes <= kFuseBytes;
+  return M <= 16 && K <= kFuseCodes && M * K <= kFuseCodes && M * K * bytes <= kFuseBytes;
 }
 
 extern "C" size_t bsq_linear_int8_workspace(int64_t M, int64_t K) {

@@ -118,3 +118,10 @@ def test_int8(lib):
         assert l(**{f"a{i}": FAKE + 8}) == E_ALIGN
     assert l(a11=need - 1) == E_WORKSPACE
     assert l(a5=0, a0=None) == OK
+
+
+def test_workspace_queries_of_impossible_sizes(lib):
+    assert lib.bsq_linear_int8_workspace(-1, 32) == 0
+    assert lib.bsq_linear_int8_workspace(16, 1 << 40) >= 16 << 40
+    assert lib.bsq_moe_few_nvfp4_workspace(4, 32768, 32768, 8, 2) > lib.bsq_moe_few_nvfp4_workspace(4, 4096, 4096, 8, 2)
+    assert lib.bsq_moe_few_nvfp4_workspace(4, 32784, 64, 8, 2) == 0
