@@ -9,6 +9,7 @@
 // output type.
 #include "bsq_device.h"
 #include "bsq_internal.h"
+#include "bsq_lds.h"
 
 using namespace bsqd;
 
@@ -155,34 +156,6 @@ int check_quant(const void* x, int dtype, int64_t rows, int64_t cols, const void
   return BSQ_OK;
 }
 
-// ---------------------------------------------------------------- loads to LDS
-// Loads that go straight to LDS, as asm because the waits are counted here: the
-// compiler would have to take every LDS read for one that may meet the newest
-// load.
-typedef uint32_t rsrc_words __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ rsrc_words descriptor(const void* p, uint32_t bytes) {
-  const uint64_t at = (uint64_t)p;
-  return (rsrc_words){(uint32_t)uniform((int)(uint32_t)at), (uint32_t)uniform((int)(uint32_t)(at >> 32)) & 0xFFFFu,
-                      (uint32_t)uniform((int)bytes), 0x00020000u};
-}
-// 64 lanes of 16 bytes: lane l's at lds + 16 l. There is no register to be
-// overwritten in flight; the address register is read at issue, and m0 is one
-// that the compiler sets anew before each use of its own.
-__device__ __forceinline__ void load_to_lds(rsrc_words rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff), "s"(rsrc),
-               "s"(soff)
-               : "memory");
-}
-template <int N>
-__device__ __forceinline__ void wait_loads() {  // all but the N youngest
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-__device__ __forceinline__ uint32_t lds_offset(const void* p) {
-  return (uint32_t)uniform((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p);
-}
-
 // ---------------------------------------------------------------- epilogue
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
@@ -251,10 +224,10 @@ __global__ __launch_bounds__(64 * few_waves(FUSED)) void k_gemm_int8_few(
   auto fetch = [&](int st, int place) {  // past the last step: issued all the same (the waits count them), past the end
     const uint32_t k = st < st1 ? (uint32_t)st * 128 : kPastEnd, at = base + place * (LOADS * 1024);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) load_to_lds(db, vb[i] + k, 0, at + i * 1024);
+    for (int i = 0; i < 2; ++i) load_to_lds<16>(db, vb[i] + k, 0, at + i * 1024);
     if constexpr (!FUSED) {
 #pragma unroll
-      for (int i = 0; i < 2 * MT; ++i) load_to_lds(da, va[i] + k, 0, at + (2 + i) * 1024);
+      for (int i = 0; i < 2 * MT; ++i) load_to_lds<16>(da, va[i] + k, 0, at + (2 + i) * 1024);
     }
   };
   if constexpr (FUSED) {
@@ -262,7 +235,7 @@ __global__ __launch_bounds__(64 * few_waves(FUSED)) void k_gemm_int8_few(
 #pragma unroll
     for (int i = 0; i < XLOADS; ++i) {
       const int c = i * kFWaves + wave;
-      load_to_lds(da, c * 1024 + lane * 16, 0, at + c * 1024);
+      load_to_lds<16>(da, c * 1024 + lane * 16, 0, at + c * 1024);
     }
   }
 #pragma unroll
@@ -429,11 +402,11 @@ __global__ __launch_bounds__(256, 1) void k_gemm_int8(const int8_t* __restrict__
     if (i < LA) {
       rsrc_words d = ra;
       if (step >= steps) d[2] = 0u;
-      load_to_lds(d, va[i < LA ? i : 0] + step * KS, 0, base + stage * STAGE + (wave * LA + i) * 1024);
+      load_to_lds<16>(d, va[i < LA ? i : 0] + step * KS, 0, base + stage * STAGE + (wave * LA + i) * 1024);
     } else {
       rsrc_words d = rb;
       if (step >= steps) d[2] = 0u;
-      load_to_lds(d, vb[i < LA ? 0 : i - LA] + step * KS, 0, base + stage * STAGE + TM * KS + (wave * LB + i - LA) * 1024);
+      load_to_lds<16>(d, vb[i < LA ? 0 : i - LA] + step * KS, 0, base + stage * STAGE + TM * KS + (wave * LB + i - LA) * 1024);
     }
   };
   const int wm = wave >> 1, wn = wave & 1;

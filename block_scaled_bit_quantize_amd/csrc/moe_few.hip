@@ -38,6 +38,7 @@
 // bits every time). Up to 16 pairs W2 and the sum are one (k_moe_last).
 #include "bsq_device.h"
 #include "bsq_internal.h"
+#include "bsq_lds.h"
 
 using namespace bsqd;
 
@@ -60,14 +61,6 @@ constexpr int kMaxExperts = 1024;
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
 }
-
-// A value that is the same in every lane, told to the compiler (it goes to a
-// scalar register; descriptors and loop bounds made of it need no lane loops).
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-
-// Workgroup barrier that completes this wave's LDS operations and leaves its
-// loads in flight.
-__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // Operands are read through buffer descriptors: a 32-bit offset per lane, the
 // tile's and step's offset in a scalar register.
@@ -449,39 +442,6 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_any(Product a) {
     }
     lds_barrier();  // the list is rewritten next
   }
-}
-
-// ---------------------------------------------------------------- loads to LDS
-// 64 lanes of SIZE bytes (4 or 16) each: lane l's at lds + l * SIZE. Written as
-// asm because the waits are counted here: the compiler would have to take every
-// LDS read for one that may meet the newest load. There is no register to be
-// overwritten in flight; the address registers are read at issue, and m0 is one
-// that the compiler sets anew before each use of its own.
-typedef uint32_t rsrc_words __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ rsrc_words descriptor(const void* p, uint32_t bytes) {
-  const uint64_t at = (uint64_t)p;
-  return (rsrc_words){(uint32_t)uniform((int)(uint32_t)at), (uint32_t)uniform((int)(uint32_t)(at >> 32)) & 0xFFFFu,
-                      (uint32_t)uniform((int)bytes), 0x00020000u};
-}
-template <int SIZE>
-__device__ __forceinline__ void load_to_lds(rsrc_words rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
-  static_assert(SIZE == 4 || SIZE == 16, "sizes of the instruction");
-  if constexpr (SIZE == 16)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
-                 "s"(rsrc), "s"(soff)
-                 : "memory");
-  else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
-                 "s"(rsrc), "s"(soff)
-                 : "memory");
-}
-template <int N>
-__device__ __forceinline__ void wait_loads() {  // all but the N youngest
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
-__device__ __forceinline__ uint32_t lds_offset(const void* p) {
-  return (uint32_t)uniform((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p);
 }
 
 // One place of a wave's ring: a span (256 values of K, 16 blocks) of 32 weight
