@@ -30,6 +30,20 @@ __device__ __forceinline__ rsrc_words descriptor(const void* p, uint32_t bytes) 
                       (uint32_t)uniform((int)bytes), 0x00020000u};
 }
 
+// Where a lane's load goes. There is nothing to load where `there` is false (the
+// same in every lane) or `mine` is: such a load is issued all the same, for the
+// waits that count it, past the buffer's end. A raw buffer's range check is
+// voff >= bytes - soff, in unsigned 32 bits, so a scalar offset that is itself
+// past the end must not stand there: the difference would wrap and let any lane
+// offset pass.
+constexpr uint32_t kPastEnd = 0x80000000u;  // past every buffer that is read this way
+struct BufferAt {
+  uint32_t voff, soff;
+};
+__host__ __device__ constexpr BufferAt buffer_at(bool there, bool mine, uint32_t voff, uint32_t soff) {
+  return {there && mine ? voff : kPastEnd, there ? soff : 0u};
+}
+
 // 64 lanes of SIZE bytes (4 or 16) each: lane l's at lds + SIZE l.
 template <int SIZE>
 __device__ __forceinline__ void load_to_lds(rsrc_words rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
@@ -42,6 +56,11 @@ __device__ __forceinline__ void load_to_lds(rsrc_words rsrc, uint32_t voff, uint
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
                  "s"(rsrc), "s"(soff)
                  : "memory");
+}
+
+template <int SIZE>
+__device__ __forceinline__ void load_to_lds(rsrc_words rsrc, BufferAt at, uint32_t lds) {
+  load_to_lds<SIZE>(rsrc, at.voff, at.soff, lds);
 }
 
 template <int N>

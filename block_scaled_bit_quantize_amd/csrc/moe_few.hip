@@ -67,7 +67,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 __device__ __forceinline__ brsrc_t buffer(const void* p, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, 0x00020000);
 }
-constexpr uint32_t kPastEnd = 0x80000000u;  // past every buffer here: reads as zero
 
 // ---------------------------------------------------------------- operands
 // A step is 128 values of K: 8 blocks. Lane (c, g) = (lane % 16, lane / 16) of
@@ -518,21 +517,21 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_stream(Product a) {
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         const uint32_t v = EVEN ? coff[b] : coff[b] + (uint32_t)block_of(span, piece[b & 1]) * 8;
-        load_to_lds<16>(codes, some && (both || b < 2) ? v : kPastEnd, (uint32_t)(tile * OUT) * pitch + (EVEN ? span * 128 : 0),
+        load_to_lds<16>(codes, buffer_at(some, both || b < 2, v, (uint32_t)(tile * OUT) * pitch + (EVEN ? span * 128 : 0)),
                         at + b * 1024);
       }
       if constexpr (EVEN) {
         const int r = (lane & 15) + (lane >> 4 & 1) * up;
-        load_to_lds<16>(scales, some && lane < 32 && (both || lane < 16) ? (uint32_t)r * nblk : kPastEnd,
-                        (uint32_t)(tile * OUT) * nblk + span * 16, at + 4096);
+        load_to_lds<16>(scales, buffer_at(some, lane < 32 && (both || lane < 16), (uint32_t)r * nblk,
+                                          (uint32_t)(tile * OUT) * nblk + span * 16), at + 4096);
       } else {
         const int w0 = block_of(span, 0);
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
           const int i = j * 64 + lane, rr = i / 5;
           const uint32_t r = tile * OUT + (rr & 15) + (rr >> 4) * up;
-          load_to_lds<4>(scales, some && i < 160 && (both || rr < 16) ? ((phase + r * nblk + w0) & ~3u) + i % 5 * 4 : kPastEnd,
-                         0, at + 4096 + j * 256);
+          load_to_lds<4>(scales, buffer_at(some, i < 160 && (both || rr < 16), ((phase + r * nblk + w0) & ~3u) + i % 5 * 4, 0),
+                         at + 4096 + j * 256);
         }
       }
     };
@@ -733,16 +732,17 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_last(Product a, const float
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const uint32_t v = EVEN ? coff[b] : coff[b] + (uint32_t)block_of(span, piece[b]) * 8;
-      load_to_lds<16>(codes, some ? v : kPastEnd, row0 * pitch + (EVEN ? span * 128 : 0), at + b * 1024);
+      load_to_lds<16>(codes, buffer_at(some, true, v, row0 * pitch + (EVEN ? span * 128 : 0)), at + b * 1024);
     }
     if constexpr (EVEN) {
-      load_to_lds<4>(scales, some ? (uint32_t)(lane >> 2) * nblk + (lane & 3) * 4 : kPastEnd, row0 * nblk + span * 16, at + 2048);
+      load_to_lds<4>(scales, buffer_at(some, true, (uint32_t)(lane >> 2) * nblk + (lane & 3) * 4, row0 * nblk + span * 16),
+                     at + 2048);
     } else {
       const int w0 = block_of(span, 0);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int i = j * 64 + lane;
-        load_to_lds<4>(scales, some && i < 80 ? ((phase + (row0 + i / 5) * nblk + w0) & ~3u) + i % 5 * 4 : kPastEnd, 0,
+        load_to_lds<4>(scales, buffer_at(some, i < 80, ((phase + (row0 + i / 5) * nblk + w0) & ~3u) + i % 5 * 4, 0),
                        at + 2048 + j * 256);
       }
     }
