@@ -20,6 +20,11 @@ inline int64_t tile_bound(int64_t total_rows, int64_t num_segments, int64_t tile
   return (total_rows + tile - 1) / tile + num_segments;
 }
 
+// Workgroups of `threads` that one launch takes: a grid has fewer than 2^32
+// work-items along a dimension. Calls of more rows than that are several
+// launches, a slice of the rows each.
+constexpr int64_t max_blocks(int threads) { return 0xFFFFFFFFll / threads; }
+
 // Compute units of the current device (persistent kernels launch one
 // workgroup per CU); 256 if the query fails. The per-device cache is atomic:
 // threads calling concurrently may each query once and store the same value.

@@ -128,14 +128,18 @@ __global__ __launch_bounds__(kQThreads) void k_quant_int8(const T* __restrict__ 
 template <typename T, int TPR, bool GLU>
 void launch_quant_tpr(const T* x, int64_t rows, int64_t C, uint32_t* codes, float* scales, hipStream_t s) {
   const int64_t per = (C / 16 + TPR - 1) / TPR;
-  const dim3 grid((unsigned)((rows + kQThreads / TPR - 1) / (kQThreads / TPR)));
-#define BSQ_Q(MB)                                                                                                \
-  hipLaunchKernelGGL((k_quant_int8<T, TPR, MB, GLU>), grid, dim3(kQThreads), 0, s, x, rows, C, codes, scales)
-  if (per <= 1) BSQ_Q(1);
-  else if (per <= 2) BSQ_Q(2);
-  else if (per <= 4) BSQ_Q(4);
-  else BSQ_Q(8);
+  constexpr int64_t group = kQThreads / TPR, most = bsqh::max_blocks(kQThreads) * group;
+  for (; rows > 0; rows -= most, x += most * C * (GLU ? 2 : 1), codes += most * C / 4, scales += most) {
+    const int64_t n = rows < most ? rows : most;
+    const dim3 grid((unsigned)((n + group - 1) / group));
+#define BSQ_Q(MB) \
+  hipLaunchKernelGGL((k_quant_int8<T, TPR, MB, GLU>), grid, dim3(kQThreads), 0, s, x, n, C, codes, scales)
+    if (per <= 1) BSQ_Q(1);
+    else if (per <= 2) BSQ_Q(2);
+    else if (per <= 4) BSQ_Q(4);
+    else BSQ_Q(8);
 #undef BSQ_Q
+  }
 }
 
 // A wave per row while the rows fill the chip and fit its registers, else a
@@ -180,10 +184,12 @@ constexpr int kFuseCodes = 16384;
 // Waves: as many as leave each of them a ring of three steps or more in 160 KB.
 constexpr int few_waves(bool fused) { return fused ? 8 : 4; }
 
+//
+// N channels from the given ones on, in rows of `pitch` outputs.
 template <typename X, typename T, int MT, bool FUSED>
 __global__ __launch_bounds__(64 * few_waves(FUSED)) void k_gemm_int8_few(
     const X* __restrict__ a, const float* __restrict__ sa, const int8_t* __restrict__ b, const float* __restrict__ sb,
-    const float* __restrict__ bias, int M, int N, int K, T* __restrict__ out) {
+    const float* __restrict__ bias, int M, int N, int K, int pitch_out, T* __restrict__ out) {
   constexpr int kFWaves = few_waves(FUSED), kFThreads = 64 * kFWaves;
   constexpr int LOADS = FUSED ? 2 : 2 + 2 * MT;           // of a step: 8 rows of 128 bytes each
   constexpr int R = FUSED ? 4 : MT == 1 ? 8 : MT == 2 ? 5 : 3;
@@ -305,7 +311,7 @@ __global__ __launch_bounds__(64 * few_waves(FUSED)) void k_gemm_int8_few(
     if constexpr (FUSED) ea[i] = row_scale(__uint_as_float(rmax[row]));
     float y = (float)s * ea[i] * eb[i];
     if (bias) y += ec[i];
-    store1(out + (int64_t)row * N + n, y);
+    store1(out + (int64_t)row * pitch_out + n, y);
   }
 }
 
@@ -523,19 +529,31 @@ __global__ __launch_bounds__(256, 1) void k_gemm_int8(const int8_t* __restrict__
   }
 }
 
+template <typename X, typename T, int MT, bool FUSED>
+void launch_few(const X* a, const float* sa, const int8_t* b, const float* sb, const float* bias, int64_t M, int64_t N,
+                int64_t K, T* out, hipStream_t s) {
+  constexpr int threads = 64 * few_waves(FUSED);
+  constexpr int64_t most = bsqh::max_blocks(threads) * 16;
+  for (int64_t n0 = 0; n0 < N; n0 += most) {
+    const int64_t n = N - n0 < most ? N - n0 : most;
+    hipLaunchKernelGGL((k_gemm_int8_few<X, T, MT, FUSED>), dim3((unsigned)((n + 15) / 16)), dim3(threads), 0, s, a, sa,
+                       b + n0 * K, sb + n0, bias ? bias + n0 : nullptr, (int)M, (int)n, (int)K, (int)N, out + n0);
+  }
+}
+
 template <typename T>
 void launch_gemm(const int8_t* a, const float* sa, const int8_t* b, const float* sb, const float* bias, int64_t M,
                  int64_t N, int64_t K, T* out, hipStream_t s) {
   if (M <= 64) {
-    const dim3 grid((unsigned)((N + 15) / 16));
-#define BSQ_F(MT)                                                                                                     \
-  hipLaunchKernelGGL((k_gemm_int8_few<int8_t, T, MT, false>), grid, dim3(64 * few_waves(false)), 0, s, a, sa, b, sb, bias, (int)M, \
-                     (int)N, (int)K, out)
-    if (M <= 16) BSQ_F(1);
-    else if (M <= 32) BSQ_F(2);
-    else BSQ_F(4);
-#undef BSQ_F
+    if (M <= 16) launch_few<int8_t, T, 1, false>(a, sa, b, sb, bias, M, N, K, out, s);
+    else if (M <= 32) launch_few<int8_t, T, 2, false>(a, sa, b, sb, bias, M, N, K, out, s);
+    else launch_few<int8_t, T, 4, false>(a, sa, b, sb, bias, M, N, K, out, s);
     return;
+  }
+  const int64_t most = bsqh::max_blocks(256) / ((N + 127) / 128) * 128;  // rows that a launch of the smallest tiles takes
+  if (M > most) {
+    launch_gemm(a, sa, b, sb, bias, most, N, K, out, s);
+    return launch_gemm(a + most * K, sa + most, b, sb, bias, M - most, N, K, out + most * N, s);
   }
   // Large tiles move fewer bytes for each product, small ones leave no CU idle.
   // Compared by the time of their rounds, in quarters of a 256 x 256 round (one
@@ -566,8 +584,9 @@ void launch_gemm(const int8_t* a, const float* sa, const int8_t* b, const float*
 
 int check_gemm(int64_t M, int64_t N, int64_t K, int out_dtype) {
   BSQ_REQUIRE(out_dtype == BSQ_F32 || out_dtype == BSQ_BF16, BSQ_E_DTYPE);
-  // 128 * 128 * K stays below 2^31; fewer than 2^31 tiles
-  BSQ_REQUIRE(M >= 0 && M < (int64_t)1 << 31 && N >= 0 && N < (int64_t)1 << 31 && K >= 16 && K % 16 == 0 && K < 131072,
+  // 128 * 128 * K stays below 2^31; fewer than 2^31 tiles, and a launch takes those of 128 rows at least
+  BSQ_REQUIRE(M >= 0 && M < (int64_t)1 << 31 && N >= 0 && N <= ((int64_t)1 << 31) - 256 && K >= 16 && K % 16 == 0 &&
+                  K < 131072,
               BSQ_E_SHAPE);
   BSQ_REQUIRE(((M + 127) / 128) * ((N + 127) / 128) < (int64_t)1 << 31, BSQ_E_SHAPE);
   return BSQ_OK;
@@ -642,11 +661,9 @@ extern "C" int bsq_linear_int8(const void* x, int dtype, const int8_t* b_codes, 
               BSQ_E_ALIGN);
   BSQ_REQUIRE(ws_bytes >= need, BSQ_E_WORKSPACE);
   if (fused(M, K, dtype == BSQ_F32 ? 4 : 2)) {
-    const dim3 grid((unsigned)((N + 15) / 16));
-#define BSQ_FUSED(X, T)                                                                                          \
-  hipLaunchKernelGGL((k_gemm_int8_few<X, T, 1, true>), grid, dim3(64 * few_waves(true)), 0, bsqh::as_stream(stream),        \
-                     static_cast<const X*>(x), static_cast<const float*>(nullptr), b_codes, b_scales, bias, (int)M, \
-                     (int)N, (int)K, static_cast<T*>(out))
+#define BSQ_FUSED(X, T)                                                                                       \
+  launch_few<X, T, 1, true>(static_cast<const X*>(x), nullptr, b_codes, b_scales, bias, M, N, K, static_cast<T*>(out), \
+                            bsqh::as_stream(stream))
     if (dtype == BSQ_BF16 && out_dtype == BSQ_BF16) BSQ_FUSED(uint16_t, uint16_t);
     else if (dtype == BSQ_BF16) BSQ_FUSED(uint16_t, float);
     else if (out_dtype == BSQ_BF16) BSQ_FUSED(float, uint16_t);

@@ -310,25 +310,34 @@ __global__ __launch_bounds__(kThreads) void k_moe_gate_backward(const float* __r
 template <typename T, int L, int V, bool WHOLE>
 void launch_gate_k(const T* logits, int64_t tokens, int E, int k, int renorm, float* weights, int32_t* ids,
                    hipStream_t s) {
-  const unsigned grid = (unsigned)((tokens + kThreads / L - 1) / (kThreads / L));
-  if (k <= L)
-    hipLaunchKernelGGL((k_moe_gate<T, L, V, WHOLE, 1>), dim3(grid), dim3(kThreads), 0, s, logits, tokens, E, k,
-                       renorm, weights, ids);
-  else
-    hipLaunchKernelGGL((k_moe_gate<T, L, V, WHOLE, 64 / L>), dim3(grid), dim3(kThreads), 0, s, logits, tokens, E, k,
-                       renorm, weights, ids);
+  constexpr int64_t per = kThreads / L, most = bsqh::max_blocks(kThreads) * per;
+  for (; tokens > 0; tokens -= most, logits += most * E, weights += most * k, ids += most * k) {
+    const int64_t n = tokens < most ? tokens : most;
+    const unsigned grid = (unsigned)((n + per - 1) / per);
+    if (k <= L)
+      hipLaunchKernelGGL((k_moe_gate<T, L, V, WHOLE, 1>), dim3(grid), dim3(kThreads), 0, s, logits, n, E, k, renorm,
+                         weights, ids);
+    else
+      hipLaunchKernelGGL((k_moe_gate<T, L, V, WHOLE, 64 / L>), dim3(grid), dim3(kThreads), 0, s, logits, n, E, k,
+                         renorm, weights, ids);
+  }
 }
 
 template <typename T, int L, int V, bool WHOLE, int KR>
 void launch_back_k(const float* dw, const float* w, const int32_t* ids, const T* logits, int64_t tokens, int E, int k,
                    int renorm, T* dlogits, hipStream_t s) {
-  const unsigned grid = (unsigned)((tokens + kThreads / L - 1) / (kThreads / L));
-  if (renorm)
-    hipLaunchKernelGGL((k_moe_gate_backward<T, L, V, WHOLE, KR, true>), dim3(grid), dim3(kThreads), 0, s, dw, w, ids,
-                       logits, tokens, E, k, dlogits);
-  else
-    hipLaunchKernelGGL((k_moe_gate_backward<T, L, V, WHOLE, KR, false>), dim3(grid), dim3(kThreads), 0, s, dw, w, ids,
-                       logits, tokens, E, k, dlogits);
+  constexpr int64_t per = kThreads / L, most = bsqh::max_blocks(kThreads) * per;
+  for (; tokens > 0; tokens -= most, dw += most * k, w += most * k, ids += most * k, dlogits += most * E) {
+    const int64_t n = tokens < most ? tokens : most;
+    const unsigned grid = (unsigned)((n + per - 1) / per);
+    if (renorm)
+      hipLaunchKernelGGL((k_moe_gate_backward<T, L, V, WHOLE, KR, true>), dim3(grid), dim3(kThreads), 0, s, dw, w, ids,
+                         logits, n, E, k, dlogits);
+    else
+      hipLaunchKernelGGL((k_moe_gate_backward<T, L, V, WHOLE, KR, false>), dim3(grid), dim3(kThreads), 0, s, dw, w, ids,
+                         logits, n, E, k, dlogits);
+    if (logits) logits += most * E;  // not given where the weights are renormalized
+  }
 }
 template <typename T, int L, int V, bool WHOLE>
 void launch_back(const float* dw, const float* w, const int32_t* ids, const T* logits, int64_t tokens, int E, int k,
@@ -351,7 +360,6 @@ void launch_back(const float* dw, const float* w, const int32_t* ids, const T* l
   else FN<T, 64, 16, false>(__VA_ARGS__)
 
 bool shape_ok(int64_t tokens, int64_t E, int64_t k) {
-  // the grid has at most tokens / 4 + 1 workgroups; offsets stay inside int64
   return tokens >= 0 && tokens < (int64_t)1 << 31 && E >= 1 && E <= 1024 && k >= 1 && k <= 64 && k <= E;
 }
 

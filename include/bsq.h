@@ -483,8 +483,8 @@ int bsq_moe_few_nvfp4(const void* x, int dtype, int64_t tokens, int64_t hidden, 
  * bsq_linear_int8: bsq_gemm_int8 of bsq_quantize_int8(x [M, K]); the same bits
  *   as the two calls. ws bsq_linear_int8_workspace() bytes (0, and ws may be
  *   NULL, where a few rows are quantized inside the product).
- * cols, ffn and (linear) K: multiples of 16 in [16, 32768]. rows, M, N < 2^31,
- * ceil(M / 128) * ceil(N / 128) < 2^31.
+ * cols, ffn and (linear) K: multiples of 16 in [16, 32768]. rows, M < 2^31,
+ * N <= 2^31 - 256, ceil(M / 128) * ceil(N / 128) < 2^31.
  * x, h13, codes and ws 16-byte aligned; out to its type; scales and bias 4.
  * Errors: NULL, SHAPE, ALIGN, DTYPE, WORKSPACE, LAUNCH.
  * ---------------------------------------------------------------------- */
