@@ -63,11 +63,17 @@ __device__ __forceinline__ uint32_t codes4(const float* v, float inv) {
   return w;
 }
 
+// The larger magnitude of m >= 0 and x, NaN if one is (fmaxf would drop it; both
+// are one instruction).
+__device__ __forceinline__ float max_abs(float m, float x) { return __builtin_elementwise_maximum(m, fabsf(x)); }
+
 // The row's scale: max * f32(1/127), or 1 where that would be below the normal range
-// (its reciprocal could overflow); all codes of such a row are 0.
+// (its reciprocal could overflow); all codes of such a row are 0. A row with a
+// NaN or an infinity has no codes that stand for it: its scale is NaN, and with
+// it every output.
 __device__ __forceinline__ float row_scale(float amax) {
   const float s = amax * (1.0f / 127.0f);
-  return s >= kFltMinNormal ? s : 1.0f;
+  return s < kFltMinNormal ? 1.0f : s < __builtin_inff() ? s : __builtin_nanf("");
 }
 
 // TPR threads share a row and keep it in registers, up to MAXB blocks of 16
@@ -98,19 +104,19 @@ __global__ __launch_bounds__(kQThreads) void k_quant_int8(const T* __restrict__ 
         load16(x + row * C + j * 16, v[b]);
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[b][i]));
+      for (int i = 0; i < 16; ++i) amax = max_abs(amax, v[b][i]);
     }
   }
-  if constexpr (TPR <= 64) {
-    amax = group_max<TPR>(amax);
-  } else {
+  static_assert(TPR == 64 || TPR == kQThreads, "a wave or a workgroup to a row");
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) amax = max_abs(amax, __shfl_xor(amax, o, 64));
+  if constexpr (TPR > 64) {
     __shared__ float red[kQThreads / 64];
-    const float wm = wave_max(amax);
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = wm;
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = amax;
     __syncthreads();
     amax = red[0];
 #pragma unroll
-    for (int w = 1; w < kQThreads / 64; ++w) amax = fmaxf(amax, red[w]);
+    for (int w = 1; w < kQThreads / 64; ++w) amax = max_abs(amax, red[w]);
   }
   const float s = row_scale(amax);
   const float inv = 1.0f / s;
@@ -256,8 +262,8 @@ __global__ __launch_bounds__(64 * few_waves(FUSED)) void k_gemm_int8_few(
       float v[16], mx = 0.0f;
       load16(reinterpret_cast<const X*>(raw) + u * 16, v);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, fabsf(v[i]));
-      atomicMax(&rmax[u / per], __float_as_uint(mx));
+      for (int i = 0; i < 16; ++i) mx = max_abs(mx, v[i]);
+      atomicMax(&rmax[u / per], __float_as_uint(mx) & 0x7FFFFFFFu);  // by bits: a NaN's are above an infinity's
     }
     lds_barrier();
     for (int u = t; u < units; u += kFThreads) {

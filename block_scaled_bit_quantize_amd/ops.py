@@ -436,7 +436,8 @@ def moe_few_tokens_nvfp4(x, topk_ids, topk_weights, w13_codes, w13_scales, w13_o
 
 def quantize_int8(x):
     """Rows of x [R, C] (float32 or bfloat16, C % 16 == 0) in 8-bit integers
-    with a scale each: (codes int8 [R, C], scales f32 [R])."""
+    with a scale each: (codes int8 [R, C], scales f32 [R]). A row with a NaN or
+    an infinity gets the scale NaN, and NaN in every output made from it."""
     lib = load_library()
     _dev(x)
     _need(x.dim() == 2, "quantize_int8: x must be [rows, cols]")

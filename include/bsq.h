@@ -470,7 +470,9 @@ int bsq_moe_few_nvfp4(const void* x, int dtype, int64_t tokens, int64_t hidden, 
  * bsq_quantize_int8: x [rows, cols] of `dtype` -> codes int8 [rows, cols] and
  *   scales FP32 [rows]: s = f32(max|x| * f32(1/127)) per row, or 1 where that is
  *   below 2^-126 (all codes are then 0); code = rint(f32(x * f32(1/s))), half to
- *   even, within [-127, 127].
+ *   even, within [-127, 127]. A row that holds a NaN or an infinity gets the
+ *   scale NaN (its codes are unspecified), so that every output of the products
+ *   in that row is NaN.
  * bsq_swiglu_quantize_int8: the same of silu(g) * u in float32, h13
  *   [rows, 2*ffn] with gate columns [0, ffn), then up columns; silu(g) is
  *   g / (1 + e^-g) by the hardware's base-2 exponential and reciprocal (a few

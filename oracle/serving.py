@@ -7,7 +7,8 @@ moe_gate_grad    the gradient of sum(dweights * weights) to the logits with the
                  selection held fixed.
 moe_few          sum_j w_j W2_e (silu(G) * U), (G; U) = W13_e x, with a bound of
                  the float32 kernels' error from the sums' absolute values.
-quantize_int8    rows in 8-bit integers, decided in float32 as the kernels do.
+quantize_int8    rows in 8-bit integers, decided in float32 as the kernels do;
+                 a row with a NaN or an infinity has the scale NaN.
 """
 import numpy as np
 
@@ -101,9 +102,12 @@ def quantize_int8(x):
     """(codes int8 [R, C], scales float32 [R]), every step in float32."""
     x = np.asarray(x, dtype=np.float32)
     s = (np.abs(x).max(1) * (np.float32(1) / np.float32(127))).astype(np.float32)
-    s = np.where(s >= np.float32(2.0 ** -126), s, np.float32(1)).astype(np.float32)
-    q = np.rint(x * (np.float32(1) / s).astype(np.float32)[:, None])
-    return np.clip(q, -127, 127).astype(np.int8), s
+    s = np.where(s < np.float32(2.0 ** -126), np.float32(1), s).astype(np.float32)
+    fine = np.isfinite(s)
+    with np.errstate(invalid="ignore"):
+        q = np.rint(x * (np.float32(1) / s).astype(np.float32)[:, None])
+    q = np.where(fine[:, None], q, 0)  # unspecified
+    return np.clip(q, -127, 127).astype(np.int8), np.where(fine, s, np.float32(np.nan)).astype(np.float32)
 
 
 def gemm_int8(a, sa, b, sb, bias=None):
