@@ -51,13 +51,23 @@ class ExpertLayer:
     def routed_few(self, x, weights, ids):
         return bsq.moe_few_tokens_nvfp4(x, ids, weights, *self.w13, *self.w2)
 
+    def whole(self, ids):
+        """ids for route, which takes distinct experts alone: a slot without one (-1: logits that are masked or NaN)
+        gets one that its token has not chosen, whose row is left out of the sum."""
+        none = ids < 0
+        chosen = torch.zeros((ids.shape[0], self.experts + 1), dtype=torch.int8, device=ids.device)
+        chosen.scatter_(1, torch.where(none, self.experts, ids).long(), 1)
+        left = torch.argsort(chosen[:, :self.experts], dim=1, stable=True)  # those not chosen first
+        return torch.where(none, left.gather(1, (none.cumsum(1) - 1).clamp(min=0)).int(), ids)
+
     def routed_many(self, x, weights, ids):
         T, k = ids.shape
-        rows, seg, pair = bsq.route(ids, self.experts)
+        rows, seg, pair = bsq.route(self.whole(ids), self.experts)
         xq = bsq.quantize_nvfp4(x, "row", four_over_six=True)
         h13 = bsq.grouped_gemm_nvfp4(*xq, *self.w13, seg, T * k, row_index=rows)
         z = bsq.grouped_gemm_nvfp4(*bsq.swiglu_quantize_nvfp4(h13), *self.w2, seg, T * k, out_dtype=torch.float32)
-        return (z[pair.long()].reshape(T, k, -1) * weights[:, :, None]).sum(1).to(x.dtype)
+        z = z[pair.long()].reshape(T, k, -1) * weights[:, :, None]
+        return z.masked_fill((ids < 0)[:, :, None], 0.0).sum(1).to(x.dtype)
 
     def __call__(self, x):
         _, weights, ids = self.gate(x)
