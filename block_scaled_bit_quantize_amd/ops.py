@@ -365,12 +365,14 @@ def moe_gate(logits, k, renormalize=True):
     (weights f32 [T, k], topk_ids int32 [T, k]), largest first, ties to the
     lowest index. The weights are a softmax over the selected logits, or with
     renormalize=False over all of them. Logits of -inf (and NaN) are masked; a
-    slot that finds no unmasked logit left gets id -1 and weight 0."""
+    slot that finds no unmasked logit left gets id -1 and weight 0. Not recorded
+    by autograd, as no operator here: moe_gate_backward is the gradient."""
     lib = load_library()
     _dev(logits)
     _need(logits.dim() == 2, "moe_gate: logits must be [tokens, experts]")
     T, E = logits.shape
     dt = _dtype(logits, "logits")
+    _need(1 <= k <= min(E, 64), "moe_gate: k must be in [1, min(experts, 64)]")
     weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
     ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
     check(lib.bsq_moe_gate(logits.data_ptr(), dt, T, E, k, 1 if renormalize else 0, weights.data_ptr(),
