@@ -26,8 +26,10 @@
 // at most 6 significant bits and lies in [2^-10, 2688]): a convert and a
 // packed multiply, one instruction a weight. Activations are scaled by a power
 // of two for each token and wave, so that the largest lies near 2^14, and
-// split into fp16 terms: bf16 inputs are one exact term (values below 2^-31 of
-// the largest lose bits, 2^-39 of it at most), float32 inputs and the SwiGLU result two (22 bits).
+// split into fp16 terms: bf16 inputs are one term, exact down to 2^-31 of the
+// largest, float32 inputs and the SwiGLU result two, 22 bits down to 2^-16 of
+// the largest. What is smaller is off by half of fp16's least step, 2^-24, and
+// so by 2^-39 of the largest at most.
 // v_mfma_f32_16x16x32_f16 sums in float32; the powers of two are taken back
 // before the waves' sums are added, the outer scales and the token's weight
 // after.

@@ -440,10 +440,11 @@ int bsq_moe_gate_backward(const float* dweights, const float* weights, const int
  * w13_*    codes [E, 2*ffn, hidden/2], scales [E, 2*ffn, hidden/16], outer [E]:
  *          gate rows [0, ffn), then up rows; w2_* [E, hidden, ffn/2], ... as
  *          bsq_quantize_nvfp4 writes them with BSQ_OUTER_TENSOR.
- * Products of exactly decoded weights in float32 sums; BF16 x is multiplied as
- * it is, F32 x and silu(G) * U to 22 significant bits (all after scaling by a
- * power of two; values below 2^-31 of a token's largest lose bits). A token's
- * experts are added in slot order in float32: the same bits on every call.
+ * Products of exactly decoded weights in float32 sums. BF16 x is multiplied as
+ * it is down to 2^-31 of the token's largest value, F32 x and silu(G) * U to 22
+ * significant bits down to 2^-16 of the largest; below that to 2^-39 of the
+ * largest. A token's experts are added in slot order in float32: the same bits
+ * on every call.
  * hidden % 16 == 0, ffn % 16 == 0, both in [16, 32768]; 1 <= E <= 1024,
  * 1 <= k <= 64, tokens * k <= BSQ_MOE_FEW_MAX_PAIRS (more tokens: the grouped
  * GEMMs).
