@@ -178,8 +178,9 @@ __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = __builtin_bi
 // of a row (64 bytes a row took the address unit twice as long, a lane a row as
 // in the matrix instruction's own layout four times). Piece p of row r lies at
 // p ^ (r / 2 % 8), so that 16 rows at one piece meet 16 different banks. The
-// exact integer partial sums meet in LDS. 50 x 2048 x 7168 takes 9.4 us (11.6
-// with 64 bytes of a row a load), 64 x 8192 x 4096 15.9 us.
+// exact integer partial sums meet in LDS. 50 x 2048 x 7168 takes 9.5 us (11.6
+// with 64 bytes of a row a load; half of the CUs have no channels there, and
+// every workgroup reads all activations), 64 x 8192 x 4096 15.9 us.
 //
 // FUSED: the activations come unquantized, few enough to lie in LDS (kFuseBytes);
 // every workgroup quantizes them itself, while the first weights are on their
@@ -334,7 +335,9 @@ __global__ __launch_bounds__(64 * few_waves(FUSED)) void k_gemm_int8_few(
 // 256 x 256 tiles are bound by the chip's power: the matrix instructions alone
 // reach 3.4 POP/s on random codes (4.8 on zeros), and with them 62% of the
 // cycles at a clock that sinks to 1.45 GHz the kernel runs at 1.9 to 2.2 POP/s
-// (65536 x 2048 x 7168: 0.88 to 1.0 ms, with the loads left out 0.79). Small
+// (65536 x 2048 x 7168: 0.85 to 1.0 ms, with the loads left out 0.79). With
+// short K a tile's first loads and its stores count too: 16384 x 4096 x 1536 (24
+// steps) 143 us, 1.45 POP/s. Small
 // tiles are bound by the latency of their loads: 128 bytes a row and step
 // (L2 serves twice the bytes with whole lines), 96 KB of them in flight a CU.
 //

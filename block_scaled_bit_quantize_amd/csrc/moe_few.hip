@@ -17,10 +17,11 @@
 // Up to 110 KB a CU are in flight, across tile ends too; the waves' partial
 // sums meet in LDS, in two buffers, with one barrier a tile that leaves the
 // loads in flight. 64 tokens, top 8 of 64 experts of 1536, hidden 4096: W13
-// 92 us (453 MB, 4.9 TB/s; 84 us with the barrier and the stores left out), W2
-// 60 us (226 MB, 3.8 TB/s; 47 us with nothing but the stream), where plain
-// reads reach 5.9 TB/s. One token: 16 and 14 us, of which the first bytes'
-// way (ids, expert, descriptor, latency) is about 5 each.
+// 96 us (453 MB, 4.7 TB/s; 8 us of them for the barrier and the stores), W2 62
+// to 69 us (226 MB, 3.3 to 3.7 TB/s; 13 us of them besides the stream, and its
+// six spans of K leave two of the eight waves without one), where plain reads
+// reach 5.9 TB/s. One token: 16.6 and 14.6 us, of which the first bytes' way
+// (ids, expert, descriptor, latency) is about 5 each.
 //
 // Weights are decoded to fp16 exactly (an E2M1 value times its E4M3 scale has
 // at most 6 significant bits and lies in [2^-10, 2688]): a convert and a
@@ -649,8 +650,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_stream(Product a) {
 // so a token's experts meet in it, in slot order, and nothing is left to another
 // launch. A wave has one or two spans of K, its activations stay in registers;
 // where K has fewer spans than there are waves, groups of waves take the
-// experts in turn. One token of 4096 x 1536, top 8: 14 us against 14 for W2 and 4 for
-// the sum; 10 of them are latency (28 MB take 5).
+// experts in turn. One token of 4096 x 1536, top 8: 14.6 us against 14 for W2 and 4
+// for the sum; 10 of them are latency (28 MB take 5).
 struct SmallPlace {  // a span of 16 weight rows; as Place
   u32x4 codes[2][64];
   uint32_t scales[128];
