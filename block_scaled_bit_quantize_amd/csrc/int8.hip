@@ -337,9 +337,9 @@ __global__ __launch_bounds__(64 * few_waves(FUSED)) void k_gemm_int8_few(
 // cycles at a clock that sinks to 1.45 GHz the kernel runs at 1.9 to 2.2 POP/s
 // (65536 x 2048 x 7168: 0.85 to 1.0 ms, with the loads left out 0.79). With
 // short K a tile's first loads and its stores count too: 16384 x 4096 x 1536 (24
-// steps) 143 us, 1.45 POP/s. Small
-// tiles are bound by the latency of their loads: 128 bytes a row and step
-// (L2 serves twice the bytes with whole lines), 96 KB of them in flight a CU.
+// steps) 143 us, 1.45 POP/s. Small tiles are bound by the latency of their
+// loads: 128 bytes a row and step (L2 serves twice the bytes with whole lines),
+// 96 KB of them in flight a CU.
 //
 // A stage's rows hold their 16-byte pieces in an order that depends on the row,
 // so that 16 rows at one piece meet 16 different banks. Fragments past K (in a
