@@ -9,6 +9,7 @@ c_i64 = ctypes.c_int64
 c_u64 = ctypes.c_uint64
 c_int = ctypes.c_int
 c_size = ctypes.c_size_t
+c_f32 = ctypes.c_float
 c_vp = ctypes.c_void_p
 
 # include/bsq.h: BSQ_ROUTE_NOALLOC_MAX_BYTES
@@ -55,6 +56,10 @@ SIGNATURES = {
     "bsq_mfma_rate_probe": (c_int, [c_int, c_int, c_i64, c_i64, c_vp, c_vp]),
     "bsq_moe_gate": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_int, c_vp, c_vp, c_vp]),
     "bsq_moe_gate_backward": (c_int, [c_vp, c_vp, c_vp, c_vp, c_int, c_i64, c_i64, c_i64, c_int, c_vp, c_vp]),
+    "bsq_moe_gate_grouped": (c_int, [c_vp, c_int, c_vp, c_i64, c_i64, c_i64, c_i64, c_i64, c_int, c_int, c_int, c_f32,
+                                     c_vp, c_vp, c_vp]),
+    "bsq_moe_gate_grouped_backward": (c_int, [c_vp, c_vp, c_vp, c_vp, c_int, c_i64, c_i64, c_i64, c_int, c_int, c_f32,
+                                              c_vp, c_vp]),
     "bsq_moe_few_nvfp4_workspace": (c_size, [c_i64, c_i64, c_i64, c_i64, c_i64]),
     "bsq_moe_few_nvfp4": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
                                   c_vp, c_vp, c_vp, c_vp, c_size, c_vp]),

@@ -1,0 +1,643 @@
+// Expert selection by scores, a balancing bias and groups of experts, and the
+// gradient of its weights.
+//
+// A token's logits l_i give scores s_i: sigmoid(l_i), or the softmax over the
+// unmasked ones. The keys c_i = s_i + b_i (bias b, which the weights do not
+// see) choose: a group of experts is worth the sum of its one or two largest
+// keys, the best group_k groups stay, and of their experts the k with the
+// largest keys are selected. Ties go to the lowest index at both steps. The
+// order is that of keys evaluated in float64. Weights:
+//   w_j = scale s_j, or scale s_j / sum of the selected scores (renormalized).
+// Gradient of sum g_j w_j, the selection held fixed, with h = sum g_j w_j:
+//   sigmoid:  dl_j = w_j (g_j - [renormalized] h / scale) (1 - s_j), 0 where not selected
+//   softmax:  renormalized  dl_j = w_j (g_j - h / scale), 0 where not selected
+//             else          dl_i = s_i (scale [i selected] g_i - h)
+//
+// How the order can be that of float64 keys at the speed of float32: keys are
+// made in float32 with a bound on their error, the selection is made by them,
+// and the groups at the cut and the selected keys next to each other are then
+// looked at. Where two are nearer than their bounds and do not come from equal
+// logits and biases (equal inputs are a true tie), the row is ambiguous and its
+// wave selects again in float64 with all 64 lanes (in 1 row of about 1000).
+//
+// Layout as in the plain router: 16 lanes share a row up to 256 experts, 64
+// above; a lane holds V neighbouring experts in registers.
+#include <math.h>
+
+#include "bsq_device.h"
+#include "bsq_internal.h"
+#include "bsq_rows.h"
+
+using namespace bsqd;
+
+namespace {
+
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kMaxGroups = 64;
+// A value that has been taken out of the selection: below every key, and a
+// number whatever its low word holds.
+constexpr uint32_t kGone = 0xFFEFFFFFu;
+constexpr float kInf = __builtin_inff();
+
+struct Choice {
+  int E, k, groups, size, group_k, group_top;  // groups 1: no restriction
+  int lanes;                                   // lanes that share a group, 0: through LDS
+  bool softmax, renorm;
+  float scale;
+};
+
+// e^x for x <= 0: the product's rounding is carried along, so that what is left
+// is the exponential instruction's error and a rounding (2^-22 relative).
+__device__ __forceinline__ float exp_neg(float x) {
+  x = fmaxf(x, -256.0f);
+  const float t = x * 1.44269504088896340736f;
+  const float r = __builtin_fmaf(x, 1.44269504088896340736f, -t) + x * 1.92596299112661746887e-8f;
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, r * 0.693147180559945309417f, e);
+}
+__device__ __forceinline__ float sigmoid32(float x) {
+  const float e = exp_neg(-fabsf(x));
+  return (x >= 0.0f ? 1.0f : e) * __builtin_amdgcn_rcpf(1.0f + e);
+}
+
+// Error bound of a float32 key c = s + b: the sigmoid is off by less than
+// 2^-20 s (exponential 2^-22, sum, reciprocal and product 2^-24 to 2^-23 each);
+// a softmax score by less than 2^-16 s (its sum by 2^-19, |l - m| 2^-24 from the
+// difference, up to 64 of it: beyond, s is below 2^-92 and the last term covers it);
+// the sum with the bias by 2^-24 |c|. Exponentials that flush to zero are below 2^-110.
+__device__ __forceinline__ float key_bound(float s, float c, bool softmax) {
+  return s * (softmax ? 0x1p-16f : 0x1p-20f) + fabsf(c) * 0x1p-23f + 0x1p-90f;
+}
+
+// Key above its index in one float64: a larger number is a larger key, or the
+// same key at a lower index. The key's low 29 bits are free.
+__device__ __forceinline__ double with_index(float c, int index) {
+  if (!(c > -kInf)) return __hiloint2double((int)kGone, 0);
+  c = fminf(fmaxf(c + 0.0f, -__FLT_MAX__), __FLT_MAX__);
+  const uint64_t b = __double_as_longlong((double)c);
+  return __longlong_as_double((long long)(b | (uint32_t)(c < 0.0f ? index : 1023 - index)));
+}
+__device__ __forceinline__ bool is_gone(double d) { return (uint32_t)__double2hiint(d) == kGone; }
+__device__ __forceinline__ int index_of(double d) {
+  const int low = __double2loint(d) & 1023;
+  return __double2hiint(d) < 0 ? low : 1023 - low;
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  return __hiloint2double(__builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, 0xF, 0xF, false),
+                          __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, 0xF, 0xF, false));
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141;  // lane exchanges inside 16 lanes
+constexpr int ror(int n) { return 0x120 + n; }
+
+template <int L>
+__device__ __forceinline__ double row_max64(double v) {
+  v = fmax(v, dpp<ror(8)>(v));
+  v = fmax(v, dpp<ror(4)>(v));
+  v = fmax(v, dpp<ror(2)>(v));
+  v = fmax(v, dpp<ror(1)>(v));
+  if constexpr (L == 64) {
+    v = fmax(v, __shfl_xor(v, 16, 64));
+    v = fmax(v, __shfl_xor(v, 32, 64));
+  }
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float row_maxf(float v) {
+  v = fmaxf(v, dpp<ror(8)>(v));
+  v = fmaxf(v, dpp<ror(4)>(v));
+  v = fmaxf(v, dpp<ror(2)>(v));
+  v = fmaxf(v, dpp<ror(1)>(v));
+  if constexpr (L == 64) {
+    v = fmaxf(v, __shfl_xor(v, 16, 64));
+    v = fmaxf(v, __shfl_xor(v, 32, 64));
+  }
+  return v;
+}
+__device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+
+// A group's best keys and largest score, over `lanes` aligned lanes of 16.
+struct Top {
+  float a, b, s;  // largest key, second, largest score
+};
+template <int CTRL>
+__device__ __forceinline__ void merge(Top& t) {
+  const float a = dpp<CTRL>(t.a), b = dpp<CTRL>(t.b);
+  t.b = fmaxf(fminf(t.a, a), fmaxf(t.b, b));
+  t.a = fmaxf(t.a, a);
+  t.s = fmaxf(t.s, dpp<CTRL>(t.s));
+}
+// [low, high] that holds the group's worth.
+__device__ __forceinline__ void worth(const Top& t, int group_top, bool softmax, float& low, float& high) {
+  if (!(t.a > -kInf)) {
+    low = high = -kInf;
+    return;
+  }
+  const bool two = group_top == 2 && t.b > -kInf;
+  const float w = two ? t.a + t.b : t.a;
+  float tol = key_bound(t.s, t.a, softmax);
+  if (two) tol += key_bound(t.s, t.b, softmax) + fabsf(w) * 0x1p-23f;
+  low = w - tol;
+  high = w + tol;
+}
+
+// What a wave needs of LDS: the rows' float32 keys (or one row's in float64),
+// a word for each of their groups (or the groups' worth in float64), the groups kept.
+template <int L, int V>
+struct WaveLds {
+  union {
+    float key[64 / L][L * V];
+    double key64[L * V];
+  };
+  union {
+    float bound[64 / L][kMaxGroups][2];
+    double worth64[kMaxGroups];
+  };
+  uint32_t keep[kMaxGroups];
+  int pick[64];
+};
+
+// One row in float64 by all lanes of a wave: the selected indexes go to lds.pick (-1: none left).
+template <typename T, int L, int V>
+__device__ __noinline__ void select64(const T* __restrict__ row, const float* __restrict__ bias, const Choice c,
+                                      WaveLds<L, V>& lds) {
+  const int lane = threadIdx.x & 63;
+  double total = 1.0, m = 0.0;
+  if (c.softmax) {
+    float top = -kInf;
+    for (int e = lane; e < c.E; e += 64) {
+      const float x = load1(row + e);
+      if (x > top) top = x;
+    }
+    top = row_maxf<64>(top);
+    m = top > -kInf ? (double)top : 0.0;
+    total = 0.0;
+    for (int e = lane; e < c.E; e += 64) {
+      const float x = load1(row + e);
+      if (x > -kInf) total += exp((double)x - m);
+    }
+    for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o, 64);
+  }
+  for (int e = lane; e < c.E; e += 64) {
+    const double x = load1(row + e);
+    const double s = c.softmax ? exp(x - m) / total : 1.0 / (1.0 + exp(-x));
+    const double key = s + (bias ? (double)bias[e] : 0.0);
+    lds.key64[e] = x > -(double)kInf && key > -(double)kInf ? key : -(double)kInf;
+  }
+  wave_fence();
+  if (c.groups > 1) {
+    double w = -(double)kInf;
+    if (lane < c.groups) {
+      double a = -(double)kInf, b = a;
+      for (int e = lane * c.size; e < (lane + 1) * c.size; ++e) {
+        const double v = lds.key64[e];
+        b = fmax(b, fmin(a, v));
+        a = fmax(a, v);
+      }
+      w = c.group_top == 2 && b > -(double)kInf ? a + b : a;
+      lds.worth64[lane] = w;
+    }
+    wave_fence();
+    if (lane < c.groups) {
+      int rank = 0;
+      for (int g = 0; g < c.groups; ++g) {
+        const double o = lds.worth64[g];
+        rank += o > w || (o == w && g < lane);
+      }
+      lds.keep[lane] = rank < c.group_k;
+    }
+    wave_fence();
+    for (int e = lane; e < c.E; e += 64)
+      if (!lds.keep[e / c.size]) lds.key64[e] = -(double)kInf;
+    wave_fence();
+  }
+  for (int j = 0; j < c.k; ++j) {
+    double best = -(double)kInf;
+    int at = 0x7FFFFFFF;
+    for (int e = lane; e < c.E; e += 64) {
+      const double v = lds.key64[e];
+      if (v > best) best = v, at = e;
+    }
+    for (int o = 32; o > 0; o >>= 1) {
+      const double v = __shfl_xor(best, o, 64);
+      const int i = __shfl_xor(at, o, 64);
+      if (v > best || (v == best && i < at)) best = v, at = i;
+    }
+    const bool any = best > -(double)kInf;
+    if (lane == 0) lds.pick[j] = any ? at : -1;
+    if (any && (at & 63) == lane) lds.key64[at] = -(double)kInf;
+    wave_fence();
+  }
+}
+
+// KR: registers that hold a row's results, lane j % L holding result j; k + 1
+// of them, since the first that is not selected is looked at too.
+template <typename T, int L, int V, bool WHOLE, int KR>
+__global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ logits, const float* __restrict__ bias,
+                                                        int64_t tokens, Choice c, float* __restrict__ weights,
+                                                        int32_t* __restrict__ ids) {
+  __shared__ WaveLds<L, V> shared[kWaves];
+  WaveLds<L, V>& lds = shared[threadIdx.x >> 6];
+  const int lane = threadIdx.x & 63, sub = lane % L, mine = lane / L;  // row of the wave
+  const int64_t t = (int64_t)blockIdx.x * (kThreads / L) + threadIdx.x / L;
+  const bool ok = t < tokens;  // lanes past the end run along on masked rows
+  const T* row = logits + (ok ? t : 0) * c.E;
+  const int e0 = sub * V;
+  float x[V], b[V], s[V];
+  load_logits<T, V, WHOLE>(row, e0, c.E, ok, x);
+#pragma unroll
+  for (int i = 0; i < V; ++i) b[i] = bias && e0 + i < c.E ? bias[e0 + i] : 0.0f;
+  float m = 0.0f, inv = 1.0f;
+  if (c.softmax) {
+    float top = -kInf, total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) top = fmaxf(top, x[i]);  // drops NaN
+    top = row_maxf<L>(top);
+    m = top > -kInf ? top : 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      s[i] = x[i] > -kInf ? exp_neg(x[i] - m) : 0.0f;
+      total += s[i];
+    }
+    total = row_sum<L>(total);
+    inv = total > 0.0f ? 1.0f / total : 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] *= inv;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] = sigmoid32(x[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) b[i] = x[i] > -kInf ? s[i] + b[i] : -kInf;  // the key; NaN is masked below
+  bool unsure = false;
+  if (c.groups > 1) {
+    Top g = {-kInf, -kInf, 0.0f};
+    if (c.lanes) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        g.b = fmaxf(g.b, fminf(g.a, b[i]));
+        g.a = fmaxf(g.a, b[i]);
+        g.s = fmaxf(g.s, s[i]);
+      }
+      if (c.lanes > 1) merge<kXor1>(g);
+      if (c.lanes > 2) merge<kXor2>(g);
+      if (c.lanes > 4) merge<kHalfMirror>(g);
+      float low, high;
+      worth(g, c.group_top, c.softmax, low, high);
+      int over = 0, near = 0;  // groups that are surely better, that may be
+#define BSQ_TURN(N)                           \
+  if (((N) & (c.lanes - 1)) == 0) {           \
+    over += dpp<ror(N)>(low) > high;          \
+    near += dpp<ror(N)>(high) >= low;         \
+  }
+      BSQ_TURN(1) BSQ_TURN(2) BSQ_TURN(3) BSQ_TURN(4) BSQ_TURN(5) BSQ_TURN(6) BSQ_TURN(7) BSQ_TURN(8)
+      BSQ_TURN(9) BSQ_TURN(10) BSQ_TURN(11) BSQ_TURN(12) BSQ_TURN(13) BSQ_TURN(14) BSQ_TURN(15)
+#undef BSQ_TURN
+      const bool keep = near < c.group_k;
+      unsure = high > -kInf && !keep && over < c.group_k;
+#pragma unroll
+      for (int i = 0; i < V; ++i) b[i] = keep ? b[i] : -kInf;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) lds.key[mine][e0 + i] = b[i];
+      // the largest score stands for all: the bound is wider than it need be
+      float most = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) most = fmaxf(most, s[i]);
+      most = row_maxf<L>(most);
+      wave_fence();
+      for (int q = sub; q < c.groups; q += L) {
+        Top o = {-kInf, -kInf, most};
+        for (int e = q * c.size; e < (q + 1) * c.size; ++e) {
+          const float v = lds.key[mine][e];
+          o.b = fmaxf(o.b, fminf(o.a, v));
+          o.a = fmaxf(o.a, v);
+        }
+        float low, high;
+        worth(o, c.group_top, c.softmax, low, high);
+        lds.bound[mine][q][0] = low;
+        lds.bound[mine][q][1] = high;
+      }
+      wave_fence();
+      uint64_t kept = 0;  // of the groups that this lane looks at
+      for (int q = sub; q < c.groups; q += L) {
+        const float low = lds.bound[mine][q][0], high = lds.bound[mine][q][1];
+        int over = 0, near = 0;
+        for (int p = 0; p < c.groups; ++p) {
+          over += p != q && lds.bound[mine][p][0] > high;
+          near += p != q && lds.bound[mine][p][1] >= low;
+        }
+        const bool keep = near < c.group_k;
+        unsure |= high > -kInf && !keep && over < c.group_k;
+        kept |= (uint64_t)keep << q;
+      }
+#pragma unroll
+      for (int o = 1; o < L; o *= 2) kept |= __shfl_xor((unsigned long long)kept, o, 64);
+#pragma unroll
+      for (int i = 0; i < V; ++i) b[i] = e0 + i < c.E && (kept >> ((e0 + i) / c.size) & 1) ? b[i] : -kInf;
+    }
+  }
+  double key[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) key[i] = with_index(b[i], e0 + i);
+  auto next = [&]() {  // the row's largest key, which is taken out
+    double best = key[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) best = fmax(best, key[i]);
+    best = row_max64<L>(best);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      key[i] = key[i] == best ? __hiloint2double((int)kGone, __double2loint(key[i])) : key[i];
+    return best;
+  };
+  int ri[KR];
+#pragma unroll
+  for (int q = 0; q < KR; ++q) ri[q] = -1;
+  for (int j = 0; j <= c.k; ++j) {
+    const double best = next();
+#pragma unroll
+    for (int q = 0; q < KR; ++q)
+      if (j == q * L + sub && !is_gone(best)) ri[q] = index_of(best);
+  }
+  // the selected ones' logits, biases, scores and keys
+  float rx[KR], rb[KR], rs[KR], rc[KR], tol[KR];
+  auto look = [&](int i, float& lx, float& lb, float& ls, float& lc, float& lt) {
+    lx = load1(row + i);
+    lb = bias ? bias[i] : 0.0f;
+    ls = c.softmax ? exp_neg(lx - m) * inv : sigmoid32(lx);
+    lc = ls + lb;
+    lt = key_bound(ls, lc, c.softmax);
+  };
+#pragma unroll
+  for (int q = 0; q < KR; ++q) look(ri[q] >= 0 ? ri[q] : 0, rx[q], rb[q], rs[q], rc[q], tol[q]);
+  // each against the one after it
+  const int first = mine * L;  // the row's first lane
+  bool tied = false;           // the last selected and the first that is not come from equal inputs
+#pragma unroll
+  for (int q = 0; q < KR; ++q) {
+    const int from = first + (sub + 1) % L;
+    int ni = __shfl(ri[q], from, 64);
+    float nx = __shfl(rx[q], from, 64), nb = __shfl(rb[q], from, 64), nc = __shfl(rc[q], from, 64);
+    float nt = __shfl(tol[q], from, 64);
+    if constexpr (KR > 1) {
+      const int q1 = q + 1 < KR ? q + 1 : q;
+      const int li = __shfl(ri[q1], first, 64);
+      const float lx = __shfl(rx[q1], first, 64), lb = __shfl(rb[q1], first, 64), lc = __shfl(rc[q1], first, 64);
+      const float lt = __shfl(tol[q1], first, 64);
+      if (sub == L - 1) ni = li, nx = lx, nb = lb, nc = lc, nt = lt;
+    }
+    const int j = q * L + sub;
+    if (j < c.k && ri[q] >= 0 && ni >= 0) {
+      const bool same = nx == rx[q] && nb == rb[q];
+      unsure |= !same && !(rc[q] - nc > tol[q] + nt);
+      tied |= same && j == c.k - 1;
+    }
+  }
+  if (__any(tied)) {  // more of the same may follow, and behind them one that is nearer than the bounds
+    const int at = first + (c.k - 1) % L;
+    float lx = 0, lb = 0, lc = 0, lt = 0;
+    bool go = false;
+#pragma unroll
+    for (int q = 0; q < KR; ++q)
+      if (q == (c.k - 1) / L) {
+        lx = __shfl(rx[q], at, 64), lb = __shfl(rb[q], at, 64), lc = __shfl(rc[q], at, 64), lt = __shfl(tol[q], at, 64);
+        go = __shfl((int)tied, at, 64);
+      }
+    while (__any(go)) {  // ends: every turn takes a key out of each row
+      const double best = next();
+      if (go) {
+        go = false;
+        if (!is_gone(best)) {
+          float nx, nb, ns, nc, nt;
+          look(index_of(best), nx, nb, ns, nc, nt);
+          if (nx == lx && nb == lb) go = true;
+          else unsure |= !(lc - nc > lt + nt);
+        }
+      }
+    }
+  }
+  // rows that float32 cannot settle, one after the other
+  uint64_t again = __ballot(unsure && ok);
+  while (again) {
+    const int r = __builtin_ctzll(again) / L;
+    again &= L == 64 ? 0ull : ~(((1ull << (L & 63)) - 1) << (r * L));
+    const int64_t tr = (int64_t)blockIdx.x * (kThreads / L) + (threadIdx.x >> 6) * (64 / L) + r;
+    wave_fence();
+    select64<T, L, V>(logits + tr * c.E, bias, c, lds);
+    if (mine == r) {
+#pragma unroll
+      for (int q = 0; q < KR; ++q) {
+        const int j = q * L + sub;
+        if (j < c.k) {
+          ri[q] = lds.pick[j];
+          rx[q] = load1(row + (ri[q] >= 0 ? ri[q] : 0));
+        }
+      }
+    }
+    wave_fence();
+  }
+  // Weights. Sigmoids over e^a, a the largest min(l, 0): their ratios hold for logits of any size.
+  float e[KR], total = 0.0f, a = -kInf;
+  if (!c.softmax && c.renorm) {
+#pragma unroll
+    for (int q = 0; q < KR; ++q)
+      if (q * L + sub < c.k && ri[q] >= 0) a = fmaxf(a, fminf(rx[q], 0.0f));
+    a = row_maxf<L>(a);
+  } else {
+    a = 0.0f;
+  }
+  if (c.softmax && c.renorm) {  // the softmax over the selected
+    a = -kInf;
+#pragma unroll
+    for (int q = 0; q < KR; ++q)
+      if (q * L + sub < c.k && ri[q] >= 0) a = fmaxf(a, rx[q]);
+    a = row_maxf<L>(a);
+    m = a;
+  }
+#pragma unroll
+  for (int q = 0; q < KR; ++q) {
+    const bool in = q * L + sub < c.k && ri[q] >= 0;
+    if (c.softmax) e[q] = in ? exp_neg(rx[q] - m) : 0.0f;
+    else e[q] = in ? exp_neg(fminf(rx[q], 0.0f) - a) / (1.0f + exp_neg(-fabsf(rx[q]))) : 0.0f;
+    total += e[q];
+  }
+  total = row_sum<L>(total);
+  const float f = c.renorm ? (total > 0.0f ? c.scale / total : 0.0f) : c.softmax ? c.scale * inv : c.scale;
+#pragma unroll
+  for (int q = 0; q < KR; ++q) {
+    const int j = q * L + sub;
+    if (ok && j < c.k) {
+      weights[t * c.k + j] = e[q] * f;
+      ids[t * c.k + j] = ri[q];
+    }
+  }
+}
+
+// The row's incoming gradients are spread over its E experts in LDS (zeros,
+// then one write per selected expert); each lane then reads its own V.
+template <typename T, int L, int V, bool WHOLE, int KR>
+__global__ __launch_bounds__(kThreads) void k_group_gate_backward(const float* __restrict__ dweights,
+                                                                 const float* __restrict__ weights,
+                                                                 const int32_t* __restrict__ ids,
+                                                                 const T* __restrict__ logits, int64_t tokens,
+                                                                 Choice c, T* __restrict__ dlogits) {
+  __shared__ float spread[kThreads / L][L * V];
+  const int sub = threadIdx.x % L;
+  const int64_t t = (int64_t)blockIdx.x * (kThreads / L) + threadIdx.x / L;
+  const bool ok = t < tokens, all = c.softmax && !c.renorm;
+  float* mine = spread[threadIdx.x / L];
+  const T* row = logits + (ok ? t : 0) * c.E;
+  float w[KR], g[KR], x[V];
+  int id[KR];
+  float inner = 0.0f;
+  if (all) load_logits<T, V, WHOLE>(row, sub * V, c.E, ok, x);
+#pragma unroll
+  for (int q = 0; q < KR; ++q) {
+    const int j = q * L + sub;
+    const bool in = ok && j < c.k;
+    id[q] = in ? ids[t * c.k + j] : -1;
+    if (id[q] >= c.E) id[q] = -1;
+    w[q] = id[q] >= 0 ? weights[t * c.k + j] : 0.0f;
+    g[q] = id[q] >= 0 ? dweights[t * c.k + j] : 0.0f;
+    inner += w[q] * g[q];
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) mine[sub * V + i] = 0.0f;
+  inner = row_sum<L>(inner);
+  wave_fence();
+  const float mean = c.renorm ? inner / c.scale : 0.0f;
+#pragma unroll
+  for (int q = 0; q < KR; ++q)
+    if (id[q] >= 0) {
+      float d = w[q] * (g[q] - mean);
+      if (all) {
+        d = c.scale * g[q];
+      } else if (!c.softmax) {
+        const float l = load1(row + id[q]), n = exp_neg(-fabsf(l));
+        d *= (l >= 0.0f ? n : 1.0f) / (1.0f + n);  // 1 - sigmoid(l)
+      }
+      mine[id[q]] = d;
+    }
+  wave_fence();
+  float d[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) d[i] = mine[sub * V + i];
+  if (all) {
+    float top = -kInf, total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) top = fmaxf(top, x[i]);  // drops NaN
+    top = row_maxf<L>(top);
+    const float m = top > -kInf ? top : 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      x[i] = x[i] > -kInf ? exp_neg(x[i] - m) : 0.0f;
+      total += x[i];
+    }
+    total = row_sum<L>(total);
+    const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) d[i] = x[i] * inv * (d[i] - inner);
+  }
+  if (ok) store_grads<T, V, WHOLE>(dlogits + t * c.E, sub * V, c.E, d);
+}
+
+template <typename T, int L, int V, bool WHOLE>
+void launch_gate(const T* logits, const float* bias, int64_t tokens, Choice c, float* weights, int32_t* ids,
+                 hipStream_t s) {
+  constexpr int64_t per = kThreads / L, most = bsqh::max_blocks(kThreads) * per;
+  // groups that whole lanes hold, a power of two of them: exchanged between lanes, else through LDS
+  c.lanes = 0;
+  if (L == 16 && c.E == L * V && c.size % V == 0 && ((c.size / V) & (c.size / V - 1)) == 0) c.lanes = c.size / V;
+  for (; tokens > 0; tokens -= most, logits += most * c.E, weights += most * c.k, ids += most * c.k) {
+    const int64_t n = tokens < most ? tokens : most;
+    const unsigned grid = (unsigned)((n + per - 1) / per);
+    if (c.k < L)
+      hipLaunchKernelGGL((k_group_gate<T, L, V, WHOLE, 1>), dim3(grid), dim3(kThreads), 0, s, logits, bias, n, c,
+                         weights, ids);
+    else
+      hipLaunchKernelGGL((k_group_gate<T, L, V, WHOLE, 64 / L + 1>), dim3(grid), dim3(kThreads), 0, s, logits, bias, n,
+                         c, weights, ids);
+  }
+}
+
+template <typename T, int L, int V, bool WHOLE>
+void launch_back(const float* dw, const float* w, const int32_t* ids, const T* logits, int64_t tokens, Choice c,
+                 T* dlogits, hipStream_t s) {
+  constexpr int64_t per = kThreads / L, most = bsqh::max_blocks(kThreads) * per;
+  for (; tokens > 0;
+       tokens -= most, dw += most * c.k, w += most * c.k, ids += most * c.k, logits += most * c.E, dlogits += most * c.E) {
+    const int64_t n = tokens < most ? tokens : most;
+    const unsigned grid = (unsigned)((n + per - 1) / per);
+    if (c.k <= L)
+      hipLaunchKernelGGL((k_group_gate_backward<T, L, V, WHOLE, 1>), dim3(grid), dim3(kThreads), 0, s, dw, w, ids,
+                         logits, n, c, dlogits);
+    else
+      hipLaunchKernelGGL((k_group_gate_backward<T, L, V, WHOLE, 64 / L>), dim3(grid), dim3(kThreads), 0, s, dw, w, ids,
+                         logits, n, c, dlogits);
+  }
+}
+
+int check(int dtype, int64_t tokens, int64_t E, int64_t k, int score, int renormalize, float scale) {
+  BSQ_REQUIRE(dtype == BSQ_F32 || dtype == BSQ_BF16, BSQ_E_DTYPE);
+  BSQ_REQUIRE((score == BSQ_SCORE_SIGMOID || score == BSQ_SCORE_SOFTMAX) && (renormalize == 0 || renormalize == 1),
+              BSQ_E_ENUM);
+  BSQ_REQUIRE(scale >= 0x1p-64f && scale <= 0x1p64f, BSQ_E_ENUM);  // NaN fails too
+  BSQ_REQUIRE(tokens >= 0 && tokens < (int64_t)1 << 31 && E >= 1 && E <= 1024 && k >= 1 && k <= 64 && k <= E,
+              BSQ_E_SHAPE);
+  return BSQ_OK;
+}
+
+}  // namespace
+
+extern "C" int bsq_moe_gate_grouped(const void* logits, int dtype, const float* bias, int64_t tokens, int64_t E,
+                                    int64_t k, int64_t groups, int64_t group_k, int group_top, int score,
+                                    int renormalize, float scale, float* weights, int32_t* topk_ids,
+                                    bsq_stream_t stream) {
+  const int st = check(dtype, tokens, E, k, score, renormalize, scale);
+  if (st != BSQ_OK) return st;
+  BSQ_REQUIRE(group_top == 1 || group_top == 2, BSQ_E_ENUM);
+  BSQ_REQUIRE(groups >= 1 && groups <= kMaxGroups && E % groups == 0 && group_k >= 1 && group_k <= groups &&
+                  k <= group_k * (E / groups),
+              BSQ_E_SHAPE);
+  if (tokens == 0) return BSQ_OK;
+  BSQ_REQUIRE(logits && weights && topk_ids, BSQ_E_NULL);
+  BSQ_REQUIRE(bsqh::aligned16(logits) && (((uintptr_t)weights | (uintptr_t)topk_ids | (uintptr_t)bias) & 3) == 0,
+              BSQ_E_ALIGN);
+  hipStream_t s = bsqh::as_stream(stream);
+  // all groups kept: no choice of groups
+  const Choice c = {(int)E, (int)k, group_k == groups ? 1 : (int)groups, (int)(E / groups), (int)group_k, group_top, 0,
+                    score == BSQ_SCORE_SOFTMAX, renormalize == 1, scale};
+  if (dtype == BSQ_F32) {
+    BSQ_GATE_SHAPES(launch_gate, float, static_cast<const float*>(logits), bias, tokens, c, weights, topk_ids, s);
+  } else {
+    BSQ_GATE_SHAPES(launch_gate, uint16_t, static_cast<const uint16_t*>(logits), bias, tokens, c, weights, topk_ids, s);
+  }
+  return bsqh::launch_status();
+}
+
+extern "C" int bsq_moe_gate_grouped_backward(const float* dweights, const float* weights, const int32_t* topk_ids,
+                                             const void* logits, int dtype, int64_t tokens, int64_t E, int64_t k,
+                                             int score, int renormalize, float scale, void* dlogits,
+                                             bsq_stream_t stream) {
+  const int st = check(dtype, tokens, E, k, score, renormalize, scale);
+  if (st != BSQ_OK || tokens == 0) return st;
+  BSQ_REQUIRE(dweights && weights && topk_ids && dlogits && logits, BSQ_E_NULL);
+  BSQ_REQUIRE(bsqh::aligned16(logits) && bsqh::aligned16(dlogits) &&
+                  (((uintptr_t)weights | (uintptr_t)dweights | (uintptr_t)topk_ids) & 3) == 0,
+              BSQ_E_ALIGN);
+  hipStream_t s = bsqh::as_stream(stream);
+  const Choice c = {(int)E, (int)k, 1, (int)E, 1, 1, 0, score == BSQ_SCORE_SOFTMAX, renormalize == 1, scale};
+  if (dtype == BSQ_F32) {
+    BSQ_GATE_SHAPES(launch_back, float, dweights, weights, topk_ids, static_cast<const float*>(logits), tokens, c,
+                    static_cast<float*>(dlogits), s);
+  } else {
+    BSQ_GATE_SHAPES(launch_back, uint16_t, dweights, weights, topk_ids, static_cast<const uint16_t*>(logits), tokens, c,
+                    static_cast<uint16_t*>(dlogits), s);
+  }
+  return bsqh::launch_status();
+}

@@ -44,6 +44,29 @@ def _ws(nbytes, device):
     return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
 
 
+class _Here:
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_HERE = _Here()
+
+
+def _on(first, *others):
+    """A context in which `first`'s device is the current one (and its stream the
+    one that _stream() gives); all tensors must be on it."""
+    index = first.device.index
+    for t in others:
+        if t is not None and t.device.index != index:
+            raise BsqError("all tensors must be on one device")
+    if _raw_device is not None and _raw_device() == index:
+        return _HERE
+    return torch.cuda.device(index)
+
+
 def quantize_nvfp4(x, mode="tensor", outer_in=None, four_over_six=False):
     """Round-to-nearest NVFP4 of x [B, R, C] or [R, C] (float32 or bfloat16);
     four_over_six picks each block's scale from the 6- and 4-mapping candidates.
@@ -398,6 +421,71 @@ def moe_gate_backward(dweights, weights, topk_ids, logits, renormalize=True):
     check(lib.bsq_moe_gate_backward(dweights.data_ptr(), weights.data_ptr(), topk_ids.data_ptr(), logits.data_ptr(),
                                     dt, T, E, k, 1 if renormalize else 0, dlogits.data_ptr(), _stream()),
           "bsq_moe_gate_backward")
+    return dlogits
+
+
+_SCORE = {"sigmoid": 0, "softmax": 1}
+
+
+def _score(score, what):
+    _need(score in _SCORE, what + ": score must be 'sigmoid' or 'softmax'")
+    return _SCORE[score]
+
+
+def moe_gate_grouped(logits, k, bias=None, groups=1, group_k=None, group_top=2, score="sigmoid", renormalize=True,
+                     scale=1.0):
+    """The k experts of each token by scores s, a balancing bias and groups:
+    logits [T, E] (float32 or bfloat16) -> (weights f32 [T, k], topk_ids int32
+    [T, k]). s is the sigmoid of the logits or their softmax; the keys s + bias
+    (f32 [E] or None) choose: the group_k groups (all unless given) of E / groups
+    neighbouring experts with the largest sums of their group_top best keys,
+    then the k largest keys in them, largest first, ties to the lowest index.
+    weights: scale * s, with renormalize divided by the selected scores' sum.
+    Logits of -inf (and NaN) are masked; a slot that finds no expert left gets
+    id -1 and weight 0. moe_gate_grouped_backward is the gradient."""
+    lib = load_library()
+    _dev(logits, bias)
+    _need(logits.dim() == 2, "moe_gate_grouped: logits must be [tokens, experts]")
+    T, E = logits.shape
+    dt = _dtype(logits, "logits")
+    group_k = groups if group_k is None else group_k
+    _need(1 <= groups <= 64 and E % groups == 0 and 1 <= group_k <= groups,
+          "moe_gate_grouped: groups must divide the experts (64 at most), 1 <= group_k <= groups")
+    _need(1 <= k <= min(64, group_k * (E // groups)), "moe_gate_grouped: k must be in [1, min(64, experts of group_k groups)]")
+    _need(bias is None or (bias.dtype == torch.float32 and bias.numel() == E),
+          "moe_gate_grouped: bias must be float32 [experts]")
+    sc = _score(score, "moe_gate_grouped")
+    weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    with _on(logits, bias):
+        check(lib.bsq_moe_gate_grouped(logits.data_ptr(), dt, _ptr(bias), T, E, k, groups, group_k, group_top, sc,
+                                       1 if renormalize else 0, scale, weights.data_ptr(), ids.data_ptr(), _stream()),
+              "bsq_moe_gate_grouped")
+    return weights, ids
+
+
+def moe_gate_grouped_backward(dweights, weights, topk_ids, logits, score="sigmoid", renormalize=True, scale=1.0):
+    """Gradient of moe_gate_grouped's weights to its logits, the selection held
+    fixed: dweights f32 [T, k] with moe_gate_grouped's outputs, input, score,
+    renormalize and scale -> dlogits [T, E] of logits' type (every element
+    written). The bias only selects and has no gradient."""
+    lib = load_library()
+    _dev(dweights, weights, topk_ids, logits)
+    _need(logits.dim() == 2 and weights.dim() == 2,
+          "moe_gate_grouped_backward: logits [tokens, experts], weights [tokens, k]")
+    T, E = logits.shape
+    k = weights.shape[1]
+    dt = _dtype(logits, "logits")
+    _need(weights.shape == (T, k) and dweights.shape == (T, k) and topk_ids.shape == (T, k),
+          "moe_gate_grouped_backward: dweights, weights and topk_ids must be [tokens, k]")
+    _need(dweights.dtype == torch.float32 and weights.dtype == torch.float32 and topk_ids.dtype == torch.int32,
+          "moe_gate_grouped_backward: dweights and weights must be float32, topk_ids int32")
+    sc = _score(score, "moe_gate_grouped_backward")
+    dlogits = torch.empty_like(logits)
+    with _on(logits, dweights, weights, topk_ids):
+        check(lib.bsq_moe_gate_grouped_backward(dweights.data_ptr(), weights.data_ptr(), topk_ids.data_ptr(),
+                                                logits.data_ptr(), dt, T, E, k, sc, 1 if renormalize else 0, scale,
+                                                dlogits.data_ptr(), _stream()), "bsq_moe_gate_grouped_backward")
     return dlogits
 
 

@@ -429,6 +429,47 @@ int bsq_moe_gate_backward(const float* dweights, const float* weights, const int
                           int renormalize, void* dlogits, bsq_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Expert selection by scores, a balancing bias and groups of experts, and the
+ * gradient of its weights (bsq_moe_gate selects by the logits alone).
+ *
+ * bsq_moe_gate_grouped
+ *   logits   [tokens, E] of `dtype` (F32 or BF16); -inf and NaN are masked:
+ *            never selected, score 0.
+ *   score    BSQ_SCORE_SIGMOID: s_i = 1 / (1 + e^-l_i); BSQ_SCORE_SOFTMAX: the
+ *            softmax over all unmasked logits of the row.
+ *   bias     FP32 [E] or NULL (zeros): keys c_i = s_i + bias_i choose, the
+ *            weights do not see it. -inf and NaN mask the expert's choice.
+ *   groups   E / groups neighbouring experts each. A group is worth the sum of
+ *            its group_top (1 or 2) largest keys (of one, if it has one
+ *            unmasked expert); the group_k best groups stay, ties to the
+ *            lowest index. groups 1: no restriction.
+ *   The k largest keys of the groups that stay, largest first, ties to the
+ *   lowest index. The order of keys and groups is that of their values in
+ *   float64. Slots past the last unmasked expert get id -1 and weight 0.
+ *   weights  FP32 [tokens, k]: scale * s_j, or with renormalize 1
+ *            scale * s_j / (sum of the row's selected scores), in float32.
+ *   topk_ids int32 [tokens, k] (a row with a -1 is no input for bsq_route).
+ *   A softmax row with a logit of +inf gives unspecified weights and ids
+ *   (distinct, in range).
+ * bsq_moe_gate_grouped_backward: gradient of sum dweights * weights to the
+ *   logits, the selection held fixed (the bias has none). dweights, weights,
+ *   topk_ids, logits as above, ids of a row distinct (ids outside [0, E) add
+ *   nothing); dlogits [tokens, E] of `dtype`, every element written.
+ * 1 <= E <= 1024, 1 <= k <= min(64, group_k * E / groups), groups <= 64 and a
+ * divisor of E, tokens < 2^31, 2^-64 <= scale <= 2^64. logits and dlogits
+ * 16-byte aligned, the others 4.
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, ENUM (score, renormalize, group_top,
+ * scale), LAUNCH.
+ * ---------------------------------------------------------------------- */
+typedef enum { BSQ_SCORE_SIGMOID = 0, BSQ_SCORE_SOFTMAX = 1 } bsq_score;
+int bsq_moe_gate_grouped(const void* logits, int dtype, const float* bias, int64_t tokens, int64_t E, int64_t k,
+                         int64_t groups, int64_t group_k, int group_top, int score, int renormalize, float scale,
+                         float* weights, int32_t* topk_ids, bsq_stream_t stream);
+int bsq_moe_gate_grouped_backward(const float* dweights, const float* weights, const int32_t* topk_ids,
+                                  const void* logits, int dtype, int64_t tokens, int64_t E, int64_t k, int score,
+                                  int renormalize, float scale, void* dlogits, bsq_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * A whole expert layer for a few tokens (decode), weights in NVFP4 and
  * activations unquantized:
  *   out[t] = sum_j topk_weights[t, j] W2_e (silu(G) * U),  (G; U) = W13_e x[t],
