@@ -67,6 +67,11 @@ SIGNATURES = {
     "bsq_swiglu_quantize_int8": (c_int, [c_vp, c_int, c_i64, c_i64, c_vp, c_vp, c_vp]),
     "bsq_gemm_int8": (c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_int, c_vp]),
     "bsq_linear_int8_workspace": (c_size, [c_i64, c_i64]),
+    "bsq_quantize_int4": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_int, c_vp, c_vp, c_vp, c_vp]),
+    "bsq_dequantize_int4": (c_int, [c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_int, c_vp]),
+    "bsq_linear_int4_workspace": (c_size, [c_i64, c_i64, c_i64, c_i64, c_int]),
+    "bsq_linear_int4": (c_int, [c_vp, c_int, c_vp, c_vp, c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_vp, c_int, c_vp,
+                                c_size, c_vp]),
     "bsq_linear_int8": (c_int, [c_vp, c_int, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_int, c_vp, c_size, c_vp]),
 }
 

@@ -602,6 +602,78 @@ def linear_int8(x, b_codes, b_scales, bias=None, out_dtype=None):
     return out
 
 
+def quantize_int4(w, group=128, symmetric=False):
+    """Weights w [N, K] (float32 or bfloat16) in 4-bit integers with a scale and
+    a zero point for each group (32, 64 or 128) of neighbours along K:
+    (codes u8 [N, K/2], scales bf16 [N, K/group], zeros u8 [N, K/group] or, with
+    symmetric, None). They stand for (q - z) * s, z = 8 without zeros."""
+    lib = load_library()
+    _dev(w)
+    _need(w.dim() == 2, "quantize_int4: w must be [N, K]")
+    N, K = w.shape
+    dt = _dtype(w, "w")
+    _need(group in (32, 64, 128) and K >= group and K % group == 0,
+          "quantize_int4: group must be 32, 64 or 128 and divide K")
+    codes = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
+    scales = torch.empty((N, K // group), dtype=torch.bfloat16, device=w.device)
+    zeros = None if symmetric else torch.empty((N, K // group), dtype=torch.uint8, device=w.device)
+    with _on(w):
+        check(lib.bsq_quantize_int4(w.data_ptr(), dt, N, K, group, 1 if symmetric else 0, codes.data_ptr(),
+                                    scales.data_ptr(), _ptr(zeros), _stream()), "bsq_quantize_int4")
+    return codes, scales, zeros
+
+
+def _int4_group(codes, scales, zeros, what):
+    """(N, K, group) of 4-bit weights."""
+    _need(codes.dim() == 2 and codes.dtype == torch.uint8 and scales.dim() == 2 and scales.dtype == torch.bfloat16
+          and scales.shape[0] == codes.shape[0] and scales.shape[1] > 0,
+          what + ": uint8 codes [N, K/2] with bfloat16 scales [N, K/group]")
+    _need(zeros is None or (zeros.dtype == torch.uint8 and zeros.shape == scales.shape),
+          what + ": zeros must be uint8 [N, K/group]")
+    N, K = codes.shape[0], 2 * codes.shape[1]
+    group = K // scales.shape[1]
+    _need(group in (32, 64, 128) and group * scales.shape[1] == K, what + ": groups must be of 32, 64 or 128")
+    return N, K, group
+
+
+def dequantize_int4(codes, scales, zeros=None, out_dtype=torch.float32):
+    """The values [N, K] that 4-bit groups stand for, (q - z) * s."""
+    lib = load_library()
+    _dev(codes, scales, zeros)
+    N, K, group = _int4_group(codes, scales, zeros, "dequantize_int4")
+    _need(out_dtype in _OUT, "out_dtype must be float32 or bfloat16")
+    out = torch.empty((N, K), dtype=out_dtype, device=codes.device)
+    with _on(codes, scales, zeros):
+        check(lib.bsq_dequantize_int4(codes.data_ptr(), scales.data_ptr(), _ptr(zeros), N, K, group, out.data_ptr(),
+                                      _OUT[out_dtype], _stream()), "bsq_dequantize_int4")
+    return out
+
+
+def linear_int4(x, codes, scales, zeros=None, bias=None, out_dtype=None):
+    """y [M, N] = x W^T + bias of unquantized activations x [M, K] (float32 or
+    bfloat16) and weights in 4-bit groups as quantize_int4 returns them; bias
+    float32 [N] or None; out_dtype is x's unless given. One token or few: bound
+    by reading the codes once."""
+    lib = load_library()
+    _dev(x, codes, scales, zeros, bias)
+    _need(x.dim() == 2, "linear_int4: x must be [M, K]")
+    dt = _dtype(x, "x")
+    N, K, group = _int4_group(codes, scales, zeros, "linear_int4")
+    M = x.shape[0]
+    out_dtype = out_dtype or x.dtype
+    _need(x.shape[1] == K, "linear_int4: x and the weights must share K")
+    _need(bias is None or (bias.dtype == torch.float32 and bias.numel() == N), "linear_int4: bias must be float32 [N]")
+    _need(out_dtype in _OUT, "out_dtype must be float32 or bfloat16")
+    out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+    with _on(x, codes, scales, zeros, bias):
+        wsb = lib.bsq_linear_int4_workspace(M, N, K, group, dt)
+        ws = _ws(wsb, x.device) if wsb else None
+        check(lib.bsq_linear_int4(x.data_ptr(), dt, codes.data_ptr(), scales.data_ptr(), _ptr(zeros), group, _ptr(bias),
+                                  M, N, K, out.data_ptr(), _OUT[out_dtype], _ptr(ws), wsb, _stream()),
+              "bsq_linear_int4")
+    return out
+
+
 def rht_s2f6_encode(x, signs):
     """Combine-codec sender: x [R, C] (float32 or bfloat16, C % 32 == 0) ->
     (codes u8 [R, C] two's-complement S2F6, scales u8 [R, C/32] UE8M0) of the

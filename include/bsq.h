@@ -545,6 +545,44 @@ int bsq_linear_int8(const void* x, int dtype, const int8_t* b_codes, const float
                     size_t ws_bytes, bsq_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Dense products with weights in 4-bit integers, a scale (and a zero point) for
+ * each group of 32, 64 or 128 neighbours along K; activations unquantized.
+ *   w[n, k] = (q[n, k] - z[n, k / group]) * s[n, k / group]
+ * codes  [N, K/2] u8, q in 0..15, element 2k in the low nibble.
+ * scales [N, K/group], bf16 bits. zeros u8 [N, K/group] in 0..15, or NULL: 8.
+ *
+ * bsq_quantize_int4: w [N, K] of `dtype` (F32 or BF16). With the quotients as
+ *   if exact and rounded half to even:
+ *   symmetric 1: s = bf16(f32(max|w| / 7)), q = clamp(rint(w / s) + 8, 0, 15);
+ *     zeros is not written and may be NULL.
+ *   symmetric 0: lo = min(w, 0), hi = max(w, 0), s = bf16(f32((hi - lo) / 15)),
+ *     z = rint(-lo / s), q = clamp(rint(w / s) + z, 0, 15).
+ *   s is 1 where it would be below 2^-126 (all values of the group are then 0),
+ *   NaN where the group holds a NaN or an infinity (codes unspecified).
+ * bsq_dequantize_int4: out [N, K] of out_dtype, (q - z) * s exact in float32,
+ *   rounded to nearest even in bf16.
+ * bsq_linear_int4: out[m, n] = sum_k x[m, k] w[n, k] + bias[n], x [M, K] of
+ *   `dtype`, bias FP32 [N] or NULL, out [M, N] of out_dtype. x (F32 too) and
+ *   the integers q - z enter unrounded; sums over a group and over groups are
+ *   float32, and the output is rounded once. A row of x with a NaN or an
+ *   infinity gives no finite output; sums of |x| * 15 over a group stay below
+ *   2^128. ws bsq_linear_int4_workspace() bytes (0, and ws may be NULL, for
+ *   few rows; 256 MiB at most).
+ * group <= K <= 32768, K % group == 0, N and M < 2^31. x, w, codes and ws (and
+ * bsq_dequantize_int4's out) 16-byte aligned, out and scales to their type,
+ * bias 4. Codes of a batch past M, N or K are neither read nor written.
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, ENUM, WORKSPACE, LAUNCH.
+ * ---------------------------------------------------------------------- */
+int bsq_quantize_int4(const void* w, int dtype, int64_t N, int64_t K, int64_t group, int symmetric, uint8_t* codes,
+                      uint16_t* scales, uint8_t* zeros, bsq_stream_t stream);
+int bsq_dequantize_int4(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, int64_t N, int64_t K,
+                        int64_t group, void* out, int out_dtype, bsq_stream_t stream);
+size_t bsq_linear_int4_workspace(int64_t M, int64_t N, int64_t K, int64_t group, int dtype);
+int bsq_linear_int4(const void* x, int dtype, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros,
+                    int64_t group, const float* bias, int64_t M, int64_t N, int64_t K, void* out, int out_dtype,
+                    void* ws, size_t ws_bytes, bsq_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Combine codec ("Quantized communications": before the combine exchange an
  * expert output row is rotated by a 32-dimensional random Hadamard transform
  * and quantized to block-scaled S2F6, one UE8M0 scale per 32 values, 8.25
