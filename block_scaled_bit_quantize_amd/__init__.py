@@ -16,7 +16,8 @@ from .ops import (BF16, F32, MXFP8, NVFP4, OUTER_GIVEN, OUTER_ROW, OUTER_TENSOR,
                   rht_s2f6_combine, rht_s2f6_encode, rng_bits16, mfma_rate_probe, route, route_noalloc, gemm_nvfp4_inreg_scale, swiglu_quantize_nvfp4,
                   gemm_int8, linear_int8, moe_few_tokens_nvfp4, moe_gate, moe_gate_backward, moe_gate_grouped,
                   moe_gate_grouped_backward, quantize_int8,
-                  swiglu_quantize_int8, quantize_int4, dequantize_int4, linear_int4)
+                  swiglu_quantize_int8, quantize_int4, dequantize_int4, linear_int4, token_logprobs,
+                  token_logprobs_backward)
 
 __all__ = [
     "BsqError", "library_path", "load_library",
@@ -28,4 +29,5 @@ __all__ = [
     "moe_gate", "moe_gate_backward", "moe_gate_grouped", "moe_gate_grouped_backward", "moe_few_tokens_nvfp4",
     "quantize_int8", "swiglu_quantize_int8", "gemm_int8", "linear_int8",
     "quantize_int4", "dequantize_int4", "linear_int4",
+    "token_logprobs", "token_logprobs_backward",
 ]

@@ -72,6 +72,10 @@ SIGNATURES = {
     "bsq_linear_int4_workspace": (c_size, [c_i64, c_i64, c_i64, c_i64, c_int]),
     "bsq_linear_int4": (c_int, [c_vp, c_int, c_vp, c_vp, c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_vp, c_int, c_vp,
                                 c_size, c_vp]),
+    "bsq_token_logprobs_workspace": (c_size, [c_i64, c_i64, c_i64, c_int]),
+    "bsq_token_logprobs": (c_int, [c_vp, c_int, c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_size,
+                                   c_vp]),
+    "bsq_token_logprobs_backward": (c_int, [c_vp, c_vp, c_vp, c_int, c_vp, c_vp, c_vp, c_i64, c_i64, c_vp, c_vp]),
     "bsq_linear_int8": (c_int, [c_vp, c_int, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_int, c_vp, c_size, c_vp]),
 }
 

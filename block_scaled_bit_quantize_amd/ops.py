@@ -674,6 +674,59 @@ def linear_int4(x, codes, scales, zeros=None, bias=None, out_dtype=None):
     return out
 
 
+def token_logprobs(logits, targets, top=0):
+    """Log probabilities of given tokens: logits [T, V] (float32 or bfloat16,
+    -inf masked), targets int64 [T] (outside [0, V): padding, log probability 0)
+    -> (logprobs f32 [T], entropy f32 [T], stats f32 [T, 2], top_logprobs f32
+    [T, top], top_ids int32 [T, top]), the last two None without `top`: the
+    largest alternatives, ties to the lowest index, id -1 where no unmasked
+    logit is left. stats (the row's maximum and log sum e^(x - maximum), which
+    add up to the log-sum-exp) is for token_logprobs_backward, the gradient."""
+    lib = load_library()
+    _dev(logits, targets)
+    _need(logits.dim() == 2, "token_logprobs: logits must be [tokens, vocabulary]")
+    T, V = logits.shape
+    dt = _dtype(logits, "logits")
+    _need(targets.dtype == torch.int64 and targets.shape == (T,), "token_logprobs: targets must be int64 [tokens]")
+    _need(1 <= V <= 1 << 20 and 0 <= top <= min(V, 64), "token_logprobs: 1 <= vocabulary <= 2^20, 0 <= top <= min(vocabulary, 64)")
+    f32 = lambda *shape: torch.empty(shape, dtype=torch.float32, device=logits.device)
+    logprobs, entropy, stats = f32(T), f32(T), f32(T, 2)
+    top_lp = f32(T, top) if top else None
+    top_ids = torch.empty((T, top), dtype=torch.int32, device=logits.device) if top else None
+    with _on(logits, targets):
+        wsb = lib.bsq_token_logprobs_workspace(T, V, top, dt)
+        ws = _ws(wsb, logits.device) if wsb else None
+        check(lib.bsq_token_logprobs(logits.data_ptr(), dt, targets.data_ptr(), T, V, top, logprobs.data_ptr(),
+                                     entropy.data_ptr(), stats.data_ptr(), _ptr(top_lp), _ptr(top_ids), _ptr(ws), wsb,
+                                     _stream()), "bsq_token_logprobs")
+    return logprobs, entropy, stats, top_lp, top_ids
+
+
+def token_logprobs_backward(dlogprobs, dentropy, logits, targets, stats, entropy):
+    """Gradient of token_logprobs' logprobs and entropy to its logits: dlogprobs
+    and dentropy f32 [T] (either may be None) with token_logprobs' inputs and
+    outputs -> dlogits [T, V] of logits' type (every element written, 0 at
+    masked logits)."""
+    lib = load_library()
+    _dev(dlogprobs, dentropy, logits, targets, stats, entropy)
+    _need(logits.dim() == 2, "token_logprobs_backward: logits must be [tokens, vocabulary]")
+    T, V = logits.shape
+    dt = _dtype(logits, "logits")
+    _need(dlogprobs is not None or dentropy is not None, "token_logprobs_backward: dlogprobs or dentropy must be given")
+    for t, shape in ((dlogprobs, (T,)), (dentropy, (T,)), (stats, (T, 2)), (entropy, (T,))):
+        _need(t is None or (t.dtype == torch.float32 and t.shape == shape),
+              "token_logprobs_backward: dlogprobs, dentropy and entropy must be float32 [tokens], stats [tokens, 2]")
+    _need(targets.dtype == torch.int64 and targets.shape == (T,),
+          "token_logprobs_backward: targets must be int64 [tokens]")
+    _need(1 <= V <= 1 << 20, "token_logprobs_backward: 1 <= vocabulary <= 2^20")
+    dlogits = torch.empty_like(logits)
+    with _on(logits, dlogprobs, dentropy, targets, stats, entropy):
+        check(lib.bsq_token_logprobs_backward(_ptr(dlogprobs), _ptr(dentropy), logits.data_ptr(), dt,
+                                              targets.data_ptr(), stats.data_ptr(), entropy.data_ptr(), T, V,
+                                              dlogits.data_ptr(), _stream()), "bsq_token_logprobs_backward")
+    return dlogits
+
+
 def rht_s2f6_encode(x, signs):
     """Combine-codec sender: x [R, C] (float32 or bfloat16, C % 32 == 0) ->
     (codes u8 [R, C] two's-complement S2F6, scales u8 [R, C/32] UE8M0) of the

@@ -583,6 +583,41 @@ int bsq_linear_int4(const void* x, int dtype, const uint8_t* codes, const uint16
                     void* ws, size_t ws_bytes, bsq_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Log probabilities of given tokens, entropies and the largest alternatives of
+ * rows of logits (sampling, and the policy's update after it), with the
+ * gradient of the first two.
+ *
+ * bsq_token_logprobs
+ *   logits   [tokens, V] of `dtype` (F32 or BF16); -inf is masked: probability
+ *            0. A row with a NaN or +inf gives NaN (top_ids as described).
+ *   targets  int64 [tokens]; outside [0, V) (padding): log probability 0.
+ *   logprobs FP32 [tokens]: log p of the target (-inf if it is masked).
+ *   entropy  FP32 [tokens]: -sum p log p (0 for a row without unmasked logit).
+ *   stats    FP32 [tokens, 2]: the row's maximum and the logarithm of
+ *            sum e^(x - maximum); their sum is the log-sum-exp. Both 0 for a
+ *            row without unmasked logit.
+ *   top_logprobs FP32, top_ids int32 [tokens, top]: the largest logits' log
+ *            probabilities, largest first, ties to the lowest index; -inf and
+ *            id -1 where no unmasked logit is left (NaN is none). May be NULL
+ *            with top 0.
+ *   Float32 sums. ws bsq_token_logprobs_workspace() bytes (may be 0).
+ * bsq_token_logprobs_backward: gradient of sum dlogprobs * logprobs +
+ *   sum dentropy * entropy to the logits; dlogprobs and dentropy FP32 [tokens],
+ *   either may be NULL (zeros); targets, stats and entropy as above. dlogits
+ *   [tokens, V] of `dtype`, every element written, 0 at masked logits.
+ * 1 <= V <= 2^20, tokens < 2^31, 0 <= top <= min(V, 64). logits, dlogits and ws
+ * 16-byte aligned, targets 8, the others 4.
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, WORKSPACE, LAUNCH.
+ * ---------------------------------------------------------------------- */
+size_t bsq_token_logprobs_workspace(int64_t tokens, int64_t V, int64_t top, int dtype);
+int bsq_token_logprobs(const void* logits, int dtype, const int64_t* targets, int64_t tokens, int64_t V, int64_t top,
+                       float* logprobs, float* entropy, float* stats, float* top_logprobs, int32_t* top_ids, void* ws,
+                       size_t ws_bytes, bsq_stream_t stream);
+int bsq_token_logprobs_backward(const float* dlogprobs, const float* dentropy, const void* logits, int dtype,
+                                const int64_t* targets, const float* stats, const float* entropy, int64_t tokens,
+                                int64_t V, void* dlogits, bsq_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Combine codec ("Quantized communications": before the combine exchange an
  * expert output row is rotated by a 32-dimensional random Hadamard transform
  * and quantized to block-scaled S2F6, one UE8M0 scale per 32 values, 8.25
