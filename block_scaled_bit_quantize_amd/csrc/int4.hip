@@ -107,32 +107,33 @@ __global__ __launch_bounds__(kQThreads) void k_quant_int4(const T* __restrict__ 
   }
 }
 
-// Sixteen values of a lane.
+// Pieces of 16 bytes of the output, neighbouring lanes side by side: bound by
+// memory (a lane's four pieces side by side took 22 us for 2048 x 7168 float32).
+constexpr int kDPieces = 4;
 template <typename T>
-__global__ __launch_bounds__(kQThreads) void k_dequant_int4(const u32x2* __restrict__ codes,
+__global__ __launch_bounds__(kQThreads) void k_dequant_int4(const uint8_t* __restrict__ codes,
                                                            const uint16_t* __restrict__ scales,
-                                                           const uint8_t* __restrict__ zeros, int64_t units, int lanes,
+                                                           const uint8_t* __restrict__ zeros, int64_t pieces, int shift,
                                                            T* __restrict__ out) {
-  const int64_t u = (int64_t)blockIdx.x * kQThreads + threadIdx.x;
-  if (u >= units) return;
-  const u32x2 c = codes[u];
-  const int64_t g = u / lanes;
-  const float s = from_bf16(scales[g]), z = zeros ? (float)zeros[g] : 8.0f;
-  float v[16];
+  constexpr int E = 16 / (int)sizeof(T);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = ((float)(c[i / 8] >> (4 * (i % 8)) & 15u) - z) * s;
-  if constexpr (sizeof(T) == 4) {
-    f32x4* to = reinterpret_cast<f32x4*>(out + u * 16);
+  for (int i = 0; i < kDPieces; ++i) {
+    const int64_t p = ((int64_t)blockIdx.x * kDPieces + i) * kQThreads + threadIdx.x;
+    if (p >= pieces) return;
+    uint32_t c = 0;
+    __builtin_memcpy(&c, __builtin_assume_aligned(codes + p * (E / 2), E / 2), E / 2);
+    const int64_t g = p * E >> shift;
+    const float s = from_bf16(scales[g]), z = zeros ? (float)zeros[g] : 8.0f;
+    float v[E];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) to[i] = (f32x4){v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
-  } else {
-    bf16x8* to = reinterpret_cast<bf16x8*>(out + u * 16);
+    for (int j = 0; j < E; ++j) v[j] = ((float)(c >> (4 * j) & 15u) - z) * s;
+    if constexpr (E == 4) {
+      *reinterpret_cast<f32x4*>(out + p * E) = (f32x4){v[0], v[1], v[2], v[3]};
+    } else {
+      bf16x8 o;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      bf16x8 p;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) p[j] = (__bf16)v[8 * i + j];
-      to[i] = p;
+      for (int j = 0; j < 8; ++j) o[j] = (__bf16)v[j];
+      *reinterpret_cast<bf16x8*>(out + p * E) = o;
     }
   }
 }
@@ -264,36 +265,48 @@ __global__ __launch_bounds__(kFThreads) void k_linear_int4_few(const X* __restri
   const int chunks = (K + 127) / 128, KG = K / G;
   const int c0 = chunks * wave / kFWaves, nc = chunks * (wave + 1) / kFWaves - c0;
   constexpr int GP = 128 / G;  // groups of a chunk
-  auto fetch = [&](int64_t tile, int c) {
-    Chunk f;
-    int64_t n = tile * 16 + col;
+  int64_t ft = blockIdx.x;     // the tile and the chunk that are asked for next
+  int fc = 0;
+  const uint8_t* at_w;
+  const uint16_t* at_s;
+  const uint8_t* at_z;
+  auto aim = [&] {  // this lane's row of the tile
+    int64_t n = ft * 16 + col;
     if (n >= N) n = N - 1;
-    const int k = c * 128 + p * 32;
-    f.w = (u32x4){0, 0, 0, 0};
-    if (k < K) f.w = *reinterpret_cast<const u32x4*>(codes + (n * K + k) / 2);
-    const int64_t g = n * KG + c * GP;
+    at_w = codes + n * (K / 2) + c0 * 64 + p * 16;
+    at_s = scales + n * KG + c0 * GP;
+    at_z = zeros ? zeros + n * KG + c0 * GP : nullptr;
+  };
+  auto fetch = [&](Chunk& f) {
+    const int c = c0 + fc;
+    if (c * 128 + p * 32 < K) f.w = *reinterpret_cast<const u32x4*>(at_w + fc * 64);
+    else f.w = (u32x4){0, 0, 0, 0};
     f.s[0] = f.s[1] = 0;
     f.z = 0x08080808u;
+    const int g = fc * GP;
+    if (GP == 1 || (c + 1) * GP <= KG) {
+      __builtin_memcpy(f.s, at_s + g, 2 * GP);
+      if (zeros) __builtin_memcpy(&f.z, at_z + g, GP);
+    } else {  // the last groups of a row
 #pragma unroll
-    for (int j = 0; j < GP; ++j)
-      if (c * GP + j < KG) {
-        f.s[j / 2] |= (uint32_t)scales[g + j] << (16 * (j & 1));
-        if (zeros) f.z = (f.z & ~(0xFFu << (8 * j))) | (uint32_t)zeros[g + j] << (8 * j);
-      }
-    return f;
-  };
-  int64_t ft = blockIdx.x;
-  int fc = 0;
-  auto advance = [&] {
-    if (++fc == nc) fc = 0, ft += gridDim.x;
+      for (int j = 0; j < GP; ++j)
+        if (c * GP + j < KG) {
+          f.s[j / 2] |= (uint32_t)at_s[g + j] << (16 * (j & 1));
+          if (zeros) f.z = (f.z & ~(0xFFu << (8 * j))) | (uint32_t)at_z[g + j] << (8 * j);
+        }
+    }
+    if (++fc == nc) {
+      fc = 0;
+      ft += gridDim.x;
+      if (ft < tiles) aim();
+    }
   };
   Chunk ring[kDeep];
   if (nc) {
+    aim();
 #pragma unroll
-    for (int d = 0; d < kDeep; ++d) {
-      ring[d] = fetch(ft < tiles ? ft : tiles - 1, c0 + fc);
-      advance();
-    }
+    for (int d = 0; d < kDeep; ++d)
+      if (ft < tiles) fetch(ring[d]);
   }
   wait_loads<0>();
   __syncthreads();
@@ -356,8 +369,7 @@ __global__ __launch_bounds__(kFThreads) void k_linear_int4_few(const X* __restri
     for (int d = 0; d < kDeep; ++d) {
       if (tile < tiles) {
         multiply(ring[d], c0 + c);
-        ring[d] = fetch(ft < tiles ? ft : tiles - 1, c0 + fc);
-        advance();
+        if (ft < tiles) fetch(ring[d]);
         if (++c == nc) {
           finish(tile);
           c = 0;
@@ -776,19 +788,18 @@ extern "C" int bsq_dequantize_int4(const uint8_t* codes, const uint16_t* scales,
   BSQ_REQUIRE(codes && scales && out, BSQ_E_NULL);
   BSQ_REQUIRE(bsqh::aligned16(codes) && bsqh::aligned16(out) && even(scales), BSQ_E_ALIGN);
   hipStream_t s = bsqh::as_stream(stream);
-  constexpr int64_t most = bsqh::max_blocks(kQThreads) * kQThreads / 8 * 8;
-  const int64_t units = N * K / 16;
-  for (int64_t u = 0; u < units; u += most) {
-    const int64_t n = units - u < most ? units - u : most;
-    const dim3 grid((unsigned)((n + kQThreads - 1) / kQThreads));
-    const int64_t g = u / (group / 16);
-    const u32x2* c = reinterpret_cast<const u32x2*>(codes) + u;
+  const int shift = group == 32 ? 5 : group == 64 ? 6 : 7;
+  const int64_t values = N * K, E = out_dtype == BSQ_F32 ? 4 : 8, tile = kDPieces * kQThreads * E;  // of a workgroup
+  const int64_t most = bsqh::max_blocks(kQThreads) * tile;  // whole groups
+  for (int64_t v = 0; v < values; v += most) {
+    const int64_t n = values - v < most ? values - v : most, g = v >> shift;
+    const dim3 grid((unsigned)((n + tile - 1) / tile));
     if (out_dtype == BSQ_F32)
-      hipLaunchKernelGGL((k_dequant_int4<float>), grid, dim3(kQThreads), 0, s, c, scales + g, zeros ? zeros + g : nullptr,
-                         n, (int)(group / 16), static_cast<float*>(out) + u * 16);
+      hipLaunchKernelGGL((k_dequant_int4<float>), grid, dim3(kQThreads), 0, s, codes + v / 2, scales + g,
+                         zeros ? zeros + g : nullptr, n / E, shift, static_cast<float*>(out) + v);
     else
-      hipLaunchKernelGGL((k_dequant_int4<uint16_t>), grid, dim3(kQThreads), 0, s, c, scales + g,
-                         zeros ? zeros + g : nullptr, n, (int)(group / 16), static_cast<uint16_t*>(out) + u * 16);
+      hipLaunchKernelGGL((k_dequant_int4<uint16_t>), grid, dim3(kQThreads), 0, s, codes + v / 2, scales + g,
+                         zeros ? zeros + g : nullptr, n / E, shift, static_cast<uint16_t*>(out) + v);
   }
   return bsqh::launch_status();
 }

@@ -93,6 +93,11 @@ struct Row {
   }
 };
 
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+
 struct Sums {
   float m, s, u;  // maximum, sum e^(x - m), sum (x - m) e^(x - m)
   __device__ __forceinline__ void raise(float to) {  // to >= m
@@ -103,27 +108,34 @@ struct Sums {
       m = to;
     }
   }
-  __device__ __forceinline__ void add(Sums o) {
-    const float to = fmaxf(m, o.m);
-    raise(to);
-    o.raise(to);
-    s += o.s;
-    u += o.u;
-  }
 };
-__device__ __forceinline__ Sums shuffled(const Sums& a, int o) {
-  return {__shfl_xor(a.m, o, 64), __shfl_xor(a.s, o, 64), __shfl_xor(a.u, o, 64)};
+// Lane exchanges within a wave's 16-lane rows, then across them.
+template <typename Op>
+__device__ __forceinline__ float wave_all(float v, Op op) {
+  v = op(v, dpp<0xB1>(v));   // lane ^ 1
+  v = op(v, dpp<0x4E>(v));   // lane ^ 2
+  v = op(v, dpp<0x141>(v));  // 7 - lane of 8: halves of equal quads
+  v = op(v, dpp<0x140>(v));  // 15 - lane of 16
+  v = op(v, __shfl_xor(v, 16, 64));
+  return op(v, __shfl_xor(v, 32, 64));
 }
-// Sums of a workgroup, in every thread.
-__device__ __forceinline__ Sums joined(Sums a, Sums* lds) {
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) a.add(shuffled(a, o));
+// Sums of a workgroup of `waves` waves, in every thread.
+__device__ __forceinline__ Sums joined(Sums a, Sums* lds, int waves) {
+  a.raise(wave_all(a.m, [](float p, float q) { return fmaxf(p, q); }));
+  a.s = wave_all(a.s, [](float p, float q) { return p + q; });
+  a.u = wave_all(a.u, [](float p, float q) { return p + q; });
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = a;
   __syncthreads();
-  a = lds[0];
-#pragma unroll
-  for (int w = 1; w < kWaves; ++w) a.add(lds[w]);
-  return a;
+  float m = -kInf;
+  for (int w = 0; w < waves; ++w) m = fmaxf(m, lds[w].m);
+  Sums t = {m, 0.0f, 0.0f};
+  for (int w = 0; w < waves; ++w) {
+    Sums o = lds[w];
+    o.raise(m);
+    t.s += o.s;
+    t.u += o.u;
+  }
+  return t;
 }
 
 struct Out {
@@ -178,8 +190,10 @@ __global__ __launch_bounds__(kThreads) void k_token_stats(const T* __restrict__ 
       for (int e = 1; e < E; ++e) big = fmaxf(big, v[i][e]);
       most = fmaxf(most, big);
       if constexpr (TOP) {
-#pragma unroll
-        for (int o = 1; o < LB; o *= 2) big = fmaxf(big, __shfl_xor(big, o, 64));
+        big = fmaxf(big, dpp<0xB1>(big));
+        big = fmaxf(big, dpp<0x4E>(big));
+        big = fmaxf(big, dpp<0x141>(big));
+        if constexpr (LB == 16) big = fmaxf(big, dpp<0x140>(big));
         const int p = p0 + i * kThreads + (int)threadIdx.x;
         if (p < last && p % LB == 0) maxima[row * blocks + p / LB] = key_of(big);
       }
@@ -196,150 +210,123 @@ __global__ __launch_bounds__(kThreads) void k_token_stats(const T* __restrict__ 
         a.u = __builtin_fmaf(z, f, a.u);
       }
   }
-  a = joined(a, lds);
+  a = joined(a, lds, kWaves);
   if (threadIdx.x == 0) {
     if (sums) sums[row * parts + part] = a;
     else finish(x, targets, row, V, a, out);
   }
 }
 
-// How many of keys[0, n) are larger than each of the thread's.
-template <int N>
-__device__ __forceinline__ void rank_of(const u64* keys, int n, const u64 (&mine)[N], int (&rank)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) rank[i] = 0;
-#pragma unroll 4
-  for (int j = 0; j < n; ++j) {
-    const u64 k = keys[j];
-#pragma unroll
-    for (int i = 0; i < N; ++i) rank[i] += k > mine[i];
+// The alternatives' kernel: 1024 threads a row, four to a key.
+constexpr int kJThreads = 1024, kJWaves = kJThreads / 64;
+constexpr int kMost = 512;  // keys that are ranked at a time
+constexpr int kLarge = 1 << 20, kSmall = 1 << 18;  // vocabularies
+constexpr int blocks_of(int V) { return V / kBlock + 1; }  // at most: the row may begin within a block
+
+// keys[0, n) are distinct but for zeros, n <= kMost. Each key's rank is the
+// number of larger ones, of which its four threads count a quarter each; `take`
+// gets (index, rank) of those that are not zero and among the `top` first, in
+// each of the four threads.
+template <typename Take>
+__device__ __forceinline__ void ranks(const u64* keys, int n, int top, Take take) {
+  const int t = threadIdx.x;
+  for (int i = t >> 2; i < n; i += kJThreads / 4) {
+    const u64 mine = keys[i];
+    int rank = 0;
+#pragma unroll 8
+    for (int j = t & 3; j < n; j += 4) rank += keys[j] > mine;
+    rank += __builtin_amdgcn_update_dpp(0, rank, 0xB1, 0xF, 0xF, false);
+    rank += __builtin_amdgcn_update_dpp(0, rank, 0x4E, 0xF, 0xF, false);
+    if (mine && rank < top) take(i, rank);
   }
 }
-
-// keys[0, n) (distinct but for zeros, n <= 512): the `top` largest to best[], largest first, 0 where none is left.
+// The `top` largest of keys[0, n) to best[], largest first, 0 where none is left.
 __device__ __forceinline__ void best_of(const u64* keys, int n, int top, u64* best) {
   const int t = threadIdx.x;
-  u64 mine[2];
-  int rank[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) mine[i] = t + i * kThreads < n ? keys[t + i * kThreads] : 0ull;
-  if (t < kMaxTop) best[t] = 0ull;
+  if (t < top) best[t] = 0ull;
   __syncthreads();
-  rank_of<2>(keys, n, mine, rank);
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (mine[i] && rank[i] < top) best[rank[i]] = mine[i];
+  ranks(keys, n, top, [&](int i, int rank) {
+    if ((t & 3) == 0) best[rank] = keys[i];
+  });
+  __syncthreads();
+}
+// Groups of `size` of n items, key(i) distinct but for zeros, at most kMost
+// groups: the items of the best `top` groups to out[0, top * size).
+template <typename Key>
+__device__ __forceinline__ void narrow(Key key, int n, int size, int top, u64* most, u64* out) {
+  const int t = threadIdx.x, groups = (n + size - 1) / size;
+  for (int g = t; g < groups; g += kJThreads) {
+    u64 m = 0;
+    for (int i = g * size; i < (g + 1) * size && i < n; ++i) {
+      const u64 k = key(i);
+      m = k > m ? k : m;
+    }
+    most[g] = m;
+  }
+  for (int i = t; i < top * size; i += kJThreads) out[i] = 0ull;
+  __syncthreads();
+  ranks(most, groups, top, [&](int g, int rank) {
+    for (int i = t & 3; i < size; i += 4)
+      if (g * size + i < n) out[rank * size + i] = key(g * size + i);
+  });
   __syncthreads();
 }
 
-// A workgroup a row: the parts' sums, then the alternatives.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void k_token_join(const T* __restrict__ x, const int64_t* __restrict__ targets,
-                                                        int64_t row0, int V, int parts, const Sums* __restrict__ sums,
-                                                        const uint32_t* __restrict__ maxima, int pitch, int top,
-                                                        Out out) {
-  constexpr int E = Row<T>::E;
-  __shared__ Sums lds[kWaves];
-  __shared__ u64 keys[kMaxTop * 33], best[kMaxTop];
+// A workgroup a row: the parts' sums, then the alternatives. MAXV: the largest
+// vocabulary.
+template <typename T, int MAXV>
+__global__ __launch_bounds__(kJThreads) void k_token_join(const T* __restrict__ x, const int64_t* __restrict__ targets,
+                                                         int64_t row0, int V, int parts, const Sums* __restrict__ sums,
+                                                         const uint32_t* __restrict__ maxima, int pitch, int top,
+                                                         Out out) {
+  constexpr int E = Row<T>::E, PB = kBlock / E;  // elements of a piece, pieces of a block
+  constexpr int kBlocks = blocks_of(MAXV);
+  constexpr int kList = kMaxTop * ((kBlocks + kMost - 1) / kMost);  // blocks of the best groups
+  constexpr int kElements = kMaxTop * kBlock;                      // of the best blocks
+  static_assert((kList + kMost - 1) / kMost * kMaxTop <= kMost && kElements / 8 <= kMost, "two steps at most");
+  __shared__ Sums lds[kJWaves];
+  __shared__ union {
+    uint32_t maxima[kBlocks];
+    u64 element[kElements];
+  } a_;
+  __shared__ u64 list[kList > kMost ? kList : kMost], most[kMost], few[kMost], best[kMaxTop];
   const int t = threadIdx.x;
   const int64_t row = row0 + blockIdx.x;
+  const Row<T> r(x, row, V);
+  const int blocks = (r.pieces() + PB - 1) / PB;
   Sums a = {-kInf, 0.0f, 0.0f};
   if (t < parts) a = sums[row * parts + t];
-  a = joined(a, lds);
+  if (top) {
+    const uint32_t* mx = maxima + row * pitch;
+    for (int b = t; b < blocks; b += kJThreads) a_.maxima[b] = mx[b];
+  }
+  a = joined(a, lds, kJWaves);  // its barrier is the maxima's, too
   if (t == 0) finish(x, targets, row, V, a, out);
   if (top == 0) return;
-  const uint32_t* mx = maxima + row * pitch;
-  const Row<T> r(x, row, V);
-  const int blocks = (r.pieces() + kBlock / E - 1) / (kBlock / E);
-  // groups of `size` blocks; with up to 64 groups kept, `keys` holds their blocks
-  const int groups = blocks > 16 * kThreads ? 2 * kThreads : kThreads, size = (blocks + groups - 1) / groups;
-  for (int g = t; g < groups; g += kThreads) {
-    u64 big = 0;
-    for (int b = g * size; b < (g + 1) * size && b < blocks; ++b) {
-      const u64 k = ranked(mx[b], (uint32_t)b);
-      big = k > big ? k : big;
-    }
-    keys[g] = big;
-  }
-  __syncthreads();
-  best_of(keys, groups, top, best);
-  // the blocks of the best groups; more than 512 are grouped once more
+  const int size = (blocks + kMost - 1) / kMost;
   int n = top * size;
-  for (int i = t; i < n; i += kThreads) {
-    const u64 g = best[i / size];
-    const int b = (int)((uint32_t)~(uint32_t)g) / size * size + i % size;
-    keys[i] = g && b < blocks ? ranked(mx[b], (uint32_t)b) : 0ull;
-  }
-  __syncthreads();
-  if (n > 512) {
-    const int per = (n + kThreads - 1) / kThreads;  // 9 at most: 64 groups of 33 blocks
-    u64 mine[9];
-    u64 most = 0;
-#pragma unroll
-    for (int i = 0; i < 9; ++i) {
-      mine[i] = i < per && t * per + i < n ? keys[t * per + i] : 0ull;
-      most = mine[i] > most ? mine[i] : most;
-    }
-    __syncthreads();
-    keys[t] = most;
-    __syncthreads();
-    const u64 one[1] = {most};
-    int rank[1];
-    rank_of<1>(keys, kThreads, one, rank);
-    __syncthreads();
-    n = top * per;
-    for (int i = t; i < n; i += kThreads) keys[i] = 0ull;
-    __syncthreads();
-    if (most && rank[0] < top) {
-#pragma unroll
-      for (int i = 0; i < 9; ++i)
-        if (i < per) keys[rank[0] * per + i] = mine[i];
-    }
-    __syncthreads();
-  }
-  if (n > 512) {  // up to 64 groups of 9: in two parts, whose best meet
-    u64* half = keys + 1024;
-    best_of(keys, 512, top, half);
-    best_of(keys + 512, n - 512, top, half + kMaxTop);
-    best_of(half, 2 * kMaxTop, top, best);
+  narrow([&](int b) { return ranked(a_.maxima[b], (uint32_t)b); }, blocks, size, top, most, list);
+  if (n <= kMost) {
+    best_of(list, n, top, best);
   } else {
-    best_of(keys, n, top, best);
+    const int again = (n + kMost - 1) / kMost;
+    narrow([&](int i) { return list[i]; }, n, again, top, most, few);
+    best_of(few, top * again, top, best);
   }
-  // eighths of the best blocks, then the elements of the best eighths
-  constexpr int EI = kBlock / 8, PE = EI / E;  // elements and pieces of an eighth
-  n = top * 8;
-  __syncthreads();
-  for (int i = t; i < n; i += kThreads) {
-    const u64 g = best[i / 8];
-    u64 k = 0;
-    if (g) {
-      const int p0 = (int)(uint32_t)~(uint32_t)g * (kBlock / E) + i % 8 * PE;
-      for (int q = 0; q < PE; ++q) {
-        float v[E];
-        r.load(p0 + q, v, -kInf);
+  // the elements of the best blocks, then those of their best eighths
+  for (int i = t; i < top * PB; i += kJThreads) {
+    const u64 g = best[i / PB];
+    const int p = (int)(uint32_t)~(uint32_t)g * PB + i % PB;
+    float v[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const u64 o = ranked(key_of(v[e]), (uint32_t)((p0 + q) * E + e));
-          k = o > k ? o : k;
-        }
-      }
-    }
-    keys[i] = k;
+    for (int e = 0; e < E; ++e) v[e] = -kInf;
+    if (g) r.load(p, v, -kInf);
+#pragma unroll
+    for (int e = 0; e < E; ++e) a_.element[i * E + e] = ranked(key_of(v[e]), (uint32_t)(p * E + e));
   }
   __syncthreads();
-  best_of(keys, n, top, best);
-  for (int i = t; i < n; i += kThreads) {
-    const u64 g = best[i / 8];
-    u64 k = 0;
-    if (g) {
-      const int at = (int)((uint32_t)~(uint32_t)g) / EI * EI + i % 8;
-      if (at >= r.lead && at < r.lead + V) k = ranked(key_of(load1(r.base + at)), (uint32_t)at);
-    }
-    keys[i] = k;
-  }
-  static_assert(EI == 8, "an eighth's elements");
-  __syncthreads();
-  best_of(keys, n, top, best);
+  narrow([&](int i) { return a_.element[i]; }, top * kBlock, 8, top, most, few);
+  best_of(few, top * 8, top, best);
   if (t < top) {
     const bool none = !(a.m > -kInf) && a.s == 0.0f;
     const u64 k = best[t];
@@ -432,7 +419,7 @@ int run_logprobs(const void* logits, const int64_t* targets, int64_t tokens, int
   const Cut c = cut_of(tokens, V, top, sizeof(T));
   Sums* sums = c.sums ? reinterpret_cast<Sums*>(ws) : nullptr;
   uint32_t* maxima = reinterpret_cast<uint32_t*>(ws + c.sums);
-  const int64_t most = bsqh::max_blocks(kThreads) / c.parts;
+  const int64_t most = bsqh::max_blocks(kJThreads) / c.parts;
   for (int64_t r = 0; r < tokens; r += most) {
     const int64_t n = tokens - r < most ? tokens - r : most;
     if (top > 0)
@@ -441,9 +428,12 @@ int run_logprobs(const void* logits, const int64_t* targets, int64_t tokens, int
     else
       hipLaunchKernelGGL((k_token_stats<T, false>), dim3((unsigned)(n * c.parts)), dim3(kThreads), 0, s, x, targets, r,
                          (int)V, c.parts, c.per, sums, maxima, c.blocks, out);
-    if (sums)
-      hipLaunchKernelGGL((k_token_join<T>), dim3((unsigned)n), dim3(kThreads), 0, s, x, targets, r, (int)V, c.parts,
-                         sums, maxima, c.blocks, (int)top, out);
+    if (sums && V <= kSmall)
+      hipLaunchKernelGGL((k_token_join<T, kSmall>), dim3((unsigned)n), dim3(kJThreads), 0, s, x, targets, r, (int)V,
+                         c.parts, sums, maxima, c.blocks, (int)top, out);
+    else if (sums)
+      hipLaunchKernelGGL((k_token_join<T, kLarge>), dim3((unsigned)n), dim3(kJThreads), 0, s, x, targets, r, (int)V,
+                         c.parts, sums, maxima, c.blocks, (int)top, out);
   }
   return bsqh::launch_status();
 }
@@ -463,7 +453,7 @@ int run_backward(const float* dlogprobs, const float* dentropy, const void* logi
 }
 
 bool shape_ok(int64_t tokens, int64_t V) {
-  return tokens >= 0 && tokens < (int64_t)1 << 31 && V >= 1 && V <= (int64_t)1 << 20;
+  return tokens >= 0 && tokens < (int64_t)1 << 31 && V >= 1 && V <= kLarge;
 }
 
 }  // namespace

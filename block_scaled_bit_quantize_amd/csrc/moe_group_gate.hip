@@ -20,8 +20,8 @@
 // logits and biases (equal inputs are a true tie), the row is ambiguous and its
 // wave selects again in float64 with all 64 lanes (in 1 row of about 1000).
 //
-// Layout as in the plain router: 16 lanes share a row up to 256 experts, 64
-// above; a lane holds V neighbouring experts in registers.
+// 8 lanes share a row up to 128 experts, 16 up to 256 and 64 above; a lane holds
+// V neighbouring experts in registers.
 #include <math.h>
 
 #include "bsq_device.h"
@@ -92,32 +92,35 @@ __device__ __forceinline__ double dpp(double v) {
   return __hiloint2double(__builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, 0xF, 0xF, false),
                           __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, 0xF, 0xF, false));
 }
-constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141;  // lane exchanges inside 16 lanes
+// Lane exchanges: ^1, ^2, ^3 within 4 lanes, 7 - lane within 8 (^7), 15 - lane within 16 (^15), rotations within 16.
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kXor3 = 0x1B, kXor7 = 0x141, kXor15 = 0x140;
 constexpr int ror(int n) { return 0x120 + n; }
 
-template <int L>
-__device__ __forceinline__ double row_max64(double v) {
-  v = fmax(v, dpp<ror(8)>(v));
-  v = fmax(v, dpp<ror(4)>(v));
-  v = fmax(v, dpp<ror(2)>(v));
-  v = fmax(v, dpp<ror(1)>(v));
-  if constexpr (L == 64) {
-    v = fmax(v, __shfl_xor(v, 16, 64));
-    v = fmax(v, __shfl_xor(v, 32, 64));
+// All-reduce over the L lanes (8, 16 or 64) that share a row; each step combines
+// the same two results in all lanes that hold them.
+template <int L, typename V, typename Op>
+__device__ __forceinline__ V over_row(V v, Op op) {
+  v = op(v, dpp<kXor1>(v));
+  v = op(v, dpp<kXor2>(v));
+  v = op(v, dpp<kXor7>(v));
+  if constexpr (L > 8) v = op(v, dpp<kXor15>(v));
+  if constexpr (L > 16) {
+    v = op(v, __shfl_xor(v, 16, 64));
+    v = op(v, __shfl_xor(v, 32, 64));
   }
   return v;
 }
 template <int L>
+__device__ __forceinline__ double row_max64(double v) {
+  return over_row<L>(v, [](double a, double b) { return fmax(a, b); });
+}
+template <int L>
 __device__ __forceinline__ float row_maxf(float v) {
-  v = fmaxf(v, dpp<ror(8)>(v));
-  v = fmaxf(v, dpp<ror(4)>(v));
-  v = fmaxf(v, dpp<ror(2)>(v));
-  v = fmaxf(v, dpp<ror(1)>(v));
-  if constexpr (L == 64) {
-    v = fmaxf(v, __shfl_xor(v, 16, 64));
-    v = fmaxf(v, __shfl_xor(v, 32, 64));
-  }
-  return v;
+  return over_row<L>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int L>
+__device__ __forceinline__ float row_addf(float v) {
+  return over_row<L>(v, [](float a, float b) { return a + b; });
 }
 __device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
@@ -264,7 +267,7 @@ __global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ l
       s[i] = x[i] > -kInf ? exp_neg(x[i] - m) : 0.0f;
       total += s[i];
     }
-    total = row_sum<L>(total);
+    total = row_addf<L>(total);
     inv = total > 0.0f ? 1.0f / total : 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) s[i] *= inv;
@@ -286,18 +289,34 @@ __global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ l
       }
       if (c.lanes > 1) merge<kXor1>(g);
       if (c.lanes > 2) merge<kXor2>(g);
-      if (c.lanes > 4) merge<kHalfMirror>(g);
+      if (c.lanes > 4) merge<kXor7>(g);
       float low, high;
       worth(g, c.group_top, c.softmax, low, high);
       int over = 0, near = 0;  // groups that are surely better, that may be
-#define BSQ_TURN(N)                           \
-  if (((N) & (c.lanes - 1)) == 0) {           \
-    over += dpp<ror(N)>(low) > high;          \
-    near += dpp<ror(N)>(high) >= low;         \
-  }
-      BSQ_TURN(1) BSQ_TURN(2) BSQ_TURN(3) BSQ_TURN(4) BSQ_TURN(5) BSQ_TURN(6) BSQ_TURN(7) BSQ_TURN(8)
-      BSQ_TURN(9) BSQ_TURN(10) BSQ_TURN(11) BSQ_TURN(12) BSQ_TURN(13) BSQ_TURN(14) BSQ_TURN(15)
+      auto meet = [&](float other_low, float other_high) {
+        over += other_low > high;
+        near += other_high >= low;
+      };
+      if constexpr (L == 8) {  // lane ^ n for all n, of which other groups' are multiples of c.lanes
+        const float l7 = dpp<kXor7>(low), h7 = dpp<kXor7>(high);
+        if (c.lanes < 2) {
+          meet(dpp<kXor1>(low), dpp<kXor1>(high));
+          meet(dpp<kXor3>(low), dpp<kXor3>(high));
+          meet(dpp<kXor2>(l7), dpp<kXor2>(h7));
+          meet(l7, h7);
+        }
+        if (c.lanes < 4) {
+          meet(dpp<kXor2>(low), dpp<kXor2>(high));
+          meet(dpp<kXor1>(l7), dpp<kXor1>(h7));
+        }
+        meet(dpp<kXor3>(l7), dpp<kXor3>(h7));
+      } else {
+#define BSQ_TURN(N) \
+  if (((N) & (c.lanes - 1)) == 0) meet(dpp<ror(N)>(low), dpp<ror(N)>(high));
+        BSQ_TURN(1) BSQ_TURN(2) BSQ_TURN(3) BSQ_TURN(4) BSQ_TURN(5) BSQ_TURN(6) BSQ_TURN(7) BSQ_TURN(8)
+        BSQ_TURN(9) BSQ_TURN(10) BSQ_TURN(11) BSQ_TURN(12) BSQ_TURN(13) BSQ_TURN(14) BSQ_TURN(15)
 #undef BSQ_TURN
+      }
       const bool keep = near < c.group_k;
       unsure = high > -kInf && !keep && over < c.group_k;
 #pragma unroll
@@ -466,7 +485,7 @@ __global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ l
     else e[q] = in ? exp_neg(fminf(rx[q], 0.0f) - a) / (1.0f + exp_neg(-fabsf(rx[q]))) : 0.0f;
     total += e[q];
   }
-  total = row_sum<L>(total);
+  total = row_addf<L>(total);
   const float f = c.renorm ? (total > 0.0f ? c.scale / total : 0.0f) : c.softmax ? c.scale * inv : c.scale;
 #pragma unroll
   for (int q = 0; q < KR; ++q) {
@@ -508,7 +527,7 @@ __global__ __launch_bounds__(kThreads) void k_group_gate_backward(const float* _
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) mine[sub * V + i] = 0.0f;
-  inner = row_sum<L>(inner);
+  inner = row_addf<L>(inner);
   wave_fence();
   const float mean = c.renorm ? inner / c.scale : 0.0f;
 #pragma unroll
@@ -538,7 +557,7 @@ __global__ __launch_bounds__(kThreads) void k_group_gate_backward(const float* _
       x[i] = x[i] > -kInf ? exp_neg(x[i] - m) : 0.0f;
       total += x[i];
     }
-    total = row_sum<L>(total);
+    total = row_addf<L>(total);
     const float inv = total > 0.0f ? 1.0f / total : 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) d[i] = x[i] * inv * (d[i] - inner);
@@ -552,16 +571,16 @@ void launch_gate(const T* logits, const float* bias, int64_t tokens, Choice c, f
   constexpr int64_t per = kThreads / L, most = bsqh::max_blocks(kThreads) * per;
   // groups that whole lanes hold, a power of two of them: exchanged between lanes, else through LDS
   c.lanes = 0;
-  if (L == 16 && c.E == L * V && c.size % V == 0 && ((c.size / V) & (c.size / V - 1)) == 0) c.lanes = c.size / V;
+  if (L <= 16 && c.E == L * V && c.size % V == 0 && ((c.size / V) & (c.size / V - 1)) == 0) c.lanes = c.size / V;
   for (; tokens > 0; tokens -= most, logits += most * c.E, weights += most * c.k, ids += most * c.k) {
     const int64_t n = tokens < most ? tokens : most;
     const unsigned grid = (unsigned)((n + per - 1) / per);
-    if (c.k < L)
-      hipLaunchKernelGGL((k_group_gate<T, L, V, WHOLE, 1>), dim3(grid), dim3(kThreads), 0, s, logits, bias, n, c,
-                         weights, ids);
-    else
-      hipLaunchKernelGGL((k_group_gate<T, L, V, WHOLE, 64 / L + 1>), dim3(grid), dim3(kThreads), 0, s, logits, bias, n,
-                         c, weights, ids);
+#define BSQ_K(KR) \
+  hipLaunchKernelGGL((k_group_gate<T, L, V, WHOLE, KR>), dim3(grid), dim3(kThreads), 0, s, logits, bias, n, c, weights, ids)
+    if (c.k < L) BSQ_K(1);
+    else if (c.k < 16) BSQ_K((16 + L - 1) / L);
+    else BSQ_K(64 / L + 1);
+#undef BSQ_K
   }
 }
 
@@ -581,6 +600,19 @@ void launch_back(const float* dw, const float* w, const int32_t* ids, const T* l
                          logits, n, c, dlogits);
   }
 }
+
+// L lanes of V experts each. A selection's round costs a search of V keys in a
+// lane, for 64 / L rows at once, and an exchange over L lanes: 8 lanes of 16
+// experts take 24 us where 16 lanes of 8 take 41 (65536 tokens, 128 experts).
+#define BSQ_GROUP_SHAPES(FN, T, ...)                  \
+  if (E == 64) FN<T, 8, 8, true>(__VA_ARGS__);        \
+  else if (E == 128) FN<T, 8, 16, true>(__VA_ARGS__); \
+  else if (E == 256) FN<T, 16, 16, true>(__VA_ARGS__); \
+  else if (E <= 32) FN<T, 8, 4, false>(__VA_ARGS__);  \
+  else if (E < 64) FN<T, 8, 8, false>(__VA_ARGS__);   \
+  else if (E < 128) FN<T, 8, 16, false>(__VA_ARGS__); \
+  else if (E < 256) FN<T, 16, 16, false>(__VA_ARGS__); \
+  else FN<T, 64, 16, false>(__VA_ARGS__)
 
 int check(int dtype, int64_t tokens, int64_t E, int64_t k, int score, int renormalize, float scale) {
   BSQ_REQUIRE(dtype == BSQ_F32 || dtype == BSQ_BF16, BSQ_E_DTYPE);
@@ -613,9 +645,9 @@ extern "C" int bsq_moe_gate_grouped(const void* logits, int dtype, const float* 
   const Choice c = {(int)E, (int)k, group_k == groups ? 1 : (int)groups, (int)(E / groups), (int)group_k, group_top, 0,
                     score == BSQ_SCORE_SOFTMAX, renormalize == 1, scale};
   if (dtype == BSQ_F32) {
-    BSQ_GATE_SHAPES(launch_gate, float, static_cast<const float*>(logits), bias, tokens, c, weights, topk_ids, s);
+    BSQ_GROUP_SHAPES(launch_gate, float, static_cast<const float*>(logits), bias, tokens, c, weights, topk_ids, s);
   } else {
-    BSQ_GATE_SHAPES(launch_gate, uint16_t, static_cast<const uint16_t*>(logits), bias, tokens, c, weights, topk_ids, s);
+    BSQ_GROUP_SHAPES(launch_gate, uint16_t, static_cast<const uint16_t*>(logits), bias, tokens, c, weights, topk_ids, s);
   }
   return bsqh::launch_status();
 }

@@ -44,27 +44,21 @@ def _ws(nbytes, device):
     return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
 
 
-class _Here:
-    def __enter__(self):
-        pass
-
-    def __exit__(self, *exc):
-        pass
-
-
-_HERE = _Here()
-
-
-def _on(first, *others):
-    """A context in which `first`'s device is the current one (and its stream the
-    one that _stream() gives); all tensors must be on it."""
-    index = first.device.index
+def _run(name, first, others, *args):
+    """Calls entry point `name` with args and the current stream of the tensors'
+    device, which is made the current one for it; all tensors must be on it."""
+    index = first.get_device()
     for t in others:
-        if t is not None and t.device.index != index:
+        if t is not None and t.get_device() != index:
             raise BsqError("all tensors must be on one device")
-    if _raw_device is not None and _raw_device() == index:
-        return _HERE
-    return torch.cuda.device(index)
+    fn = getattr(load_library(), name)
+    if _raw_device is not None and _raw_stream is not None and _raw_device() == index:
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _stream())
+    if status:
+        check(status, name)
 
 
 def quantize_nvfp4(x, mode="tensor", outer_in=None, four_over_six=False):
@@ -443,7 +437,6 @@ def moe_gate_grouped(logits, k, bias=None, groups=1, group_k=None, group_top=2, 
     weights: scale * s, with renormalize divided by the selected scores' sum.
     Logits of -inf (and NaN) are masked; a slot that finds no expert left gets
     id -1 and weight 0. moe_gate_grouped_backward is the gradient."""
-    lib = load_library()
     _dev(logits, bias)
     _need(logits.dim() == 2, "moe_gate_grouped: logits must be [tokens, experts]")
     T, E = logits.shape
@@ -457,10 +450,8 @@ def moe_gate_grouped(logits, k, bias=None, groups=1, group_k=None, group_top=2, 
     sc = _score(score, "moe_gate_grouped")
     weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
     ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    with _on(logits, bias):
-        check(lib.bsq_moe_gate_grouped(logits.data_ptr(), dt, _ptr(bias), T, E, k, groups, group_k, group_top, sc,
-                                       1 if renormalize else 0, scale, weights.data_ptr(), ids.data_ptr(), _stream()),
-              "bsq_moe_gate_grouped")
+    _run("bsq_moe_gate_grouped", logits, (bias,), logits.data_ptr(), dt, _ptr(bias), T, E, k, groups, group_k,
+         group_top, sc, 1 if renormalize else 0, scale, weights.data_ptr(), ids.data_ptr())
     return weights, ids
 
 
@@ -469,7 +460,6 @@ def moe_gate_grouped_backward(dweights, weights, topk_ids, logits, score="sigmoi
     fixed: dweights f32 [T, k] with moe_gate_grouped's outputs, input, score,
     renormalize and scale -> dlogits [T, E] of logits' type (every element
     written). The bias only selects and has no gradient."""
-    lib = load_library()
     _dev(dweights, weights, topk_ids, logits)
     _need(logits.dim() == 2 and weights.dim() == 2,
           "moe_gate_grouped_backward: logits [tokens, experts], weights [tokens, k]")
@@ -482,10 +472,9 @@ def moe_gate_grouped_backward(dweights, weights, topk_ids, logits, score="sigmoi
           "moe_gate_grouped_backward: dweights and weights must be float32, topk_ids int32")
     sc = _score(score, "moe_gate_grouped_backward")
     dlogits = torch.empty_like(logits)
-    with _on(logits, dweights, weights, topk_ids):
-        check(lib.bsq_moe_gate_grouped_backward(dweights.data_ptr(), weights.data_ptr(), topk_ids.data_ptr(),
-                                                logits.data_ptr(), dt, T, E, k, sc, 1 if renormalize else 0, scale,
-                                                dlogits.data_ptr(), _stream()), "bsq_moe_gate_grouped_backward")
+    _run("bsq_moe_gate_grouped_backward", logits, (dweights, weights, topk_ids), dweights.data_ptr(),
+         weights.data_ptr(), topk_ids.data_ptr(), logits.data_ptr(), dt, T, E, k, sc, 1 if renormalize else 0, scale,
+         dlogits.data_ptr())
     return dlogits
 
 
@@ -607,7 +596,6 @@ def quantize_int4(w, group=128, symmetric=False):
     a zero point for each group (32, 64 or 128) of neighbours along K:
     (codes u8 [N, K/2], scales bf16 [N, K/group], zeros u8 [N, K/group] or, with
     symmetric, None). They stand for (q - z) * s, z = 8 without zeros."""
-    lib = load_library()
     _dev(w)
     _need(w.dim() == 2, "quantize_int4: w must be [N, K]")
     N, K = w.shape
@@ -617,9 +605,8 @@ def quantize_int4(w, group=128, symmetric=False):
     codes = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
     scales = torch.empty((N, K // group), dtype=torch.bfloat16, device=w.device)
     zeros = None if symmetric else torch.empty((N, K // group), dtype=torch.uint8, device=w.device)
-    with _on(w):
-        check(lib.bsq_quantize_int4(w.data_ptr(), dt, N, K, group, 1 if symmetric else 0, codes.data_ptr(),
-                                    scales.data_ptr(), _ptr(zeros), _stream()), "bsq_quantize_int4")
+    _run("bsq_quantize_int4", w, (), w.data_ptr(), dt, N, K, group, 1 if symmetric else 0, codes.data_ptr(),
+         scales.data_ptr(), _ptr(zeros))
     return codes, scales, zeros
 
 
@@ -638,14 +625,12 @@ def _int4_group(codes, scales, zeros, what):
 
 def dequantize_int4(codes, scales, zeros=None, out_dtype=torch.float32):
     """The values [N, K] that 4-bit groups stand for, (q - z) * s."""
-    lib = load_library()
     _dev(codes, scales, zeros)
     N, K, group = _int4_group(codes, scales, zeros, "dequantize_int4")
     _need(out_dtype in _OUT, "out_dtype must be float32 or bfloat16")
     out = torch.empty((N, K), dtype=out_dtype, device=codes.device)
-    with _on(codes, scales, zeros):
-        check(lib.bsq_dequantize_int4(codes.data_ptr(), scales.data_ptr(), _ptr(zeros), N, K, group, out.data_ptr(),
-                                      _OUT[out_dtype], _stream()), "bsq_dequantize_int4")
+    _run("bsq_dequantize_int4", codes, (scales, zeros), codes.data_ptr(), scales.data_ptr(), _ptr(zeros), N, K, group,
+         out.data_ptr(), _OUT[out_dtype])
     return out
 
 
@@ -665,12 +650,10 @@ def linear_int4(x, codes, scales, zeros=None, bias=None, out_dtype=None):
     _need(bias is None or (bias.dtype == torch.float32 and bias.numel() == N), "linear_int4: bias must be float32 [N]")
     _need(out_dtype in _OUT, "out_dtype must be float32 or bfloat16")
     out = torch.empty((M, N), dtype=out_dtype, device=x.device)
-    with _on(x, codes, scales, zeros, bias):
-        wsb = lib.bsq_linear_int4_workspace(M, N, K, group, dt)
-        ws = _ws(wsb, x.device) if wsb else None
-        check(lib.bsq_linear_int4(x.data_ptr(), dt, codes.data_ptr(), scales.data_ptr(), _ptr(zeros), group, _ptr(bias),
-                                  M, N, K, out.data_ptr(), _OUT[out_dtype], _ptr(ws), wsb, _stream()),
-              "bsq_linear_int4")
+    wsb = lib.bsq_linear_int4_workspace(M, N, K, group, dt)
+    ws = _ws(wsb, x.device) if wsb else None
+    _run("bsq_linear_int4", x, (codes, scales, zeros, bias), x.data_ptr(), dt, codes.data_ptr(), scales.data_ptr(),
+         _ptr(zeros), group, _ptr(bias), M, N, K, out.data_ptr(), _OUT[out_dtype], _ptr(ws), wsb)
     return out
 
 
@@ -693,12 +676,10 @@ def token_logprobs(logits, targets, top=0):
     logprobs, entropy, stats = f32(T), f32(T), f32(T, 2)
     top_lp = f32(T, top) if top else None
     top_ids = torch.empty((T, top), dtype=torch.int32, device=logits.device) if top else None
-    with _on(logits, targets):
-        wsb = lib.bsq_token_logprobs_workspace(T, V, top, dt)
-        ws = _ws(wsb, logits.device) if wsb else None
-        check(lib.bsq_token_logprobs(logits.data_ptr(), dt, targets.data_ptr(), T, V, top, logprobs.data_ptr(),
-                                     entropy.data_ptr(), stats.data_ptr(), _ptr(top_lp), _ptr(top_ids), _ptr(ws), wsb,
-                                     _stream()), "bsq_token_logprobs")
+    wsb = lib.bsq_token_logprobs_workspace(T, V, top, dt)
+    ws = _ws(wsb, logits.device) if wsb else None
+    _run("bsq_token_logprobs", logits, (targets,), logits.data_ptr(), dt, targets.data_ptr(), T, V, top,
+         logprobs.data_ptr(), entropy.data_ptr(), stats.data_ptr(), _ptr(top_lp), _ptr(top_ids), _ptr(ws), wsb)
     return logprobs, entropy, stats, top_lp, top_ids
 
 
@@ -707,7 +688,6 @@ def token_logprobs_backward(dlogprobs, dentropy, logits, targets, stats, entropy
     and dentropy f32 [T] (either may be None) with token_logprobs' inputs and
     outputs -> dlogits [T, V] of logits' type (every element written, 0 at
     masked logits)."""
-    lib = load_library()
     _dev(dlogprobs, dentropy, logits, targets, stats, entropy)
     _need(logits.dim() == 2, "token_logprobs_backward: logits must be [tokens, vocabulary]")
     T, V = logits.shape
@@ -720,10 +700,9 @@ def token_logprobs_backward(dlogprobs, dentropy, logits, targets, stats, entropy
           "token_logprobs_backward: targets must be int64 [tokens]")
     _need(1 <= V <= 1 << 20, "token_logprobs_backward: 1 <= vocabulary <= 2^20")
     dlogits = torch.empty_like(logits)
-    with _on(logits, dlogprobs, dentropy, targets, stats, entropy):
-        check(lib.bsq_token_logprobs_backward(_ptr(dlogprobs), _ptr(dentropy), logits.data_ptr(), dt,
-                                              targets.data_ptr(), stats.data_ptr(), entropy.data_ptr(), T, V,
-                                              dlogits.data_ptr(), _stream()), "bsq_token_logprobs_backward")
+    _run("bsq_token_logprobs_backward", logits, (dlogprobs, dentropy, targets, stats, entropy), _ptr(dlogprobs),
+         _ptr(dentropy), logits.data_ptr(), dt, targets.data_ptr(), stats.data_ptr(), entropy.data_ptr(), T, V,
+         dlogits.data_ptr())
     return dlogits
 
 
