@@ -17,8 +17,11 @@
 // made in float32 with a bound on their error, the selection is made by them,
 // and the groups at the cut and the selected keys next to each other are then
 // looked at. Where two are nearer than their bounds and do not come from equal
-// logits and biases (equal inputs are a true tie), the row is ambiguous and its
-// wave selects again in float64 with all 64 lanes (in 1 row of about 1000).
+// logits and biases (equal inputs are a true tie), the row is ambiguous (1 row in
+// about 500). Where all that may be selected has a place in its lanes, those are
+// put in order by float64 keys; else its wave selects from the start in float64
+// with all 64 lanes (for all ambiguous rows that made 24 us of kernel 37: 65536
+// tokens, 128 experts).
 //
 // 8 lanes share a row up to 128 experts, 16 up to 256 and 64 above; a lane holds
 // V neighbouring experts in registers.
@@ -61,12 +64,13 @@ __device__ __forceinline__ float sigmoid32(float x) {
 }
 
 // Error bound of a float32 key c = s + b: the sigmoid is off by less than
-// 2^-20 s (exponential 2^-22, sum, reciprocal and product 2^-24 to 2^-23 each);
+// 2^-21 s (in 2^-24: the exponential 3, the sum and the product 1 each, the
+// reciprocal 2);
 // a softmax score by less than 2^-16 s (its sum by 2^-19, |l - m| 2^-24 from the
 // difference, up to 64 of it: beyond, s is below 2^-92 and the last term covers it);
 // the sum with the bias by 2^-24 |c|. Exponentials that flush to zero are below 2^-110.
 __device__ __forceinline__ float key_bound(float s, float c, bool softmax) {
-  return s * (softmax ? 0x1p-16f : 0x1p-20f) + fabsf(c) * 0x1p-23f + 0x1p-90f;
+  return s * (softmax ? 0x1p-16f : 0x1p-21f) + fabsf(c) * 0x1p-23f + 0x1p-90f;
 }
 
 // Key above its index in one float64: a larger number is a larger key, or the
@@ -162,8 +166,13 @@ struct WaveLds {
     double worth64[kMaxGroups];
   };
   uint32_t keep[kMaxGroups];
-  int pick[64];
+  int pick[128];
 };
+
+// The key of a logit that is not masked, in float64.
+__device__ __noinline__ double key64(double x, float bias, bool softmax, double m, double total) {
+  return (softmax ? exp(x - m) / total : 1.0 / (1.0 + exp(-x))) + (double)bias;
+}
 
 // One row in float64 by all lanes of a wave: the selected indexes go to lds.pick (-1: none left).
 template <typename T, int L, int V>
@@ -187,9 +196,7 @@ __device__ __noinline__ void select64(const T* __restrict__ row, const float* __
     for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o, 64);
   }
   for (int e = lane; e < c.E; e += 64) {
-    const double x = load1(row + e);
-    const double s = c.softmax ? exp(x - m) / total : 1.0 / (1.0 + exp(-x));
-    const double key = s + (bias ? (double)bias[e] : 0.0);
+    const double x = load1(row + e), key = key64(x, bias ? bias[e] : 0.0f, c.softmax, m, total);
     lds.key64[e] = x > -(double)kInf && key > -(double)kInf ? key : -(double)kInf;
   }
   wave_fence();
@@ -254,7 +261,15 @@ __global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ l
   float x[V], b[V], s[V];
   load_logits<T, V, WHOLE>(row, e0, c.E, ok, x);
 #pragma unroll
-  for (int i = 0; i < V; ++i) b[i] = bias && e0 + i < c.E ? bias[e0 + i] : 0.0f;
+  for (int i = 0; i < V; ++i) b[i] = 0.0f;
+  if (bias) {
+    if constexpr (WHOLE) {
+      __builtin_memcpy(b, bias + e0, sizeof(b));
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) b[i] = e0 + i < c.E ? bias[e0 + i] : 0.0f;
+    }
+  }
   float m = 0.0f, inv = 1.0f;
   if (c.softmax) {
     float top = -kInf, total = 0.0f;
@@ -397,6 +412,8 @@ __global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ l
   // each against the one after it
   const int first = mine * L;  // the row's first lane
   bool tied = false;           // the last selected and the first that is not come from equal inputs
+  bool close = false;          // two that follow each other are nearer than the bounds
+  bool open = false;           // the last selected and the first that is not are
 #pragma unroll
   for (int q = 0; q < KR; ++q) {
     const int from = first + (sub + 1) % L;
@@ -413,7 +430,9 @@ __global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ l
     const int j = q * L + sub;
     if (j < c.k && ri[q] >= 0 && ni >= 0) {
       const bool same = nx == rx[q] && nb == rb[q];
-      unsure |= !same && !(rc[q] - nc > tol[q] + nt);
+      const bool near = !same && !(rc[q] - nc > tol[q] + nt);
+      close |= near;
+      open |= near && j == c.k - 1;
       tied |= same && j == c.k - 1;
     }
   }
@@ -439,6 +458,75 @@ __global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ l
         }
       }
     }
+    unsure |= close;
+  } else if (KR <= 2 && __any(close && ok)) {
+    // Where it is open what is selected, the free places of a row take the keys that follow: all that may be
+    // selected are then there, unless the last of them is still near the last selected one. What is there is put in
+    // order by float64 keys.
+    constexpr int C = L * KR;
+    const bool more = __any(open && ok);
+    for (int j = c.k + 1; more && j < C; ++j) {
+      const double best = next();
+#pragma unroll
+      for (int q = 0; q < KR; ++q)
+        if (j == q * L + sub && !is_gone(best)) ri[q] = index_of(best);
+    }
+    const uint64_t of_row = (L == 64 ? ~0ull : (1ull << (L & 63)) - 1) << first;
+    const bool sort = (__ballot(close) & of_row) != 0, cuts = (__ballot(open) & of_row) != 0;
+    double total = 1.0;
+    if (c.softmax) {
+      total = 0.0;
+#pragma unroll 1
+      for (int e = e0; e < e0 + V && e < c.E; ++e) {
+        const float l = load1(row + e);
+        if (l > -kInf) total += exp((double)l - (double)m);
+      }
+      total = over_row<L>(total, [](double p, double q) { return p + q; });
+    }
+    double kd[KR];
+    float cut = 0.0f, cut_tol = 0.0f, end = -kInf, end_tol = 0.0f;
+#pragma unroll
+    for (int q = 0; q < KR; ++q) {
+      float ls, lc = -kInf, lt = 0.0f;
+      kd[q] = -(double)kInf;
+      if (ri[q] >= 0) {
+        look(ri[q], rx[q], rb[q], ls, lc, lt);
+        kd[q] = key64(rx[q], rb[q], c.softmax, m, total);
+      }
+      const float vc = __shfl(lc, first + (c.k - 1) % L, 64), vt = __shfl(lt, first + (c.k - 1) % L, 64);
+      if (q == (c.k - 1) / L) cut = vc, cut_tol = vt;
+      if (q == KR - 1) end = __shfl(lc, first + L - 1, 64), end_tol = __shfl(lt, first + L - 1, 64);
+    }
+    if (cuts && end > -kInf && !(cut - end > cut_tol + end_tol)) unsure = true;
+    int rank[KR];
+#pragma unroll
+    for (int q = 0; q < KR; ++q) rank[q] = 0;
+#pragma unroll
+    for (int z = 0; z < KR; ++z)
+#pragma unroll 8
+      for (int l = 0; l < L; ++l) {
+        const double od = __shfl(kd[z], first + l, 64);
+        const int oi = __shfl(ri[z], first + l, 64);
+#pragma unroll
+        for (int q = 0; q < KR; ++q) rank[q] += od > kd[q] || (od == kd[q] && oi < ri[q]);
+      }
+#pragma unroll
+    for (int q = 0; q < KR; ++q)
+      if (ri[q] >= 0) lds.pick[mine * C + rank[q]] = ri[q];
+    wave_fence();
+    if (sort) {
+#pragma unroll
+      for (int q = 0; q < KR; ++q) {
+        const int j = q * L + sub;
+        if (j < c.k && ri[q] >= 0) {
+          ri[q] = lds.pick[mine * C + j];
+          rx[q] = load1(row + ri[q]);
+        }
+      }
+    }
+    wave_fence();
+  } else {
+    unsure |= close;
   }
   // rows that float32 cannot settle, one after the other
   uint64_t again = __ballot(unsure && ok);
