@@ -9,6 +9,8 @@
 //   y[m, n] = sum_g s[n, g] sum_(k in g) (q[n, k] - z[n, g]) x[m, k]
 // so that float32 sums are the only roundings before the output's. float32
 // activations go as three bf16 parts whose sum they are (24 bits in 8 + 8 + 8).
+#include <type_traits>
+
 #include "bsq_device.h"
 #include "bsq_internal.h"
 #include "bsq_lds.h"
@@ -23,6 +25,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 
 __device__ __forceinline__ float from_bf16(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
@@ -408,12 +411,13 @@ void launch_few(const X* x, const uint8_t* codes, const uint16_t* scales, const 
 // instructions, with the scales brought in at the end of each group: a tile has
 // one set of accumulators for the group and one for the sum over groups.
 //
-// PL parts of the activations: 1 (bf16) or 3 (float32, split beforehand).
+// PL parts of the activations: 1 (bf16) or 2 (float32, split beforehand).
 constexpr int kUThreads = 256;
+template <typename V>
 __global__ __launch_bounds__(kUThreads) void k_unpack_int4(const u32x2* __restrict__ codes,
                                                           const uint16_t* __restrict__ scales,
                                                           const uint8_t* __restrict__ zeros, int64_t units, int lanes,
-                                                          int KG, int64_t pitch, bf16x8* __restrict__ w,
+                                                          int KG, int64_t pitch, V* __restrict__ w,
                                                           float* __restrict__ turned) {
   const int64_t u = (int64_t)blockIdx.x * kUThreads + threadIdx.x;
   if (u >= units) return;
@@ -422,46 +426,94 @@ __global__ __launch_bounds__(kUThreads) void k_unpack_int4(const u32x2* __restri
   const float z = zeros ? (float)zeros[g] : 8.0f;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    bf16x8 v;
+    V v;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = (__bf16)((float)(c[i] >> (4 * j) & 15u) - z);
+    for (int j = 0; j < 8; ++j) v[j] = (decltype(v[0] + v[0]))((float)(c[i] >> (4 * j) & 15u) - z);
     w[u * 2 + i] = v;
   }
   if (u % lanes == 0) turned[g % KG * pitch + g / KG] = from_bf16(scales[g]);
 }
 
-// float32 activations as three planes of bf16, the smallest parts first.
-__global__ __launch_bounds__(kUThreads) void k_split_f32(const uint8_t* __restrict__ x, int64_t units,
-                                                        bf16x8* __restrict__ planes) {
-  const int64_t u = (int64_t)blockIdx.x * kUThreads + threadIdx.x;
-  if (u >= units) return;
-  Parts<float> a;
-  a.load(x + u * 32);
+// float32 activations as two planes of fp16: a row is scaled by the power of two
+// that brings its largest value to [2^14, 2^15), which is exact, and each value
+// is cut into its nearest fp16 and the nearest of the rest: 22 bits, down to 2^-16
+// of the row's largest; below that to 2^-39 of it. (Three bf16 planes would keep
+// all 24 bits for half as many matrix instructions again; the float32 sums are
+// off by more than the two bits.) A workgroup a row.
+__global__ __launch_bounds__(kUThreads) void k_split_f32(const f32x4* __restrict__ x, int64_t rows, int K,
+                                                        f16x8* __restrict__ planes, float* __restrict__ back) {
+  __shared__ float red[kUThreads / 64];
+  const int64_t row = blockIdx.x;
+  const f32x4* from = x + row * (K / 4);
+  float most = 0.0f;
+  for (int i = threadIdx.x; i < K / 4; i += kUThreads) {
+    const f32x4 v = from[i];
 #pragma unroll
-  for (int part = 0; part < 3; ++part) planes[part * units + u] = a.p[part];
+    for (int j = 0; j < 4; ++j) most = fmaxf(most, fabsf(v[j]));
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor(most, o, 64));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = most;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kUThreads / 64; ++w) most = fmaxf(most, red[w]);
+  // exponent of the largest, biased; a row with an infinity goes as it is (NaN and infinities stay such in fp16)
+  const int e = (int)(__float_as_uint(most) >> 23);
+  const int up = most < __builtin_inff() ? (141 - e < 126 ? 141 - e : 126) : 0;
+  const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+  if (threadIdx.x == 0) back[row] = __uint_as_float((uint32_t)(127 - up) << 23);
+  for (int i = threadIdx.x; i < K / 8; i += kUThreads) {
+    f16x8 hi, lo;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const f32x4 v = from[2 * i + h];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float y = v[j] * f;
+        hi[4 * h + j] = (_Float16)y;
+        lo[4 * h + j] = (_Float16)(y - (float)hi[4 * h + j]);
+      }
+    }
+    planes[row * (K / 8) + i] = lo;
+    planes[(rows + row) * (K / 8) + i] = hi;
+  }
 }
 
 // A step is 64 values of K: rows of 128 bytes, of which the 16-byte piece p of
 // row r lies at p ^ (r / 2 % 8), so that 16 rows at one piece meet 16 different
-// banks. Waves of 32 MI x 32 NI outputs, WM x WN of them.
+// banks. Waves of 32 MI x 32 NI outputs, WM x WN of them; K advances through a
+// ring of ST stages in LDS, filled by loads that go straight there and are
+// counted here. A wave reads the next fragments while it multiplies: the barrier
+// stands before the last instructions along a step, whose fragments are in
+// registers by then. A group's accumulators are scaled and added to the sums
+// right before the next group's first instructions write them anew.
 constexpr int kStep = 64;
+template <int PL>
+__device__ __forceinline__ f32x16 multiply(u32x4 a, u32x4 b, f32x16 c) {
+  if constexpr (PL == 1)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
 template <typename T, int PL, int G, int WM, int WN, int MI, int NI, int ST>
-__global__ __launch_bounds__(64 * WM * WN) void k_gemm_int4(const uint16_t* __restrict__ a, int64_t plane,
-                                                           const uint16_t* __restrict__ w,
-                                                           const float* __restrict__ scales, int64_t pitch,
-                                                           const float* __restrict__ bias, int64_t M, int N, int K,
-                                                           int64_t pitch_out, int splits, int64_t part,
-                                                           T* __restrict__ out) {
+__global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_int4(
+    const uint16_t* __restrict__ a, int64_t plane, const float* __restrict__ back, const uint16_t* __restrict__ w,
+    const float* __restrict__ scales, int64_t pitch, const float* __restrict__ bias, int64_t M, int N, int K,
+    int64_t pitch_out, int splits, int64_t part, T* __restrict__ out) {
   constexpr int WAVES = WM * WN;
   constexpr int TM = 32 * MI * WM, TN = 32 * NI * WN;
   constexpr int GP = G < kStep ? kStep / G : 1;          // groups of a step
   constexpr int GS = G > kStep ? G / kStep : 1;          // steps of a group
+  constexpr int GQ = 4 / GP;                             // instructions along a group within a step
   constexpr int SCALES = GP * TN * 4;                    // bytes of a stage
   constexpr int STAGE = (PL * TM + TN) * 128 + SCALES;
   constexpr int LA = PL * TM / 8 / WAVES, LB = TN / 8 / WAVES, LOADS = LA + LB + 1;
+  constexpr int SLOTS = 4 * NI;                          // rows of matrix instructions in a step
+  constexpr int FRAGS = NI + PL * MI;                    // to read for an instruction along K
   constexpr int PITCH = 32 * NI * (int)sizeof(T) + 16, OUT = 32 * PITCH;  // of a wave, 32 rows at a time
   static_assert(LA * 8 * WAVES == PL * TM && LB * 8 * WAVES == TN && TM % 8 == 0, "whole loads");
   static_assert(SCALES / 256 <= WAVES && WAVES % (SCALES / 256) == 0, "a load of scales a wave");
+  static_assert(ST * STAGE <= 163840, "the LDS of a CU");
   __shared__ __attribute__((aligned(16))) uint8_t lds[ST * STAGE > WAVES * OUT ? ST * STAGE : WAVES * OUT];
   const int t = threadIdx.x, wave = uniform(t >> 6), lane = t & 63;
   // Workgroups go round the 8 XCDs; each XCD takes a contiguous part of the tiles, columns first.
@@ -476,7 +528,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm_int4(const uint16_t* __re
   const int rows_a = M - m0 < TM ? (int)(M - m0) : TM, rows_b = N - n0 < TN ? N - n0 : TN;
   const int units = (K + GS * kStep - 1) / (GS * kStep);  // whole groups and whole steps
   const int steps = (K + kStep - 1) / kStep;
-  int st0 = (int)((int64_t)units * split / splits) * GS, st1 = (int)((int64_t)units * (split + 1) / splits) * GS;
+  const int st0 = (int)((int64_t)units * split / splits) * GS;
+  int st1 = (int)((int64_t)units * (split + 1) / splits) * GS;
   if (st1 > steps) st1 = steps;
   // the planes of a split lie in one buffer, of 64 MiB at most
   const rsrc_words ra = descriptor(a + m0 * K, (uint32_t)(((PL - 1) * plane + (int64_t)rows_a * K) * 2));
@@ -499,72 +552,109 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm_int4(const uint16_t* __re
     }
   }
   const uint32_t base = lds_offset(lds);
-  auto fetch = [&](int step, int stage) {  // past the end: issued all the same (the waits count them)
+  // Loads past the end are issued all the same (the waits count them).
+  auto fetch = [&](int step, int stage, int i) {
     const bool there = step < st1;
     const uint32_t k = there ? (uint32_t)step * 128 : 0u, at = base + stage * STAGE;
+    if (i < LA) {
+      load_to_lds<16>(ra, buffer_at(there, true, va[i < LA ? i : 0], k), at + (wave * LA + i) * 1024);
+    } else if (i < LA + LB) {
+      load_to_lds<16>(rb, buffer_at(there, true, vb[i < LA || i >= LA + LB ? 0 : i - LA], k),
+                      at + PL * TM * 128 + (wave * LB + i - LA) * 1024);
+    } else {  // 64 scales: part c of the step's groups (several waves may fetch the same)
+      const int c = wave % (SCALES / 256);
+      int g = step * kStep / G + c / (TN / 64);
+      if (g >= KG) g = KG - 1;
+      const uint32_t vs = (uint32_t)(((int64_t)g * pitch + c % (TN / 64) * 64 + lane) * 4);
+      load_to_lds<4>(rs, buffer_at(there, true, vs, 0), at + (PL * TM + TN) * 128 + c * 256);
+    }
+  };
+  // slot k of the loads that fill one stage: the last NI rows of a step begin, the others end in the next step
+  auto slot_of = [&](int step, int stage, int k) {
 #pragma unroll
-    for (int i = 0; i < LA; ++i)
-      load_to_lds<16>(ra, buffer_at(there, true, va[i], k), at + (wave * LA + i) * 1024);
-#pragma unroll
-    for (int i = 0; i < LB; ++i)
-      load_to_lds<16>(rb, buffer_at(there, true, vb[i], k), at + PL * TM * 128 + (wave * LB + i) * 1024);
-    // 64 scales: part c of the step's groups (several waves may fetch the same)
-    const int c = wave % (SCALES / 256);
-    int g = step * kStep / G + c / (TN / 64);
-    if (g >= KG) g = KG - 1;
-    const uint32_t vs = (uint32_t)(((int64_t)g * pitch + c % (TN / 64) * 64 + lane) * 4);
-    load_to_lds<4>(rs, buffer_at(there, true, vs, 0), at + (PL * TM + TN) * 128 + c * 256);
+    for (int i = k * LOADS / SLOTS; i < (k + 1) * LOADS / SLOTS; ++i) fetch(step, stage, i);
   };
 #pragma unroll
-  for (int s = 0; s < ST - 1; ++s) fetch(st0 + s, s);
+  for (int s = 0; s < ST; ++s)
+#pragma unroll
+    for (int k = 0; k < (s < ST - 1 ? SLOTS : NI); ++k) slot_of(st0 + s, s, k);
+  wait_loads<(ST - 2) * LOADS + NI * LOADS / SLOTS>();
+  lds_barrier();
   const int wm = wave / WN, wn = wave % WN;
   const int myrow = (lane & 31) * 128, mysw = lane >> 1 & 7;
-  f32x16 sum[MI][NI] = {}, acc[MI][NI];
+  u32x4 fa[2][PL][MI], fb[2][NI];  // fragments of even and odd instructions along K
+  auto read = [&](int stage, int q, int i) {
+    const uint8_t* p = lds + stage * STAGE + myrow + ((2 * q + (lane >> 5)) ^ mysw) * 16;
+    if (i < NI) {
+      fb[q & 1][i < NI ? i : 0] = *reinterpret_cast<const u32x4*>(p + (PL * TM + (wn * NI + i) * 32) * 128);
+    } else {
+      const int j = i - NI < 0 ? 0 : i - NI, pl = j / MI, im = j % MI;
+      fa[q & 1][pl][im] = *reinterpret_cast<const u32x4*>(p + (pl * TM + (wm * MI + im) * 32) * 128);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < FRAGS; ++i) read(0, 0, i);
+  f32x16 sum[MI][NI] = {}, acc[MI][NI] = {};
+  float now[GP][NI], scale[NI] = {};  // of the step's groups, of the group in the accumulators
+  auto scales_of = [&](int stage) {
+    const float* s = reinterpret_cast<const float*>(lds + stage * STAGE + (PL * TM + TN) * 128) + wn * 32 * NI + (lane & 31);
+#pragma unroll
+    for (int g = 0; g < GP; ++g)
+#pragma unroll
+      for (int j = 0; j < NI; ++j) now[g][j] = s[g * TN + j * 32];
+  };
+  auto products = [&](int q, int j, bool first) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      if (first) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sum[i][j][r] = __builtin_fmaf(scale[j], acc[i][j][r], sum[i][j][r]);
+        acc[i][j] = multiply<PL>(fa[q & 1][0][i], fb[q & 1][j], (f32x16){});
+      } else {
+        acc[i][j] = multiply<PL>(fa[q & 1][0][i], fb[q & 1][j], acc[i][j]);
+      }
+#pragma unroll
+      for (int p = 1; p < PL; ++p) acc[i][j] = multiply<PL>(fa[q & 1][p][i], fb[q & 1][j], acc[i][j]);
+    }
+    if (first) scale[j] = now[q / GQ][j];
+  };
+  const bool half = G == 32 && st1 * kStep > K;  // a last step of which there is half
+  const int whole = half ? st1 - 1 : st1;
   int stage = 0;
 #pragma unroll 1
-  for (int step = st0; step < st1; ++step) {
-    wait_loads<(ST - 2) * LOADS>();  // this stage has come
-    lds_barrier();                   // for every wave, and the stage before it is read
-    fetch(step + ST - 1, stage == 0 ? ST - 1 : stage - 1);
-    const uint8_t* at = lds + stage * STAGE;
-    const bool begins = GS == 1 || (step - st0) % GS == 0, ends = GS == 1 || (step - st0) % GS == GS - 1;
+  for (int step0 = st0; step0 < whole; step0 += GS) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {  // 16 values of K
-      if (GP > 1 && step * kStep + q * 16 >= K) break;
-      bf16x8 fb[NI];
-      const int piece = ((2 * q + (lane >> 5)) ^ mysw) * 16 + myrow;
+    for (int u = 0; u < GS; ++u) {  // the steps of a group (K is whole groups)
+      const int step = step0 + u;
+      const int next = stage == ST - 1 ? 0 : stage + 1, last = stage == 0 ? ST - 1 : stage - 1;
+      if (u == 0) scales_of(stage);
 #pragma unroll
-      for (int j = 0; j < NI; ++j)
-        fb[j] = *reinterpret_cast<const bf16x8*>(at + (PL * TM + (wn * NI + j) * 32) * 128 + piece);
-      const bool first = q * 16 % G == 0 && (GS == 1 || q == 0);
-#pragma unroll
-      for (int p = 0; p < PL; ++p)
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-          const bf16x8 fa = *reinterpret_cast<const bf16x8*>(at + (p * TM + (wm * MI + i) * 32) * 128 + piece);
-#pragma unroll
-          for (int j = 0; j < NI; ++j) {
-            if (first && p == 0 && begins)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa, fb[j], (f32x16){}, 0, 0, 0);
-            else
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa, fb[j], acc[i][j], 0, 0, 0);
-          }
+      for (int q = 0; q < 4; ++q) {
+        if (q == 3) {
+          wait_loads<(ST - 2) * LOADS>();  // the next stage has come
+          lds_barrier();                   // for every wave, and this one is read
         }
-      if ((q * 16 + 16) % G == 0 || q == 3) {
-        if (ends) {
-          const float* s = reinterpret_cast<const float*>(at + (PL * TM + TN) * 128) + q * 16 / G * TN + wn * 32 * NI + (lane & 31);
 #pragma unroll
-          for (int j = 0; j < NI; ++j) {
-            const float f = s[j * 32];
+        for (int j = 0; j < NI; ++j) {
+          if (q == 3) slot_of(step + ST, stage, j);
+          else slot_of(step + ST - 1, last, (q + 1) * NI + j);
 #pragma unroll
-            for (int i = 0; i < MI; ++i)
-#pragma unroll
-              for (int r = 0; r < 16; ++r) sum[i][j][r] = __builtin_fmaf(f, acc[i][j][r], sum[i][j][r]);
-          }
+          for (int z = j * FRAGS / NI; z < (j + 1) * FRAGS / NI; ++z) read(q == 3 ? next : stage, (q + 1) % 4, z);
+          products(q, j, q % GQ == 0 && u == 0);
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
+      stage = next;
     }
-    stage = stage == ST - 1 ? 0 : stage + 1;
+  }
+  if (half) {
+    scales_of(stage);
+#pragma unroll
+    for (int i = 0; i < FRAGS; ++i) read(stage, 1, i);
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int j = 0; j < NI; ++j) products(q, j, q == 0);
   }
   wait_loads<0>();
   lds_barrier();
@@ -576,18 +666,25 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm_int4(const uint16_t* __re
   const int nw = n0 + wn * 32 * NI;
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
+    const int64_t mw = m0 + (wm * MI + i) * 32;
+    f32x4 rows[4];  // what undoes the scaling of the rows
+    if constexpr (PL > 1) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) rows[r] = *reinterpret_cast<const f32x4*>(back + mw + 8 * r + 4 * (lane >> 5));
+    }
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
       const int n = nw + j * 32 + (lane & 31);
       const float add = bias && n < N ? bias[n] : 0.0f;
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        store1(reinterpret_cast<T*>(mylds + (8 * (r / 4) + 4 * (lane >> 5) + r % 4) * PITCH) + j * 32 + (lane & 31),
-               sum[i][j][r] + add);
+      for (int r = 0; r < 16; ++r) {
+        float y = __builtin_fmaf(scale[j], acc[i][j][r], sum[i][j][r]);
+        if constexpr (PL > 1) y *= rows[r / 4][r % 4];
+        store1(reinterpret_cast<T*>(mylds + (8 * (r / 4) + 4 * (lane >> 5) + r % 4) * PITCH) + j * 32 + (lane & 31), y + add);
+      }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the wave reads what its own lanes wrote
     constexpr int EP = 16 / (int)sizeof(T), OP = 32 * NI / EP;  // elements of a piece, pieces of a row
-    const int64_t mw = m0 + (wm * MI + i) * 32;
 #pragma unroll
     for (int o = lane; o < 32 * OP; o += 64) {
       const int row = o / OP, pc = o % OP, n = nw + pc * EP;
@@ -626,7 +723,7 @@ struct Plan {
   int64_t rows;     // few: rows of x a launch; many: rows of x split at a time
   int64_t slice;    // rows of weights unpacked at a time (of 128)
   int tile, splits; // tile: rows and columns of a workgroup's outputs, 0 64 x 64, 1 128 x 128, 2 256 x 128
-  size_t w, s, x, parts;  // bytes of the workspace
+  size_t w, s, x, back, parts;  // bytes of the workspace
 };
 
 constexpr int64_t kUnpacked = (int64_t)64 << 20;  // bytes of unpacked weights and of split activations at a time
@@ -645,9 +742,12 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int64_t group, int dtype) {
   if (whole < p.slice) p.slice = whole;
   // fewer than 2^24 workgroups of 256 work-items
   p.rows = ((int64_t)1 << 22) / (p.slice / 128) * 128;
-  if (dtype == BSQ_F32 && kUnpacked / (6 * K) / 256 * 256 < p.rows) p.rows = kUnpacked / (6 * K) / 256 * 256;
+  if (dtype == BSQ_F32 && kUnpacked / (4 * K) / 256 * 256 < p.rows) p.rows = kUnpacked / (4 * K) / 256 * 256;
   if (M < p.rows) p.rows = M;
-  if (dtype == BSQ_F32) p.x = (size_t)(p.rows * K * 6);
+  if (dtype == BSQ_F32) {
+    p.x = (size_t)(p.rows * K * 4);
+    p.back = (size_t)((p.rows + 767) / 768 * 768 * 4);  // whole tiles of 64, 128 and 192 rows
+  }
   p.w = (size_t)(p.slice * K * 2);
   p.s = (size_t)(p.slice * (K / group) * 4);
   const int64_t cus = bsqh::device_cus();
@@ -661,65 +761,73 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int64_t group, int dtype) {
     if (sp > 8) sp = 8;
     p.splits = sp < 1 ? 1 : (int)sp;
   } else {
-    p.tile = dtype == BSQ_F32 || big < cus ? 1 : 2;
+    p.tile = dtype == BSQ_F32 ? (small > cus && ((p.rows + 191) / 192) * (p.slice / 128) <= cus ? 2 : 1) : big < cus ? 1 : 2;
   }
   if (p.splits > 1) p.parts = (size_t)(p.splits * p.rows * p.slice * 4);
   return p;
 }
 
 template <typename T, int PL, int G>
-void launch_tiles(const Plan& p, const uint16_t* a, int64_t plane, const uint16_t* w, const float* sc,
+void launch_tiles(const Plan& p, const uint16_t* a, int64_t plane, const float* back, const uint16_t* w, const float* sc,
                   const float* bias, int64_t M, int64_t N, int64_t K, int64_t pitch_out, int64_t part, T* out,
                   hipStream_t s) {
 #define BSQ_TILE(WM, WN, MI, NI, ST)                                                                                   \
   hipLaunchKernelGGL((k_gemm_int4<T, PL, G, WM, WN, MI, NI, ST>),                                                     \
                      dim3((unsigned)(((M + 32 * MI * WM - 1) / (32 * MI * WM)) * ((N + 32 * NI * WN - 1) / (32 * NI * WN)) * \
                                      p.splits)),                                                                      \
-                     dim3(64 * WM * WN), 0, s, a, plane, w, sc, p.slice, bias, M, (int)N, (int)K, pitch_out, p.splits, \
-                     part, out)
-  if (p.tile == 0) BSQ_TILE(2, 2, 1, 1, 3);
-  else if (p.tile == 1) BSQ_TILE(2, 2, 2, 2, 2);
-  else if constexpr (PL == 1) BSQ_TILE(4, 2, 2, 2, 3);
+                     dim3(64 * WM * WN), 0, s, a, plane, back, w, sc, p.slice, bias, M, (int)N, (int)K, pitch_out,    \
+                     p.splits, part, out)
+  if constexpr (PL == 1) {
+    if (p.tile == 0) BSQ_TILE(2, 2, 1, 1, 3);
+    else if (p.tile == 1) BSQ_TILE(2, 2, 2, 2, 2);
+    else BSQ_TILE(4, 2, 2, 2, 3);
+  } else {
+    if (p.tile == 0) BSQ_TILE(2, 2, 1, 1, 3);
+    else if (p.tile == 1) BSQ_TILE(2, 2, 2, 2, 3);
+    else BSQ_TILE(2, 2, 3, 2, 2);
+  }
 #undef BSQ_TILE
 }
 
 template <typename X, typename T, int G>
 int run_linear(const X* x, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, const float* bias,
                int64_t M, int64_t N, int64_t K, T* out, uint8_t* ws, hipStream_t s) {
-  constexpr int PL = sizeof(X) == 4 ? 3 : 1;
-  const Plan p = plan_of(M, N, K, G, PL == 3 ? BSQ_F32 : BSQ_BF16);
+  constexpr int PL = sizeof(X) == 4 ? 2 : 1;
+  const Plan p = plan_of(M, N, K, G, PL == 2 ? BSQ_F32 : BSQ_BF16);
   if (p.few) {
     for (int64_t m = 0; m < M; m += p.rows)
       launch_few<X, T, G>(x + m * K, codes, scales, zeros, bias, M - m < p.rows ? M - m : p.rows, N, K, out + m * N, s);
     return bsqh::launch_status();
   }
-  uint16_t* w = reinterpret_cast<uint16_t*>(ws);
+  typedef typename std::conditional<PL == 2, f16x8, bf16x8>::type V;
+  V* w = reinterpret_cast<V*>(ws);
   float* turned = reinterpret_cast<float*>(ws + p.w);
   uint16_t* planes = reinterpret_cast<uint16_t*>(ws + p.w + p.s);
-  float* parts = reinterpret_cast<float*>(ws + p.w + p.s + p.x);
+  float* back = reinterpret_cast<float*>(ws + p.w + p.s + p.x);
+  float* parts = reinterpret_cast<float*>(ws + p.w + p.s + p.x + p.back);
   const int64_t KG = K / G;
   for (int64_t n0 = 0; n0 < N; n0 += p.slice) {
     const int64_t n = N - n0 < p.slice ? N - n0 : p.slice, units = n * K / 16;
-    hipLaunchKernelGGL(k_unpack_int4, dim3((unsigned)((units + kUThreads - 1) / kUThreads)), dim3(kUThreads), 0, s,
+    hipLaunchKernelGGL((k_unpack_int4<V>), dim3((unsigned)((units + kUThreads - 1) / kUThreads)), dim3(kUThreads), 0, s,
                        reinterpret_cast<const u32x2*>(codes + n0 * K / 2), scales + n0 * KG,
-                       zeros ? zeros + n0 * KG : nullptr, units, G / 16, (int)KG, p.slice, reinterpret_cast<bf16x8*>(w),
-                       turned);
+                       zeros ? zeros + n0 * KG : nullptr, units, G / 16, (int)KG, p.slice, w, turned);
     for (int64_t m0 = 0; m0 < M; m0 += p.rows) {
       const int64_t m = M - m0 < p.rows ? M - m0 : p.rows;
       const uint16_t* a = reinterpret_cast<const uint16_t*>(x + m0 * K);
-      if constexpr (PL == 3) {
-        const int64_t xu = m * K / 8;
-        hipLaunchKernelGGL(k_split_f32, dim3((unsigned)((xu + kUThreads - 1) / kUThreads)), dim3(kUThreads), 0, s,
-                           reinterpret_cast<const uint8_t*>(x + m0 * K), xu, reinterpret_cast<bf16x8*>(planes));
+      if constexpr (PL == 2) {
+        if (n0 == 0 || M > p.rows)
+          hipLaunchKernelGGL(k_split_f32, dim3((unsigned)m), dim3(kUThreads), 0, s,
+                             reinterpret_cast<const f32x4*>(x + m0 * K), m, (int)K, reinterpret_cast<f16x8*>(planes), back);
         a = planes;
       }
+      const uint16_t* wb = reinterpret_cast<const uint16_t*>(w);
       const float* add = bias ? bias + n0 : nullptr;
       T* to = out + m0 * N + n0;
       if (p.splits == 1) {
-        launch_tiles<T, PL, G>(p, a, m * K, w, turned, add, m, n, K, N, 0, to, s);
+        launch_tiles<T, PL, G>(p, a, m * K, back, wb, turned, add, m, n, K, N, 0, to, s);
       } else {
         const int64_t part = m * n;
-        launch_tiles<float, PL, G>(p, a, m * K, w, turned, nullptr, m, n, K, n, part, parts, s);
+        launch_tiles<float, PL, G>(p, a, m * K, back, wb, turned, nullptr, m, n, K, n, part, parts, s);
         hipLaunchKernelGGL((k_join_int4<T>), dim3((unsigned)((part + kUThreads - 1) / kUThreads)), dim3(kUThreads), 0, s,
                            parts, p.splits, part, m, (int)n, add, N, to);
       }
@@ -807,7 +915,7 @@ extern "C" int bsq_dequantize_int4(const uint8_t* codes, const uint16_t* scales,
 extern "C" size_t bsq_linear_int4_workspace(int64_t M, int64_t N, int64_t K, int64_t group, int dtype) {
   if (M <= 0 || N <= 0 || M >= (int64_t)1 << 31 || !weights_ok(N, K, group)) return 0;
   const Plan p = plan_of(M, N, K, group, dtype);
-  return p.w + p.s + p.x + p.parts;
+  return p.w + p.s + p.x + p.back + p.parts;
 }
 
 extern "C" int bsq_linear_int4(const void* x, int dtype, const uint8_t* codes, const uint16_t* scales,
