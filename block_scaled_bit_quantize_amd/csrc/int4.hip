@@ -9,8 +9,6 @@
 //   y[m, n] = sum_g s[n, g] sum_(k in g) (q[n, k] - z[n, g]) x[m, k]
 // so that float32 sums are the only roundings before the output's. float32
 // activations go as three bf16 parts whose sum they are (24 bits in 8 + 8 + 8).
-#include <type_traits>
-
 #include "bsq_device.h"
 #include "bsq_internal.h"
 #include "bsq_lds.h"
@@ -142,79 +140,106 @@ __global__ __launch_bounds__(kQThreads) void k_dequant_int4(const uint8_t* __res
 }
 
 // ---------------------------------------------------------------- operands
-// Eight codes (the lowest nibble first) as bf16 integers. A byte below 16 is,
-// read as E4M3, itself times 2^-9: its subnormals and its first binade have the
-// same step.
-__device__ __forceinline__ bf16x8 codes_bf16(uint32_t w) {
-  const uint32_t even = w & 0x0F0F0F0Fu, odd = w >> 4 & 0x0F0F0F0Fu;
-  const uint32_t a = __builtin_amdgcn_perm(odd, even, 0x05010400u), b = __builtin_amdgcn_perm(odd, even, 0x07030602u);
-  union {
-    bf16x2 p[4];
-    bf16x8 v;
-  } r;
-  r.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 512.0f, false);
-  r.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 512.0f, true);
-  r.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.0f, false);
-  r.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.0f, true);
-  return r.v;
-}
-
-// Eight activations as bf16 parts, the smallest part first.
+// The activations' type in the matrix instructions: bf16 as they come, float32 as
+// two fp16 parts of a scaled row.
 template <typename X>
-struct Parts;
+struct Mfma;
 template <>
-struct Parts<uint16_t> {
-  static constexpr int n = 1;
-  bf16x8 p[1];
-  __device__ __forceinline__ void load(const uint8_t* at) { p[0] = *reinterpret_cast<const bf16x8*>(at); }
+struct Mfma<uint16_t> {
+  typedef bf16x8 V;
+  static constexpr int parts = 1;
+  static constexpr uint32_t ones = 0x3F803F80u;
+  static __device__ __forceinline__ f32x4 mul16(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x16 mul32(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b), c, 0, 0, 0);
+  }
+  template <bool HIGH>
+  static __device__ __forceinline__ uint32_t pair(uint32_t bytes) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(bytes, 512.0f, HIGH));
+  }
 };
 template <>
-struct Parts<float> {
-  static constexpr int n = 3;
-  bf16x8 p[3];
-  __device__ __forceinline__ void load(const uint8_t* at) {
-    const f32x4 a = reinterpret_cast<const f32x4*>(at)[0], b = reinterpret_cast<const f32x4*>(at)[1];
-    uint32_t w[3][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float v[2];
-      v[0] = i < 2 ? a[2 * (i & 1)] : b[2 * (i & 1)];
-      v[1] = i < 2 ? a[2 * (i & 1) + 1] : b[2 * (i & 1) + 1];
-#pragma unroll
-      for (int part = 2; part >= 0; --part) {  // cut off the upper 16 bits: the rest is exact
-        const uint32_t u0 = __float_as_uint(v[0]), u1 = __float_as_uint(v[1]);
-        w[part][i] = __builtin_amdgcn_perm(u1, u0, 0x07060302u);
-        v[0] -= __uint_as_float(u0 & 0xFFFF0000u);
-        v[1] -= __uint_as_float(u1 & 0xFFFF0000u);
-      }
-    }
-#pragma unroll
-    for (int part = 0; part < 3; ++part) p[part] = __builtin_bit_cast(bf16x8, (u32x4){w[part][0], w[part][1], w[part][2], w[part][3]});
+struct Mfma<float> {
+  typedef f16x8 V;
+  static constexpr int parts = 2;
+  static constexpr uint32_t ones = 0x3C003C00u;
+  static __device__ __forceinline__ f32x4 mul16(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x16 mul32(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b), c, 0, 0, 0);
+  }
+  template <bool HIGH>
+  static __device__ __forceinline__ uint32_t pair(uint32_t bytes) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(bytes, 512.0f, HIGH));
   }
 };
 
+// Eight codes (the lowest nibble first) as integers of that type. A byte below
+// 16 is, read as E4M3, itself times 2^-9: its subnormals and its first binade
+// have the same step.
+template <typename X>
+__device__ __forceinline__ u32x4 codes_of(uint32_t w) {
+  const uint32_t even = w & 0x0F0F0F0Fu, odd = w >> 4 & 0x0F0F0F0Fu;
+  const uint32_t a = __builtin_amdgcn_perm(odd, even, 0x05010400u), b = __builtin_amdgcn_perm(odd, even, 0x07030602u);
+  return (u32x4){Mfma<X>::template pair<false>(a), Mfma<X>::template pair<true>(a), Mfma<X>::template pair<false>(b),
+                 Mfma<X>::template pair<true>(b)};
+}
+
+// float32 activations as two fp16 parts: a row (or what a workgroup has of it) is
+// scaled by the power of two that brings its largest value to [2^14, 2^15), which
+// is exact, and each value is cut into its nearest fp16 and the nearest of the
+// rest: 22 bits, down to 2^-16 of the largest; below that to 2^-39 of it. (Three
+// bf16 parts would keep all 24 bits for half as many matrix instructions again;
+// the float32 sums are off by more than the two bits.) Biased exponent of the
+// factor for rows whose largest magnitude has these bits; rows with a NaN or an
+// infinity go as they are.
+__device__ __forceinline__ uint32_t row_factor(uint32_t most) {
+  if (most >= 0x7F800000u) return 127;
+  const int up = 141 - (int)(most >> 23);
+  return (uint32_t)(127 + (up < 126 ? up : 126));
+}
+__device__ __forceinline__ float of_exponent(uint32_t e) { return __uint_as_float(e << 23); }
+__device__ __forceinline__ void split8(f32x4 a, f32x4 b, float f, u32x4& hi, u32x4& lo) {
+  f16x8 h, l;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float y = (j < 4 ? a[j & 3] : b[j & 3]) * f;
+    h[j] = (_Float16)y;
+    l[j] = (_Float16)(y - (float)h[j]);
+  }
+  hi = __builtin_bit_cast(u32x4, h);
+  lo = __builtin_bit_cast(u32x4, l);
+}
+
 // ---------------------------------------------------------------- few rows
-// Up to 16 rows of activations, which stay in LDS: bound by reading the weights
-// once. A workgroup of eight waves takes tiles of 16 weight rows one after the
-// other; its waves share K, in chunks of 128, of which each keeps kDeep on their
-// way in registers, across tiles. The partial sums meet in LDS.
+// Up to 64 rows of activations, which stay in LDS: bound by reading the weights
+// once. Weights go from memory to registers: a wave keeps kDeep chunks of 16 rows
+// by 128 codes on their way, across tiles of 16 rows.
+//   SHARE: up to 16 rows of x, whole in LDS. The eight waves of a workgroup share
+//   K, and their partial sums meet in LDS; a workgroup takes tile after tile.
+//   else: more rows, or longer ones. A workgroup has a slab of K of them in LDS,
+//   and each wave tiles of its own; the slabs' sums meet in a second launch.
 //
 // Lane l holds row l % 16's codes [32 p, 32 p + 32) of a chunk, p = l / 16, as
 // one 16-byte load. Matrix instruction i multiplies one word of each lane: 32
 // codes of the chunk. Groups of 128 take them as they lie; for shorter groups
 // lanes exchange words first, so that the 32 codes are of one group.
 //
-// Zero points: sum (q - z) x = sum q x - z sum x, the second sum by the same
-// instruction with ones.
+// Zero points: sum (q - z) x = sum q x - z sum x; the second sums are made once
+// for all tiles, by the same instruction with ones.
 constexpr int kFWaves = 8, kFThreads = 64 * kFWaves;
-constexpr int kFewRows = 16;
 constexpr int kDeep = 4;
-constexpr int kFewLds = 163840, kFewRed = 2 * kFWaves * 1024;
+constexpr int kFewLds = 163840 - 512, kFewRed = 2 * kFWaves * 1024;  // a CU's LDS but for the rows' largest values
+constexpr int kFewHalf = 81920 - 512;
+constexpr int kSlabLds = 131072;  // of x, but for the rows' 16 bytes more
 
-template <typename X>
-__host__ __device__ constexpr int64_t few_pitch(int64_t K) {  // a row of x: whole loads, and 16 bytes against bank conflicts
-  return (K * (int64_t)sizeof(X) + 1023) / 1024 * 1024 + 16;
-}
+// A row of k values of x in LDS: whole loads, and 16 bytes against bank conflicts.
+__host__ __device__ constexpr int64_t few_pitch(int64_t k, int64_t size) { return (k * size + 1023) / 1024 * 1024 + 16; }
+// Sums of x by groups, [group][row].
+__host__ __device__ constexpr int64_t few_table(int64_t k, int64_t group, int mt) { return (k + 127) / 128 * (128 / group) * mt * 64; }
 
 template <int G>
 __device__ __forceinline__ void regroup(u32x4& w) {
@@ -243,32 +268,43 @@ struct Chunk {
   uint32_t s[2], z;  // scales and zero points of its groups, the first lowest
 };
 
-// BYTES of LDS: half of a CU's where that does, for two workgroups a CU.
-template <typename X, typename T, int G, int BYTES>
+// BYTES of LDS: half of a CU's where that does, for two workgroups a CU. slab:
+// values of K of a workgroup. Outputs, or (parts given) a slab's sums, [slab][M][N].
+template <typename X, typename T, int G, int MT, bool SHARE, int BYTES>
 __global__ __launch_bounds__(kFThreads) void k_linear_int4_few(const X* __restrict__ x, const uint8_t* __restrict__ codes,
                                                               const uint16_t* __restrict__ scales,
                                                               const uint8_t* __restrict__ zeros,
                                                               const float* __restrict__ bias, int M, int64_t N, int K,
+                                                              int slab, float* __restrict__ parts, int64_t pitch_out,
                                                               T* __restrict__ out) {
+  constexpr int P = Mfma<X>::parts, GP = 128 / G;  // groups of a chunk
   __shared__ __attribute__((aligned(16))) uint8_t lds[BYTES];
-  f32x4* red = reinterpret_cast<f32x4*>(lds);  // [2][waves][64]
-  uint8_t* xs = lds + kFewRed;
+  __shared__ uint32_t rmax[P > 1 ? 16 * MT : 1];
+  f32x4* red = reinterpret_cast<f32x4*>(lds);  // SHARE: [2][waves][64]
   const int t = threadIdx.x, wave = uniform(t >> 6), lane = t & 63, col = lane & 15, p = lane >> 4;
-  const int pitch = (int)few_pitch<X>(K), row_loads = pitch / 1024;
+  const int k0 = SHARE ? 0 : (int)blockIdx.y * slab, k_end = K - k0 < slab ? K : k0 + slab;  // this workgroup's K
+  const int chunks = (k_end - k0 + 127) / 128, pitch = (int)few_pitch(slab, sizeof(X));
+  f32x4* table = reinterpret_cast<f32x4*>(lds + (SHARE ? kFewRed : 0));
+  uint8_t* xs = lds + (SHARE ? kFewRed : 0) + few_table(slab, G, MT);
   {
     const rsrc_words d = descriptor(x, (uint32_t)M * K * (uint32_t)sizeof(X));
-    const uint32_t base = lds_offset(xs), row_bytes = (uint32_t)K * sizeof(X);
+    const uint32_t base = lds_offset(xs), from = (uint32_t)k0 * sizeof(X), to = (uint32_t)k_end * sizeof(X);
+    const int row_loads = pitch / 1024;
     for (int i = wave; i < M * row_loads; i += kFWaves) {
       const int r = i / row_loads, c = i - r * row_loads;
-      const uint32_t at = c * 1024 + lane * 16;
-      load_to_lds<16>(d, buffer_at(true, at < row_bytes, (uint32_t)r * row_bytes + at, 0), base + r * pitch + c * 1024);
+      const uint32_t at = from + c * 1024 + lane * 16;
+      load_to_lds<16>(d, buffer_at(true, at < to, (uint32_t)r * K * (uint32_t)sizeof(X) + at, 0), base + r * pitch + c * 1024);
     }
   }
-  const int64_t tiles = (N + 15) / 16;
-  const int chunks = (K + 127) / 128, KG = K / G;
-  const int c0 = chunks * wave / kFWaves, nc = chunks * (wave + 1) / kFWaves - c0;
-  constexpr int GP = 128 / G;  // groups of a chunk
-  int64_t ft = blockIdx.x;     // the tile and the chunk that are asked for next
+  if constexpr (P > 1) {
+    if (t < 16 * MT) rmax[t] = 0u;
+  }
+  const int64_t tiles = (N + 15) / 16, stride = SHARE ? gridDim.x : (int64_t)gridDim.x * kFWaves;
+  const int64_t tile0 = SHARE ? blockIdx.x : (int64_t)blockIdx.x * kFWaves + wave;
+  const int KG = K / G;
+  const int c0 = SHARE ? chunks * wave / kFWaves : 0;  // this wave's chunks
+  const int nc = SHARE ? chunks * (wave + 1) / kFWaves - c0 : chunks;
+  int64_t ft = tile0;  // the tile and the chunk that are asked for next
   int fc = 0;
   const uint8_t* at_w;
   const uint16_t* at_s;
@@ -276,36 +312,36 @@ __global__ __launch_bounds__(kFThreads) void k_linear_int4_few(const X* __restri
   auto aim = [&] {  // this lane's row of the tile
     int64_t n = ft * 16 + col;
     if (n >= N) n = N - 1;
-    at_w = codes + n * (K / 2) + c0 * 64 + p * 16;
-    at_s = scales + n * KG + c0 * GP;
-    at_z = zeros ? zeros + n * KG + c0 * GP : nullptr;
+    at_w = codes + n * (K / 2) + k0 / 2 + c0 * 64 + p * 16;
+    at_s = scales + n * KG + k0 / G + c0 * GP;
+    at_z = zeros ? zeros + n * KG + k0 / G + c0 * GP : nullptr;
   };
   auto fetch = [&](Chunk& f) {
-    const int c = c0 + fc;
-    if (c * 128 + p * 32 < K) f.w = *reinterpret_cast<const u32x4*>(at_w + fc * 64);
+    const int k = k0 + (c0 + fc) * 128;
+    if (k + p * 32 < K) f.w = *reinterpret_cast<const u32x4*>(at_w + fc * 64);
     else f.w = (u32x4){0, 0, 0, 0};
     f.s[0] = f.s[1] = 0;
     f.z = 0x08080808u;
     const int g = fc * GP;
-    if (GP == 1 || (c + 1) * GP <= KG) {
+    if (GP == 1 || k + 128 <= K) {
       __builtin_memcpy(f.s, at_s + g, 2 * GP);
       if (zeros) __builtin_memcpy(&f.z, at_z + g, GP);
     } else {  // the last groups of a row
 #pragma unroll
       for (int j = 0; j < GP; ++j)
-        if (c * GP + j < KG) {
+        if (k + j * G < K) {
           f.s[j / 2] |= (uint32_t)at_s[g + j] << (16 * (j & 1));
           if (zeros) f.z = (f.z & ~(0xFFu << (8 * j))) | (uint32_t)at_z[g + j] << (8 * j);
         }
     }
     if (++fc == nc) {
       fc = 0;
-      ft += gridDim.x;
+      ft += stride;
       if (ft < tiles) aim();
     }
   };
   Chunk ring[kDeep];
-  if (nc) {
+  if (nc && ft < tiles) {
     aim();
 #pragma unroll
     for (int d = 0; d < kDeep; ++d)
@@ -313,59 +349,129 @@ __global__ __launch_bounds__(kFThreads) void k_linear_int4_few(const X* __restri
   }
   wait_loads<0>();
   __syncthreads();
-  const int row = col < M ? col : 0;  // lanes past M repeat row 0
-  const uint8_t* mine = xs + row * pitch;
-  const bf16x8 ones = __builtin_bit_cast(bf16x8, (u32x4){0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
-  f32x4 acc = {0, 0, 0, 0};
+  if ((k_end - k0) % 128) {  // past the end of K anything may lie there
+    const int from = (k_end - k0) * (int)sizeof(X), per = (chunks * 128 * (int)sizeof(X) - from) / 16;
+    for (int u = t; u < M * per; u += kFThreads)
+      *reinterpret_cast<u32x4*>(xs + u / per * pitch + from + u % per * 16) = (u32x4){0, 0, 0, 0};
+    if constexpr (P == 1) __syncthreads();  // else those of the parts
+  }
+  if constexpr (P > 1) {  // eight values of x become their two parts, in place
+    const int per = (k_end - k0) / 8, units = M * per;
+    for (int u = t; u < units; u += kFThreads) {
+      const int r = u / per;
+      const u32x4* v = reinterpret_cast<const u32x4*>(xs + r * pitch + (u - r * per) * 32);
+      uint32_t most = 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t b = v[h][j] & 0x7FFFFFFFu;  // by bits: a NaN's are above an infinity's
+          most = b > most ? b : most;
+        }
+      atomicMax(&rmax[r], most);
+    }
+    __syncthreads();
+    for (int u = t; u < units; u += kFThreads) {
+      const int r = u / per;
+      u32x4* v = reinterpret_cast<u32x4*>(xs + r * pitch + (u - r * per) * 32);
+      u32x4 hi, lo;
+      split8(__builtin_bit_cast(f32x4, v[0]), __builtin_bit_cast(f32x4, v[1]), of_exponent(row_factor(rmax[r])), hi, lo);
+      v[0] = lo;
+      v[1] = hi;
+    }
+    __syncthreads();
+  }
+  // the eight values from k on of row 16 m + col (rows past M repeat row 0)
+  const uint8_t* my_x[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) my_x[m] = xs + (m * 16 + col < M ? m * 16 + col : 0) * pitch;
+  auto load_x = [&](int m, int k, int part) {
+    return *reinterpret_cast<const u32x4*>(my_x[m] + k * (int)sizeof(X) + part * 16);
+  };
+  for (int c = wave; c < chunks; c += kFWaves) {
+    const u32x4 ones = {Mfma<X>::ones, Mfma<X>::ones, Mfma<X>::ones, Mfma<X>::ones};
+#pragma unroll
+    for (int j = 0; j < GP; ++j)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        f32x4 of_x = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = j * (4 / GP); i < (j + 1) * (4 / GP); ++i)
+#pragma unroll
+          for (int part = 0; part < P; ++part)
+            of_x = Mfma<X>::mul16(load_x(m, c * 128 + place_of<G>(p, i), part), ones, of_x);
+        if (col == 0) table[(c * GP + j) * MT * 4 + m * 4 + p] = of_x;  // rows 16 m + 4 p + (0, 1, 2, 3)
+      }
+  }
+  __syncthreads();
+  f32x4 acc[MT] = {};
   auto multiply = [&](Chunk f, int c) {
     regroup<G>(f.w);
-    const bool whole = c * 128 + 128 <= K;
 #pragma unroll
     for (int j = 0; j < GP; ++j) {
-      f32x4 sum = {0, 0, 0, 0}, of_x = {0, 0, 0, 0};
+      f32x4 sum[MT] = {};
 #pragma unroll
       for (int i = j * (4 / GP); i < (j + 1) * (4 / GP); ++i) {
         const int k = c * 128 + place_of<G>(p, i);
-        Parts<X> a;
-        a.load(mine + k * sizeof(X));
-        const bf16x8 b = codes_bf16(f.w[i]);
+        const u32x4 b = codes_of<X>(f.w[i]);
 #pragma unroll
-        for (int part = 0; part < Parts<X>::n; ++part) {
-          if (!whole && k >= K) a.p[part] = __builtin_bit_cast(bf16x8, (u32x4){0, 0, 0, 0});  // past the row: anything may lie there
-          sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[part], b, sum, 0, 0, 0);
-          of_x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[part], ones, of_x, 0, 0, 0);
-        }
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int part = 0; part < P; ++part) sum[m] = Mfma<X>::mul16(load_x(m, k, part), b, sum[m]);
       }
       const float s = __uint_as_float(j & 1 ? f.s[j / 2] & 0xFFFF0000u : f.s[j / 2] << 16);
       const float z = (float)(f.z >> (8 * j) & 0xFFu);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(s, __builtin_fmaf(-z, of_x[r], sum[r]), acc[r]);
+      for (int m = 0; m < MT; ++m) {
+        const f32x4 of_x = table[(c * GP + j) * MT * 4 + m * 4 + p];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[m][r] = __builtin_fmaf(s, __builtin_fmaf(-z, of_x[r], sum[m][r]), acc[m][r]);
+      }
+    }
+  };
+  auto store = [&](int m, int64_t n, float y) {  // row m's sum for weight row n
+    if constexpr (P > 1) y *= of_exponent(254u - row_factor(rmax[m]));
+    if (!SHARE && parts) {
+      parts[((int64_t)blockIdx.y * M + m) * N + n] = y;
+    } else {
+      if (bias) y += bias[n];
+      store1(out + m * pitch_out + n, y);
     }
   };
   int buf = 0;
   auto finish = [&](int64_t tile) {
-    red[(buf * kFWaves + wave) * 64 + lane] = acc;
-    acc = (f32x4){0, 0, 0, 0};
-    __syncthreads();
-    if (t < 256) {
-      float y = 0.0f;
+    if constexpr (SHARE) {
+      red[(buf * kFWaves + wave) * 64 + lane] = acc[0];
+      __syncthreads();
+      if (t < 256) {
+        float y = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kFWaves; ++w) y += reinterpret_cast<const float*>(red)[(buf * kFWaves + w) * 256 + t];
-      // float t of a partial tile: register t % 4 of lane t / 4
-      const int m = (t >> 6) * 4 + (t & 3);
-      const int64_t n = tile * 16 + (t >> 2 & 15);
-      if (m < M && n < N) {
-        if (bias) y += bias[n];
-        store1(out + m * N + n, y);
+        for (int w = 0; w < kFWaves; ++w) y += reinterpret_cast<const float*>(red)[(buf * kFWaves + w) * 256 + t];
+        // float t of a partial tile: register t % 4 of lane t / 4
+        const int m = (t >> 6) * 4 + (t & 3);
+        const int64_t n = tile * 16 + (t >> 2 & 15);
+        if (m < M && n < N) store(m, n, y);
       }
+      buf ^= 1;  // the next tile's sums go elsewhere: its barrier stands between this one's reads and their reuse
+    } else {
+      const int64_t n = tile * 16 + col;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = m * 16 + p * 4 + r;
+          if (row < M && n < N) store(row, n, acc[m][r]);
+        }
     }
-    buf ^= 1;  // the next tile's sums go elsewhere: its barrier stands between this one's reads and their reuse
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[m] = (f32x4){0, 0, 0, 0};
   };
   if (nc == 0) {
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) finish(tile);
+    if constexpr (SHARE)
+      for (int64_t tile = tile0; tile < tiles; tile += stride) finish(tile);
     return;
   }
-  int64_t tile = blockIdx.x;
+  int64_t tile = tile0;
   int c = 0;
   while (tile < tiles) {
 #pragma unroll
@@ -376,32 +482,11 @@ __global__ __launch_bounds__(kFThreads) void k_linear_int4_few(const X* __restri
         if (++c == nc) {
           finish(tile);
           c = 0;
-          tile += gridDim.x;
+          tile += stride;
         }
       }
     }
   }
-}
-
-int64_t few_rows(int64_t K, int dtype) {  // rows of x that fit
-  const int64_t pitch = dtype == BSQ_F32 ? few_pitch<float>(K) : few_pitch<uint16_t>(K);
-  const int64_t rows = (kFewLds - kFewRed) / pitch;
-  return rows < kFewRows ? rows : kFewRows;
-}
-
-template <typename X, typename T, int G>
-void launch_few(const X* x, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, const float* bias,
-                int64_t M, int64_t N, int64_t K, T* out, hipStream_t s) {
-  const int64_t bytes = M * few_pitch<X>(K) + kFewRed, tiles = (N + 15) / 16;
-  const bool half = bytes <= kFewLds / 2;
-  const int64_t most = bsqh::device_cus() * (half ? 2 : 1);
-  const dim3 grid((unsigned)(tiles < most ? tiles : most));
-  if (half)
-    hipLaunchKernelGGL((k_linear_int4_few<X, T, G, kFewLds / 2>), grid, dim3(kFThreads), 0, s, x, codes, scales, zeros,
-                       bias, (int)M, N, (int)K, out);
-  else
-    hipLaunchKernelGGL((k_linear_int4_few<X, T, G, kFewLds>), grid, dim3(kFThreads), 0, s, x, codes, scales, zeros, bias,
-                       (int)M, N, (int)K, out);
 }
 
 // ---------------------------------------------------------------- many rows
@@ -434,46 +519,33 @@ __global__ __launch_bounds__(kUThreads) void k_unpack_int4(const u32x2* __restri
   if (u % lanes == 0) turned[g % KG * pitch + g / KG] = from_bf16(scales[g]);
 }
 
-// float32 activations as two planes of fp16: a row is scaled by the power of two
-// that brings its largest value to [2^14, 2^15), which is exact, and each value
-// is cut into its nearest fp16 and the nearest of the rest: 22 bits, down to 2^-16
-// of the row's largest; below that to 2^-39 of it. (Three bf16 planes would keep
-// all 24 bits for half as many matrix instructions again; the float32 sums are
-// off by more than the two bits.) A workgroup a row.
+// float32 activations as two planes of fp16, the smaller parts first, and what
+// undoes the rows' scaling. A workgroup a row.
 __global__ __launch_bounds__(kUThreads) void k_split_f32(const f32x4* __restrict__ x, int64_t rows, int K,
-                                                        f16x8* __restrict__ planes, float* __restrict__ back) {
-  __shared__ float red[kUThreads / 64];
+                                                        u32x4* __restrict__ planes, float* __restrict__ back) {
+  __shared__ uint32_t red[kUThreads / 64];
   const int64_t row = blockIdx.x;
   const f32x4* from = x + row * (K / 4);
-  float most = 0.0f;
+  uint32_t most = 0;
   for (int i = threadIdx.x; i < K / 4; i += kUThreads) {
-    const f32x4 v = from[i];
+    const u32x4 v = __builtin_bit_cast(u32x4, from[i]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) most = fmaxf(most, fabsf(v[j]));
+    for (int j = 0; j < 4; ++j) most = (v[j] & 0x7FFFFFFFu) > most ? v[j] & 0x7FFFFFFFu : most;
   }
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor(most, o, 64));
+  for (int o = 32; o > 0; o >>= 1) {
+    const uint32_t other = (uint32_t)__shfl_xor((int)most, o, 64);
+    most = other > most ? other : most;
+  }
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = most;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kUThreads / 64; ++w) most = fmaxf(most, red[w]);
-  // exponent of the largest, biased; a row with an infinity goes as it is (NaN and infinities stay such in fp16)
-  const int e = (int)(__float_as_uint(most) >> 23);
-  const int up = most < __builtin_inff() ? (141 - e < 126 ? 141 - e : 126) : 0;
-  const float f = __uint_as_float((uint32_t)(127 + up) << 23);
-  if (threadIdx.x == 0) back[row] = __uint_as_float((uint32_t)(127 - up) << 23);
+  for (int w = 0; w < kUThreads / 64; ++w) most = red[w] > most ? red[w] : most;
+  const uint32_t e = row_factor(most);
+  if (threadIdx.x == 0) back[row] = of_exponent(254u - e);
   for (int i = threadIdx.x; i < K / 8; i += kUThreads) {
-    f16x8 hi, lo;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const f32x4 v = from[2 * i + h];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float y = v[j] * f;
-        hi[4 * h + j] = (_Float16)y;
-        lo[4 * h + j] = (_Float16)(y - (float)hi[4 * h + j]);
-      }
-    }
+    u32x4 hi, lo;
+    split8(from[2 * i], from[2 * i + 1], of_exponent(e), hi, lo);
     planes[row * (K / 8) + i] = lo;
     planes[(rows + row) * (K / 8) + i] = hi;
   }
@@ -488,19 +560,12 @@ __global__ __launch_bounds__(kUThreads) void k_split_f32(const f32x4* __restrict
 // registers by then. A group's accumulators are scaled and added to the sums
 // right before the next group's first instructions write them anew.
 constexpr int kStep = 64;
-template <int PL>
-__device__ __forceinline__ f32x16 multiply(u32x4 a, u32x4 b, f32x16 c) {
-  if constexpr (PL == 1)
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-  else
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-}
-template <typename T, int PL, int G, int WM, int WN, int MI, int NI, int ST>
+template <typename X, typename T, int G, int WM, int WN, int MI, int NI, int ST>
 __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_int4(
     const uint16_t* __restrict__ a, int64_t plane, const float* __restrict__ back, const uint16_t* __restrict__ w,
     const float* __restrict__ scales, int64_t pitch, const float* __restrict__ bias, int64_t M, int N, int K,
     int64_t pitch_out, int splits, int64_t part, T* __restrict__ out) {
-  constexpr int WAVES = WM * WN;
+  constexpr int WAVES = WM * WN, PL = Mfma<X>::parts;
   constexpr int TM = 32 * MI * WM, TN = 32 * NI * WN;
   constexpr int GP = G < kStep ? kStep / G : 1;          // groups of a step
   constexpr int GS = G > kStep ? G / kStep : 1;          // steps of a group
@@ -516,15 +581,20 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_int4(
   static_assert(ST * STAGE <= 163840, "the LDS of a CU");
   __shared__ __attribute__((aligned(16))) uint8_t lds[ST * STAGE > WAVES * OUT ? ST * STAGE : WAVES * OUT];
   const int t = threadIdx.x, wave = uniform(t >> 6), lane = t & 63;
-  // Workgroups go round the 8 XCDs; each XCD takes a contiguous part of the tiles, columns first.
+  // Workgroups go round the 8 XCDs; each XCD takes a contiguous part of the tiles, which lie in bands of kBand rows of
+  // them, a band column by column: what an XCD runs at once shares rows of both operands in its L2.
+  constexpr int kBand = 1024 / TM;
   const int ntn = (N + TN - 1) / TN;
   const int64_t ntiles = gridDim.x / splits;
   const int64_t per = ntiles / 8, extra = ntiles % 8;
   const int64_t b = blockIdx.x % ntiles;
   const int split = (int)(blockIdx.x / ntiles), xcd = (int)(b % 8);
   const int64_t tile = xcd * per + (xcd < extra ? xcd : extra) + b / 8;
-  const int64_t m0 = tile / ntn * TM;
-  const int n0 = (int)(tile % ntn) * TN;
+  const int64_t band = tile / ((int64_t)kBand * ntn), in_band = tile - band * kBand * ntn;
+  const int64_t left = ntiles / ntn - band * kBand;  // rows of tiles from the band on
+  const int high = left < kBand ? (int)left : kBand;
+  const int64_t m0 = (band * kBand + in_band % high) * TM;
+  const int n0 = (int)(in_band / high) * TN;
   const int rows_a = M - m0 < TM ? (int)(M - m0) : TM, rows_b = N - n0 < TN ? N - n0 : TN;
   const int units = (K + GS * kStep - 1) / (GS * kStep);  // whole groups and whole steps
   const int steps = (K + kStep - 1) / kStep;
@@ -609,12 +679,12 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_int4(
       if (first) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) sum[i][j][r] = __builtin_fmaf(scale[j], acc[i][j][r], sum[i][j][r]);
-        acc[i][j] = multiply<PL>(fa[q & 1][0][i], fb[q & 1][j], (f32x16){});
+        acc[i][j] = Mfma<X>::mul32(fa[q & 1][0][i], fb[q & 1][j], (f32x16){});
       } else {
-        acc[i][j] = multiply<PL>(fa[q & 1][0][i], fb[q & 1][j], acc[i][j]);
+        acc[i][j] = Mfma<X>::mul32(fa[q & 1][0][i], fb[q & 1][j], acc[i][j]);
       }
 #pragma unroll
-      for (int p = 1; p < PL; ++p) acc[i][j] = multiply<PL>(fa[q & 1][p][i], fb[q & 1][j], acc[i][j]);
+      for (int p = 1; p < PL; ++p) acc[i][j] = Mfma<X>::mul32(fa[q & 1][p][i], fb[q & 1][j], acc[i][j]);
     }
     if (first) scale[j] = now[q / GQ][j];
   };
@@ -705,38 +775,66 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_int4(
 // The parts of a split K, added in their order.
 template <typename T>
 __global__ __launch_bounds__(kUThreads) void k_join_int4(const float* __restrict__ parts, int splits, int64_t part,
-                                                        int64_t M, int N, const float* __restrict__ bias,
+                                                        int64_t M, int64_t N, const float* __restrict__ bias,
                                                         int64_t pitch_out, T* __restrict__ out) {
   const int64_t u = (int64_t)blockIdx.x * kUThreads + threadIdx.x;
   if (u >= part) return;
   float y = 0.0f;
   for (int s = 0; s < splits; ++s) y += parts[s * part + u];
-  const int64_t m = u / N;
-  const int n = (int)(u - m * N);
+  const int64_t m = u / N, n = u - m * N;
   if (bias) y += bias[n];
   store1(out + m * pitch_out + n, y);
 }
 
 // How a call's work is laid out.
 struct Plan {
-  bool few;
-  int64_t rows;     // few: rows of x a launch; many: rows of x split at a time
-  int64_t slice;    // rows of weights unpacked at a time (of 128)
-  int tile, splits; // tile: rows and columns of a workgroup's outputs, 0 64 x 64, 1 128 x 128, 2 256 x 128
+  enum Way { kShare, kSlabs, kTiles } way;
+  int64_t rows;      // of x a launch
+  int mt;            // kSlabs: rows of 16
+  int64_t slab;      // kSlabs: values of K of a workgroup
+  int splits;        // slabs, or parts of K of a tile
+  int64_t slice;     // rows of weights at a time (kTiles: of 128)
+  int tile;          // kTiles: see launch_tiles
   size_t w, s, x, back, parts;  // bytes of the workspace
 };
 
 constexpr int64_t kUnpacked = (int64_t)64 << 20;  // bytes of unpacked weights and of split activations at a time
+constexpr int64_t kParts = (int64_t)128 << 20;    // bytes of slabs' sums at a time
+
+int64_t share_bytes(int64_t M, int64_t K, int64_t group, int64_t size) {
+  return M * few_pitch(K, size) + few_table(K, group, 1) + kFewRed;
+}
 
 Plan plan_of(int64_t M, int64_t N, int64_t K, int64_t group, int dtype) {
   Plan p = {};
-  const int64_t fit = few_rows(K, dtype);
-  p.few = M <= 3 * fit;
-  if (p.few) {
-    const int64_t launches = (M + fit - 1) / fit;
-    p.rows = (M + launches - 1) / launches;
+  const int64_t size = dtype == BSQ_F32 ? 4 : 2, cus = bsqh::device_cus();
+  p.splits = 1;
+  if (M <= 16 && share_bytes(M, K, group, size) <= kFewLds) {
+    p.way = Plan::kShare;
+    p.rows = M;
+    p.slab = K;
     return p;
   }
+  if (M <= 192) {
+    p.way = Plan::kSlabs;
+    const int64_t launches = (M + 63) / 64;
+    p.rows = (M + launches - 1) / launches;
+    p.mt = p.rows <= 16 ? 1 : p.rows <= 32 ? 2 : 4;
+    // whole loads, kSlabLds of x at most, and as many slabs as give each wave of the card a tile
+    const int64_t unit = 1024 / size, most = kSlabLds / (16 * p.mt * size), tiles = (N + 15) / 16;
+    int64_t want = (kFWaves * cus + tiles - 1) / tiles;
+    if (want < (K + most - 1) / most) want = (K + most - 1) / most;
+    p.slab = ((K + want - 1) / want + unit - 1) / unit * unit;
+    p.splits = (int)((K + p.slab - 1) / p.slab);
+    p.slice = N;
+    if (p.splits > 1) {
+      const int64_t wide = kParts / (p.splits * p.rows * 4) / 128 * 128;
+      if (wide < p.slice) p.slice = wide;
+      p.parts = (size_t)(p.splits * p.rows * p.slice * 4);
+    }
+    return p;
+  }
+  p.way = Plan::kTiles;
   const int64_t whole = (N + 127) / 128 * 128;
   p.slice = kUnpacked / (2 * K) / 128 * 128;
   if (whole < p.slice) p.slice = whole;
@@ -750,9 +848,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int64_t group, int dtype) {
   }
   p.w = (size_t)(p.slice * K * 2);
   p.s = (size_t)(p.slice * (K / group) * 4);
-  const int64_t cus = bsqh::device_cus();
   const int64_t small = ((p.rows + 127) / 128) * (p.slice / 128), big = ((p.rows + 255) / 256) * (p.slice / 128);
-  p.splits = 1;
   if (small * 2 <= cus) {
     p.tile = 0;
     const int64_t tiles = ((p.rows + 63) / 64) * (p.slice / 64), most_splits = K / 256;
@@ -761,30 +857,65 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int64_t group, int dtype) {
     if (sp > 8) sp = 8;
     p.splits = sp < 1 ? 1 : (int)sp;
   } else {
-    p.tile = dtype == BSQ_F32 ? (small > cus && ((p.rows + 191) / 192) * (p.slice / 128) <= cus ? 2 : 1) : big < cus ? 1 : 2;
+    p.tile = dtype == BSQ_F32 ? (small > cus && ((p.rows + 191) / 192) * (p.slice / 128) <= cus ? 2 : 1) : big < cus ? 2 : 3;
   }
   if (p.splits > 1) p.parts = (size_t)(p.splits * p.rows * p.slice * 4);
   return p;
 }
 
-template <typename T, int PL, int G>
+template <typename X, typename T, int G>
+void launch_share(const X* x, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, const float* bias,
+                  int64_t M, int64_t N, int64_t K, T* out, hipStream_t s) {
+  const int64_t tiles = (N + 15) / 16;
+  const bool half = share_bytes(M, K, G, sizeof(X)) <= kFewHalf;
+  const int64_t most = bsqh::device_cus() * (half ? 2 : 1);
+  const dim3 grid((unsigned)(tiles < most ? tiles : most));
+#define BSQ_FEW(BYTES)                                                                                                 \
+  hipLaunchKernelGGL((k_linear_int4_few<X, T, G, 1, true, BYTES>), grid, dim3(kFThreads), 0, s, x, codes, scales, zeros, \
+                     bias, (int)M, N, (int)K, (int)K, nullptr, N, out)
+  if (half) BSQ_FEW(kFewHalf);
+  else BSQ_FEW(kFewLds);
+#undef BSQ_FEW
+}
+
+// The slabs' sums go to `parts` where there are several.
+template <typename X, typename T, int G>
+void launch_slabs(const Plan& p, const X* x, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros,
+                  const float* bias, int64_t M, int64_t N, int64_t K, float* parts, int64_t pitch_out, T* out,
+                  hipStream_t s) {
+  const int64_t tiles = (N + 15) / 16, groups = (tiles + kFWaves - 1) / kFWaves;
+  int64_t most = bsqh::device_cus() / p.splits;  // workgroups of a slab
+  if (most < 1) most = 1;
+  const dim3 grid((unsigned)(groups < most ? groups : most), (unsigned)p.splits);
+#define BSQ_FEW(MT)                                                                                             \
+  hipLaunchKernelGGL((k_linear_int4_few<X, T, G, MT, false, kSlabLds + 256 * MT + 8192>), grid, dim3(kFThreads), 0, s, \
+                     x, codes, scales, zeros, bias, (int)M, N, (int)K, (int)p.slab, p.splits > 1 ? parts : nullptr,   \
+                     pitch_out, out)
+  if (p.mt == 1) BSQ_FEW(1);
+  else if (p.mt == 2) BSQ_FEW(2);
+  else BSQ_FEW(4);
+#undef BSQ_FEW
+}
+
+template <typename X, typename T, int G>
 void launch_tiles(const Plan& p, const uint16_t* a, int64_t plane, const float* back, const uint16_t* w, const float* sc,
                   const float* bias, int64_t M, int64_t N, int64_t K, int64_t pitch_out, int64_t part, T* out,
                   hipStream_t s) {
 #define BSQ_TILE(WM, WN, MI, NI, ST)                                                                                   \
-  hipLaunchKernelGGL((k_gemm_int4<T, PL, G, WM, WN, MI, NI, ST>),                                                     \
+  hipLaunchKernelGGL((k_gemm_int4<X, T, G, WM, WN, MI, NI, ST>),                                                     \
                      dim3((unsigned)(((M + 32 * MI * WM - 1) / (32 * MI * WM)) * ((N + 32 * NI * WN - 1) / (32 * NI * WN)) * \
                                      p.splits)),                                                                      \
                      dim3(64 * WM * WN), 0, s, a, plane, back, w, sc, p.slice, bias, M, (int)N, (int)K, pitch_out,    \
                      p.splits, part, out)
-  if constexpr (PL == 1) {
-    if (p.tile == 0) BSQ_TILE(2, 2, 1, 1, 3);
-    else if (p.tile == 1) BSQ_TILE(2, 2, 2, 2, 2);
+  if constexpr (sizeof(X) == 2) {
+    if (p.tile == 0) BSQ_TILE(2, 2, 1, 1, 8);
+    else if (p.tile == 1) BSQ_TILE(2, 2, 2, 2, 4);
+    else if (p.tile == 2) BSQ_TILE(2, 2, 2, 2, 2);
     else BSQ_TILE(4, 2, 2, 2, 3);
   } else {
-    if (p.tile == 0) BSQ_TILE(2, 2, 1, 1, 3);
-    else if (p.tile == 1) BSQ_TILE(2, 2, 2, 2, 3);
-    else BSQ_TILE(2, 2, 3, 2, 2);
+    if (p.tile == 0) BSQ_TILE(2, 2, 1, 1, 6);
+    else if (p.tile == 1) BSQ_TILE(4, 2, 1, 2, 3);
+    else BSQ_TILE(2, 4, 3, 1, 2);
   }
 #undef BSQ_TILE
 }
@@ -792,14 +923,32 @@ void launch_tiles(const Plan& p, const uint16_t* a, int64_t plane, const float* 
 template <typename X, typename T, int G>
 int run_linear(const X* x, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, const float* bias,
                int64_t M, int64_t N, int64_t K, T* out, uint8_t* ws, hipStream_t s) {
-  constexpr int PL = sizeof(X) == 4 ? 2 : 1;
-  const Plan p = plan_of(M, N, K, G, PL == 2 ? BSQ_F32 : BSQ_BF16);
-  if (p.few) {
-    for (int64_t m = 0; m < M; m += p.rows)
-      launch_few<X, T, G>(x + m * K, codes, scales, zeros, bias, M - m < p.rows ? M - m : p.rows, N, K, out + m * N, s);
+  const Plan p = plan_of(M, N, K, G, sizeof(X) == 4 ? BSQ_F32 : BSQ_BF16);
+  auto join = [&](const float* parts, int64_t m, int64_t n, const float* add, T* to) {
+    const int64_t part = m * n;
+    hipLaunchKernelGGL((k_join_int4<T>), dim3((unsigned)((part + kUThreads - 1) / kUThreads)), dim3(kUThreads), 0, s,
+                       parts, p.splits, part, m, n, add, N, to);
+  };
+  if (p.way == Plan::kShare) {
+    launch_share<X, T, G>(x, codes, scales, zeros, bias, M, N, K, out, s);
     return bsqh::launch_status();
   }
-  typedef typename std::conditional<PL == 2, f16x8, bf16x8>::type V;
+  if (p.way == Plan::kSlabs) {
+    float* parts = reinterpret_cast<float*>(ws);
+    for (int64_t n0 = 0; n0 < N; n0 += p.slice) {
+      const int64_t n = N - n0 < p.slice ? N - n0 : p.slice, g0 = n0 * (K / G);
+      const float* add = bias ? bias + n0 : nullptr;
+      for (int64_t m0 = 0; m0 < M; m0 += p.rows) {
+        const int64_t m = M - m0 < p.rows ? M - m0 : p.rows;
+        T* to = out + m0 * N + n0;
+        launch_slabs<X, T, G>(p, x + m0 * K, codes + n0 * (K / 2), scales + g0, zeros ? zeros + g0 : nullptr, add, m, n, K,
+                              parts, N, to, s);
+        if (p.splits > 1) join(parts, m, n, add, to);
+      }
+    }
+    return bsqh::launch_status();
+  }
+  typedef typename Mfma<X>::V V;
   V* w = reinterpret_cast<V*>(ws);
   float* turned = reinterpret_cast<float*>(ws + p.w);
   uint16_t* planes = reinterpret_cast<uint16_t*>(ws + p.w + p.s);
@@ -814,22 +963,20 @@ int run_linear(const X* x, const uint8_t* codes, const uint16_t* scales, const u
     for (int64_t m0 = 0; m0 < M; m0 += p.rows) {
       const int64_t m = M - m0 < p.rows ? M - m0 : p.rows;
       const uint16_t* a = reinterpret_cast<const uint16_t*>(x + m0 * K);
-      if constexpr (PL == 2) {
+      if constexpr (sizeof(X) == 4) {
         if (n0 == 0 || M > p.rows)
           hipLaunchKernelGGL(k_split_f32, dim3((unsigned)m), dim3(kUThreads), 0, s,
-                             reinterpret_cast<const f32x4*>(x + m0 * K), m, (int)K, reinterpret_cast<f16x8*>(planes), back);
+                             reinterpret_cast<const f32x4*>(x + m0 * K), m, (int)K, reinterpret_cast<u32x4*>(planes), back);
         a = planes;
       }
       const uint16_t* wb = reinterpret_cast<const uint16_t*>(w);
       const float* add = bias ? bias + n0 : nullptr;
       T* to = out + m0 * N + n0;
       if (p.splits == 1) {
-        launch_tiles<T, PL, G>(p, a, m * K, back, wb, turned, add, m, n, K, N, 0, to, s);
+        launch_tiles<X, T, G>(p, a, m * K, back, wb, turned, add, m, n, K, N, 0, to, s);
       } else {
-        const int64_t part = m * n;
-        launch_tiles<float, PL, G>(p, a, m * K, back, wb, turned, nullptr, m, n, K, n, part, parts, s);
-        hipLaunchKernelGGL((k_join_int4<T>), dim3((unsigned)((part + kUThreads - 1) / kUThreads)), dim3(kUThreads), 0, s,
-                           parts, p.splits, part, m, (int)n, add, N, to);
+        launch_tiles<X, float, G>(p, a, m * K, back, wb, turned, nullptr, m, n, K, n, m * n, parts, s);
+        join(parts, m, n, add, to);
       }
     }
   }

@@ -144,6 +144,30 @@ def test_few_ragged(M, N, K, group, dtype):
     check_linear(rng, M, N, K, group, True, dtype, bias=True)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("M,N,K", [(17, 16, 128), (31, 100, 2048), (48, 515, 4096), (64, 33, 8192), (192, 70, 1152),
+                                   (16, 50, 8192), (130, 4100, 512)])
+def test_slabs(M, N, K, group, dtype):
+    """More rows than share a workgroup's LDS whole: slabs of K, one or several, one launch or several."""
+    rng = np.random.default_rng(M + N + K)
+    check_linear(rng, M, N, K, group, True, dtype)
+    check_linear(rng, M, N, K, group, False, dtype, BF16, bias=True)
+
+
+def test_slabs_of_many_channels():
+    """More channels than the slabs' sums are kept for at a time: the columns around the border and the last ones."""
+    rng = np.random.default_rng(11)
+    M, N, K, group = 64, 66000, 8192, 128
+    (c, s, z), w = weights(rng, N, K, group, True)
+    x, xv = dev(rng.standard_normal((M, K)), BF16)
+    log(f"linear_int4 {M} x {N} x {K}")
+    y = bsq.linear_int4(x, *w, out_dtype=F32)
+    for n in (slice(0, 20), slice(65500, 65560), slice(N - 20, N)):
+        want, bound = Q.linear(xv, c[n], s[n], z[n])
+        assert (np.abs(y[:, n].double().cpu().numpy() - want) <= bound + 2.0 ** -24 * np.abs(want)).all()
+
+
 @pytest.mark.parametrize("dtype,out", [(BF16, F32), (F32, BF16)])
 def test_other_output_type(dtype, out):
     rng = np.random.default_rng(1)
