@@ -149,6 +149,7 @@ struct Mfma<uint16_t> {
   typedef bf16x8 V;
   static constexpr int parts = 1;
   static constexpr uint32_t ones = 0x3F803F80u;
+  static __device__ __forceinline__ __bf16 near(float v) { return (__bf16)v; }
   static __device__ __forceinline__ f32x4 mul16(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b), c, 0, 0, 0);
   }
@@ -165,6 +166,7 @@ struct Mfma<float> {
   typedef f16x8 V;
   static constexpr int parts = 2;
   static constexpr uint32_t ones = 0x3C003C00u;
+  static __device__ __forceinline__ _Float16 near(float v) { return (_Float16)v; }
   static __device__ __forceinline__ f32x4 mul16(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b), c, 0, 0, 0);
   }
@@ -490,33 +492,50 @@ __global__ __launch_bounds__(kFThreads) void k_linear_int4_few(const X* __restri
 }
 
 // ---------------------------------------------------------------- many rows
-// The weights are unpacked to bf16 integers q - z once for all rows of
-// activations (2 bytes each in the workspace, a slice of the rows of weights at
-// a time), their scales turned to [group][row]; then tiles by matrix
-// instructions, with the scales brought in at the end of each group: a tile has
-// one set of accumulators for the group and one for the sum over groups.
-//
-// PL parts of the activations: 1 (bf16) or 2 (float32, split beforehand).
+// The weights are unpacked to 16-bit integers q - z once for all rows of
+// activations (in the workspace, a slice of the rows of weights at a time), their
+// scales turned to [group][row]; then tiles by matrix instructions. The
+// accumulators hold the sum in units of the group's scale: before group g they
+// are multiplied by s[g - 1] / s[g], at the end by the last scale, so that there
+// is one set of them (a second one for the group's own sum left room for tiles of
+// 256 x 128 only, which are bound by L2: 12 TB/s, 1.07 PFLOP/s).
 constexpr int kUThreads = 256;
-template <typename V>
-__global__ __launch_bounds__(kUThreads) void k_unpack_int4(const u32x2* __restrict__ codes,
+// A wave a row of weights. The tiles hold sums in units of a group's scale, so no
+// scale may be too small for the others': one below 2^-64 of the row's largest is
+// raised to that, and its integers become the (then rounded) smaller values.
+// turned: [group][row] the scale of the group before over the group's, then the
+// same of the scales (divisions here, once, cost the tiles nothing).
+template <typename X>
+__global__ __launch_bounds__(kUThreads) void k_unpack_int4(const uint32_t* __restrict__ codes,
                                                           const uint16_t* __restrict__ scales,
-                                                          const uint8_t* __restrict__ zeros, int64_t units, int lanes,
-                                                          int KG, int64_t pitch, V* __restrict__ w,
+                                                          const uint8_t* __restrict__ zeros, int64_t rows, int units,
+                                                          int shift, int KG, int64_t pitch, u32x4* __restrict__ w,
                                                           float* __restrict__ turned) {
-  const int64_t u = (int64_t)blockIdx.x * kUThreads + threadIdx.x;
-  if (u >= units) return;
-  const u32x2 c = codes[u];
-  const int64_t g = u / lanes;
-  const float z = zeros ? (float)zeros[g] : 8.0f;
+  const int64_t row = (int64_t)blockIdx.x * (kUThreads / 64) + (threadIdx.x >> 6);
+  if (row >= rows) return;
+  const int lane = threadIdx.x & 63;
+  float most = 0.0f;
+  for (int g = lane; g < KG; g += 64) most = fmaxf(most, fabsf(from_bf16(scales[row * KG + g])));
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    V v;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = (decltype(v[0] + v[0]))((float)(c[i] >> (4 * j) & 15u) - z);
-    w[u * 2 + i] = v;
+  for (int o = 32; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor(most, o, 64));
+  const float least = most > 0.0f ? most * 0x1p-64f : 1.0f;
+  auto raised = [&](float v) { return fabsf(v) < least ? least : v; };
+  for (int g = lane; g < KG; g += 64) {
+    const float s = raised(from_bf16(scales[row * KG + g]));
+    turned[g * pitch + row] = g ? raised(from_bf16(scales[row * KG + g - 1])) / s : 0.0f;
+    turned[(KG + g) * pitch + row] = s;
   }
-  if (u % lanes == 0) turned[g % KG * pitch + g / KG] = from_bf16(scales[g]);
+#pragma unroll 4
+  for (int u = lane; u < units; u += 64) {  // eight codes
+    const uint32_t c = codes[row * units + u];
+    const int64_t g = row * KG + (u >> shift);
+    const float z = zeros ? (float)zeros[g] : 8.0f, own = from_bf16(scales[g]), s = raised(own);
+    const float f = s == own ? 1.0f : own / s;  // NaN: f is NaN, and the values
+    typename Mfma<X>::V v;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = Mfma<X>::near(((float)(c >> (4 * j) & 15u) - z) * f);
+    w[row * units + u] = __builtin_bit_cast(u32x4, v);
+  }
 }
 
 // float32 activations as two planes of fp16, the smaller parts first, and what
@@ -555,15 +574,15 @@ __global__ __launch_bounds__(kUThreads) void k_split_f32(const f32x4* __restrict
 // row r lies at p ^ (r / 2 % 8), so that 16 rows at one piece meet 16 different
 // banks. Waves of 32 MI x 32 NI outputs, WM x WN of them; K advances through a
 // ring of ST stages in LDS, filled by loads that go straight there and are
-// counted here. A wave reads the next fragments while it multiplies: the barrier
-// stands before the last instructions along a step, whose fragments are in
-// registers by then. A group's accumulators are scaled and added to the sums
-// right before the next group's first instructions write them anew.
-constexpr int kStep = 64;
+// counted here. A wave reads the fragments of the instructions after the next
+// while it multiplies (the ones right ahead came too late: 0.67 us a step of
+// 128 x 128 tiles): the barrier stands before the last kAhead instructions along
+// a step, whose fragments are in registers by then.
+constexpr int kStep = 64, kAhead = 2;
 template <typename X, typename T, int G, int WM, int WN, int MI, int NI, int ST>
 __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_int4(
     const uint16_t* __restrict__ a, int64_t plane, const float* __restrict__ back, const uint16_t* __restrict__ w,
-    const float* __restrict__ scales, int64_t pitch, const float* __restrict__ bias, int64_t M, int N, int K,
+    const float* __restrict__ turned, int64_t pitch, const float* __restrict__ bias, int64_t M, int N, int K,
     int64_t pitch_out, int splits, int64_t part, T* __restrict__ out) {
   constexpr int WAVES = WM * WN, PL = Mfma<X>::parts;
   constexpr int TM = 32 * MI * WM, TN = 32 * NI * WN;
@@ -605,7 +624,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_int4(
   const rsrc_words ra = descriptor(a + m0 * K, (uint32_t)(((PL - 1) * plane + (int64_t)rows_a * K) * 2));
   const rsrc_words rb = descriptor(w + (int64_t)n0 * K, (uint32_t)rows_b * K * 2);
   const int KG = K / G;
-  const rsrc_words rs = descriptor(scales + n0, (uint32_t)(((int64_t)(KG - 1) * pitch + TN) * 4));
+  const rsrc_words rs = descriptor(turned + n0, (uint32_t)(((int64_t)(KG - 1) * pitch + TN) * 4));
   uint32_t va[LA], vb[LB];
   {
     const int r = lane >> 3;
@@ -631,7 +650,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_int4(
     } else if (i < LA + LB) {
       load_to_lds<16>(rb, buffer_at(there, true, vb[i < LA || i >= LA + LB ? 0 : i - LA], k),
                       at + PL * TM * 128 + (wave * LB + i - LA) * 1024);
-    } else {  // 64 scales: part c of the step's groups (several waves may fetch the same)
+    } else {  // 64 ratios of scales: part c of the step's groups (several waves may fetch the same)
       const int c = wave % (SCALES / 256);
       int g = step * kStep / G + c / (TN / 64);
       if (g >= KG) g = KG - 1;
@@ -639,7 +658,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_int4(
       load_to_lds<4>(rs, buffer_at(there, true, vs, 0), at + (PL * TM + TN) * 128 + c * 256);
     }
   };
-  // slot k of the loads that fill one stage: the last NI rows of a step begin, the others end in the next step
+  // slot k of the loads that fill one stage: the last kAhead * NI rows of a step begin, the others end in the next step
   auto slot_of = [&](int step, int stage, int k) {
 #pragma unroll
     for (int i = k * LOADS / SLOTS; i < (k + 1) * LOADS / SLOTS; ++i) fetch(step, stage, i);
@@ -647,46 +666,45 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_int4(
 #pragma unroll
   for (int s = 0; s < ST; ++s)
 #pragma unroll
-    for (int k = 0; k < (s < ST - 1 ? SLOTS : NI); ++k) slot_of(st0 + s, s, k);
-  wait_loads<(ST - 2) * LOADS + NI * LOADS / SLOTS>();
+    for (int k = 0; k < (s < ST - 1 ? SLOTS : kAhead * NI); ++k) slot_of(st0 + s, s, k);
+  wait_loads<(ST - 2) * LOADS + kAhead * NI * LOADS / SLOTS>();
   lds_barrier();
   const int wm = wave / WN, wn = wave % WN;
   const int myrow = (lane & 31) * 128, mysw = lane >> 1 & 7;
-  u32x4 fa[2][PL][MI], fb[2][NI];  // fragments of even and odd instructions along K
+  u32x4 fa[4][PL][MI], fb[4][NI];  // fragments of the instructions along a step, kAhead + 1 of them alive
   auto read = [&](int stage, int q, int i) {
     const uint8_t* p = lds + stage * STAGE + myrow + ((2 * q + (lane >> 5)) ^ mysw) * 16;
     if (i < NI) {
-      fb[q & 1][i < NI ? i : 0] = *reinterpret_cast<const u32x4*>(p + (PL * TM + (wn * NI + i) * 32) * 128);
+      fb[q][i < NI ? i : 0] = *reinterpret_cast<const u32x4*>(p + (PL * TM + (wn * NI + i) * 32) * 128);
     } else {
       const int j = i - NI < 0 ? 0 : i - NI, pl = j / MI, im = j % MI;
-      fa[q & 1][pl][im] = *reinterpret_cast<const u32x4*>(p + (pl * TM + (wm * MI + im) * 32) * 128);
+      fa[q][pl][im] = *reinterpret_cast<const u32x4*>(p + (pl * TM + (wm * MI + im) * 32) * 128);
     }
   };
 #pragma unroll
-  for (int i = 0; i < FRAGS; ++i) read(0, 0, i);
-  f32x16 sum[MI][NI] = {}, acc[MI][NI] = {};
-  float now[GP][NI], scale[NI] = {};  // of the step's groups, of the group in the accumulators
-  auto scales_of = [&](int stage) {
+  for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+    for (int i = 0; i < FRAGS; ++i) read(0, q, i);
+  f32x16 acc[MI][NI] = {};
+  float ratio[GP][NI];  // of the groups that begin next
+  auto ratios_of = [&](int stage) {
     const float* s = reinterpret_cast<const float*>(lds + stage * STAGE + (PL * TM + TN) * 128) + wn * 32 * NI + (lane & 31);
 #pragma unroll
     for (int g = 0; g < GP; ++g)
 #pragma unroll
-      for (int j = 0; j < NI; ++j) now[g][j] = s[g * TN + j * 32];
+      for (int j = 0; j < NI; ++j) ratio[g][j] = s[g * TN + j * 32];
   };
+  ratios_of(0);
   auto products = [&](int q, int j, bool first) {
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
       if (first) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) sum[i][j][r] = __builtin_fmaf(scale[j], acc[i][j][r], sum[i][j][r]);
-        acc[i][j] = Mfma<X>::mul32(fa[q & 1][0][i], fb[q & 1][j], (f32x16){});
-      } else {
-        acc[i][j] = Mfma<X>::mul32(fa[q & 1][0][i], fb[q & 1][j], acc[i][j]);
+        for (int r = 0; r < 16; ++r) acc[i][j][r] *= ratio[q / GQ][j];
       }
 #pragma unroll
-      for (int p = 1; p < PL; ++p) acc[i][j] = Mfma<X>::mul32(fa[q & 1][p][i], fb[q & 1][j], acc[i][j]);
+      for (int p = 0; p < PL; ++p) acc[i][j] = Mfma<X>::mul32(fa[q][p][i], fb[q][j], acc[i][j]);
     }
-    if (first) scale[j] = now[q / GQ][j];
   };
   const bool half = G == 32 && st1 * kStep > K;  // a last step of which there is half
   const int whole = half ? st1 - 1 : st1;
@@ -697,19 +715,20 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_int4(
     for (int u = 0; u < GS; ++u) {  // the steps of a group (K is whole groups)
       const int step = step0 + u;
       const int next = stage == ST - 1 ? 0 : stage + 1, last = stage == 0 ? ST - 1 : stage - 1;
-      if (u == 0) scales_of(stage);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        if (q == 3) {
+        if (q == 4 - kAhead) {
           wait_loads<(ST - 2) * LOADS>();  // the next stage has come
           lds_barrier();                   // for every wave, and this one is read
         }
 #pragma unroll
         for (int j = 0; j < NI; ++j) {
-          if (q == 3) slot_of(step + ST, stage, j);
-          else slot_of(step + ST - 1, last, (q + 1) * NI + j);
+          if (q >= 4 - kAhead) slot_of(step + ST, stage, (q - (4 - kAhead)) * NI + j);
+          else slot_of(step + ST - 1, last, (q + kAhead) * NI + j);
+          if (q == 3 && j == 0 && u == GS - 1) ratios_of(next);  // this step's are done with
 #pragma unroll
-          for (int z = j * FRAGS / NI; z < (j + 1) * FRAGS / NI; ++z) read(q == 3 ? next : stage, (q + 1) % 4, z);
+          for (int z = j * FRAGS / NI; z < (j + 1) * FRAGS / NI; ++z)
+            read(q >= 4 - kAhead ? next : stage, (q + kAhead) % 4, z);
           products(q, j, q % GQ == 0 && u == 0);
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -717,10 +736,8 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_int4(
       stage = next;
     }
   }
+  static_assert(kAhead == 2, "half a step is in registers");
   if (half) {
-    scales_of(stage);
-#pragma unroll
-    for (int i = 0; i < FRAGS; ++i) read(stage, 1, i);
 #pragma unroll
     for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -731,6 +748,13 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_int4(
 
   // outputs: lane holds column lane % 32 and rows 8 (r / 4) + 4 (lane / 32) + r % 4 of the 32 x 32 tile (i, j); they
   // leave through LDS, 32 rows of the wave at a time, as 16-byte pieces of rows
+  // in units of the last group's scale
+  float scale[NI] = {};
+  if (st0 < st1) {
+    const int g = (st1 * kStep < K ? st1 * kStep : K) / G - 1;
+#pragma unroll
+    for (int j = 0; j < NI; ++j) scale[j] = turned[(int64_t)(KG + g) * pitch + n0 + (wn * NI + j) * 32 + (lane & 31)];
+  }
   T* to_part = out + split * part;
   uint8_t* mylds = lds + wave * OUT;
   const int nw = n0 + wn * 32 * NI;
@@ -748,7 +772,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_int4(
       const float add = bias && n < N ? bias[n] : 0.0f;
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        float y = __builtin_fmaf(scale[j], acc[i][j][r], sum[i][j][r]);
+        float y = scale[j] * acc[i][j][r];
         if constexpr (PL > 1) y *= rows[r / 4][r % 4];
         store1(reinterpret_cast<T*>(mylds + (8 * (r / 4) + 4 * (lane >> 5) + r % 4) * PITCH) + j * 32 + (lane & 31), y + add);
       }
@@ -847,7 +871,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int64_t group, int dtype) {
     p.back = (size_t)((p.rows + 767) / 768 * 768 * 4);  // whole tiles of 64, 128 and 192 rows
   }
   p.w = (size_t)(p.slice * K * 2);
-  p.s = (size_t)(p.slice * (K / group) * 4);
+  p.s = (size_t)(p.slice * (K / group) * 8);
   const int64_t small = ((p.rows + 127) / 128) * (p.slice / 128), big = ((p.rows + 255) / 256) * (p.slice / 128);
   if (small * 2 <= cus) {
     p.tile = 0;
@@ -908,14 +932,13 @@ void launch_tiles(const Plan& p, const uint16_t* a, int64_t plane, const float* 
                      dim3(64 * WM * WN), 0, s, a, plane, back, w, sc, p.slice, bias, M, (int)N, (int)K, pitch_out,    \
                      p.splits, part, out)
   if constexpr (sizeof(X) == 2) {
-    if (p.tile == 0) BSQ_TILE(2, 2, 1, 1, 8);
-    else if (p.tile == 1) BSQ_TILE(2, 2, 2, 2, 4);
-    else if (p.tile == 2) BSQ_TILE(2, 2, 2, 2, 2);
-    else BSQ_TILE(4, 2, 2, 2, 3);
+    if (p.tile == 0) BSQ_TILE(2, 2, 2, 2, 4);
+    else if (p.tile == 1) BSQ_TILE(4, 2, 2, 2, 3);
+    else BSQ_TILE(2, 4, 4, 2, 2);
   } else {
-    if (p.tile == 0) BSQ_TILE(2, 2, 1, 1, 6);
-    else if (p.tile == 1) BSQ_TILE(4, 2, 1, 2, 3);
-    else BSQ_TILE(2, 4, 3, 1, 2);
+    if (p.tile == 0) BSQ_TILE(4, 2, 1, 2, 3);
+    else if (p.tile == 1) BSQ_TILE(2, 4, 3, 1, 2);
+    else BSQ_TILE(2, 4, 2, 2, 2);
   }
 #undef BSQ_TILE
 }
@@ -948,18 +971,18 @@ int run_linear(const X* x, const uint8_t* codes, const uint16_t* scales, const u
     }
     return bsqh::launch_status();
   }
-  typedef typename Mfma<X>::V V;
-  V* w = reinterpret_cast<V*>(ws);
+  u32x4* w = reinterpret_cast<u32x4*>(ws);
   float* turned = reinterpret_cast<float*>(ws + p.w);
   uint16_t* planes = reinterpret_cast<uint16_t*>(ws + p.w + p.s);
   float* back = reinterpret_cast<float*>(ws + p.w + p.s + p.x);
   float* parts = reinterpret_cast<float*>(ws + p.w + p.s + p.x + p.back);
   const int64_t KG = K / G;
   for (int64_t n0 = 0; n0 < N; n0 += p.slice) {
-    const int64_t n = N - n0 < p.slice ? N - n0 : p.slice, units = n * K / 16;
-    hipLaunchKernelGGL((k_unpack_int4<V>), dim3((unsigned)((units + kUThreads - 1) / kUThreads)), dim3(kUThreads), 0, s,
-                       reinterpret_cast<const u32x2*>(codes + n0 * K / 2), scales + n0 * KG,
-                       zeros ? zeros + n0 * KG : nullptr, units, G / 16, (int)KG, p.slice, w, turned);
+    const int64_t n = N - n0 < p.slice ? N - n0 : p.slice;
+    hipLaunchKernelGGL((k_unpack_int4<X>), dim3((unsigned)((n + kUThreads / 64 - 1) / (kUThreads / 64))), dim3(kUThreads), 0,
+                       s, reinterpret_cast<const uint32_t*>(codes + n0 * (K / 2)), scales + n0 * KG,
+                       zeros ? zeros + n0 * KG : nullptr, n, (int)(K / 8), G == 32 ? 2 : G == 64 ? 3 : 4, (int)KG, p.slice,
+                       w, turned);
     for (int64_t m0 = 0; m0 < M; m0 += p.rows) {
       const int64_t m = M - m0 < p.rows ? M - m0 : p.rows;
       const uint16_t* a = reinterpret_cast<const uint16_t*>(x + m0 * K);
