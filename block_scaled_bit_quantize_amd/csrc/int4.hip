@@ -580,7 +580,7 @@ __global__ __launch_bounds__(kUThreads) void k_split_f32(const f32x4* __restrict
 // a step, whose fragments are in registers by then.
 constexpr int kStep = 64, kAhead = 2;
 template <typename X, typename T, int G, int WM, int WN, int MI, int NI, int ST>
-__global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_int4(
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm_int4(
     const uint16_t* __restrict__ a, int64_t plane, const float* __restrict__ back, const uint16_t* __restrict__ w,
     const float* __restrict__ turned, int64_t pitch, const float* __restrict__ bias, int64_t M, int N, int K,
     int64_t pitch_out, int splits, int64_t part, T* __restrict__ out) {
@@ -822,7 +822,8 @@ struct Plan {
   size_t w, s, x, back, parts;  // bytes of the workspace
 };
 
-constexpr int64_t kUnpacked = (int64_t)64 << 20;  // bytes of unpacked weights and of split activations at a time
+constexpr int64_t kUnpacked = (int64_t)128 << 20;  // bytes of unpacked weights at a time
+constexpr int64_t kPlanes = (int64_t)64 << 20;    // bytes of split activations at a time
 constexpr int64_t kParts = (int64_t)128 << 20;    // bytes of slabs' sums at a time
 
 int64_t share_bytes(int64_t M, int64_t K, int64_t group, int64_t size) {
@@ -839,9 +840,14 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int64_t group, int dtype) {
     p.slab = K;
     return p;
   }
-  if (M <= 192) {
+  // A launch of slabs takes up to 64 rows, and reads all weights; the tiles' way
+  // unpacks them first. 4096 x 4096 in bf16: 64 rows 17 and 30 us, 128 rows 35 and
+  // 30 us; 100003 x 4096: 128 rows 320 and 550 us, 256
+  // rows 640 and 600 us. float32: 64 rows 28 and 37 us,
+  // 128 rows 55 and 37 us.
+  const int64_t launches = (M + 63) / 64, few = N * K < (int64_t)1 << 26 ? 1 : dtype == BSQ_F32 ? 2 : 3;
+  if (launches <= few) {
     p.way = Plan::kSlabs;
-    const int64_t launches = (M + 63) / 64;
     p.rows = (M + launches - 1) / launches;
     p.mt = p.rows <= 16 ? 1 : p.rows <= 32 ? 2 : 4;
     // whole loads, kSlabLds of x at most, and as many slabs as give each wave of the card a tile
@@ -864,7 +870,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int64_t group, int dtype) {
   if (whole < p.slice) p.slice = whole;
   // fewer than 2^24 workgroups of 256 work-items
   p.rows = ((int64_t)1 << 22) / (p.slice / 128) * 128;
-  if (dtype == BSQ_F32 && kUnpacked / (4 * K) / 256 * 256 < p.rows) p.rows = kUnpacked / (4 * K) / 256 * 256;
+  if (dtype == BSQ_F32 && kPlanes / (4 * K) / 256 * 256 < p.rows) p.rows = kPlanes / (4 * K) / 256 * 256;
   if (M < p.rows) p.rows = M;
   if (dtype == BSQ_F32) {
     p.x = (size_t)(p.rows * K * 4);
@@ -872,17 +878,26 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int64_t group, int dtype) {
   }
   p.w = (size_t)(p.slice * K * 2);
   p.s = (size_t)(p.slice * (K / group) * 8);
-  const int64_t small = ((p.rows + 127) / 128) * (p.slice / 128), big = ((p.rows + 255) / 256) * (p.slice / 128);
-  if (small * 2 <= cus) {
-    p.tile = 0;
-    const int64_t tiles = ((p.rows + 63) / 64) * (p.slice / 64), most_splits = K / 256;
-    int64_t sp = cus / tiles;
-    if (sp > most_splits) sp = most_splits;
-    if (sp > 8) sp = 8;
-    p.splits = sp < 1 ? 1 : (int)sp;
-  } else {
-    p.tile = dtype == BSQ_F32 ? (small > cus && ((p.rows + 191) / 192) * (p.slice / 128) <= cus ? 2 : 1) : big < cus ? 2 : 3;
-  }
+  // The tile and the parts of K of the least time: rounds of a tile a CU, each of
+  // so many us a step of 64 along K, and the parts' second launch (5 us and its
+  // bytes at 4 TB/s). Measured a step: bf16 128 x 128 0.53 to 0.61, 256 x 128 0.71
+  // to 0.98, 256 x 256 1.45 to 1.8 us; float32 128 x 128 0.98, 192 x 128 1.33, 128 x
+  // 256 1.45 to 1.84 us. 4096 x 4096 in bf16: 256 rows 47, 38, 34 us in 1, 2, 4 parts
+  // of 128 x 128; 1536 rows 80, 65, 109 us by the three tiles; 16384 rows 700, 500, 470.
+  static constexpr struct {
+    int m, n;
+    double us;
+  } kTilesOf[2][3] = {{{128, 128, 0.57}, {256, 128, 0.9}, {256, 256, 1.7}}, {{128, 128, 0.95}, {192, 128, 1.35}, {128, 256, 1.75}}};
+  const int64_t steps = (K + kStep - 1) / kStep;
+  double least = 1e30;
+  for (int t = 0; t < 3; ++t)
+    for (int64_t sp = 1; sp <= 8 && (sp == 1 || steps >= 8 * sp); sp *= 2) {
+      const auto& tile = kTilesOf[dtype == BSQ_F32][t];
+      const int64_t n = ((p.rows + tile.m - 1) / tile.m) * ((p.slice + tile.n - 1) / tile.n) * sp;
+      double us = (double)((n + cus - 1) / cus) * (double)((steps + sp - 1) / sp) * tile.us;
+      if (sp > 1) us += 5.0 + (double)(sp * p.rows * p.slice) * 8.0 / 4e6;
+      if (us < least) least = us, p.tile = t, p.splits = (int)sp;
+    }
   if (p.splits > 1) p.parts = (size_t)(p.splits * p.rows * p.slice * 4);
   return p;
 }
@@ -932,7 +947,7 @@ void launch_tiles(const Plan& p, const uint16_t* a, int64_t plane, const float* 
                      dim3(64 * WM * WN), 0, s, a, plane, back, w, sc, p.slice, bias, M, (int)N, (int)K, pitch_out,    \
                      p.splits, part, out)
   if constexpr (sizeof(X) == 2) {
-    if (p.tile == 0) BSQ_TILE(2, 2, 2, 2, 4);
+    if (p.tile == 0) BSQ_TILE(4, 2, 1, 2, 4);
     else if (p.tile == 1) BSQ_TILE(4, 2, 2, 2, 3);
     else BSQ_TILE(2, 4, 4, 2, 2);
   } else {

@@ -567,7 +567,7 @@ int bsq_linear_int8(const void* x, int dtype, const int8_t* b_codes, const float
  *   float32, and the output is rounded once. A row of x with a NaN or an
  *   infinity gives no finite output; sums of |x| * 15 over a group stay below
  *   2^128. ws bsq_linear_int4_workspace() bytes (0, and ws may be NULL, for
- *   few rows; 256 MiB at most).
+ *   few rows; 320 MiB at most).
  * group <= K <= 32768, K % group == 0, N and M < 2^31. x, w, codes and ws (and
  * bsq_dequantize_int4's out) 16-byte aligned, out and scales to their type,
  * bias 4. Codes of a batch past M, N or K are neither read nor written.
