@@ -219,21 +219,24 @@ __device__ __forceinline__ void split8(f32x4 a, f32x4 b, float f, u32x4& hi, u32
 // ---------------------------------------------------------------- few rows
 // Up to 64 rows of activations, which stay in LDS: bound by reading the weights
 // once. Weights go from memory to registers: a wave keeps kDeep chunks of 16 rows
-// by 128 codes on their way, across tiles of 16 rows.
+// by 256 codes on their way, across tiles of 16 rows. (With chunks of 128 the loads
+// of scales and zero points, a row a lane, kept the address unit as busy as those
+// of the codes: 72 us for 100003 x 4096 and one row.)
 //   SHARE: up to 16 rows of x, whole in LDS. The eight waves of a workgroup share
 //   K, and their partial sums meet in LDS; a workgroup takes tile after tile.
 //   else: more rows, or longer ones. A workgroup has a slab of K of them in LDS,
 //   and each wave tiles of its own; the slabs' sums meet in a second launch.
 //
-// Lane l holds row l % 16's codes [32 p, 32 p + 32) of a chunk, p = l / 16, as
-// one 16-byte load. Matrix instruction i multiplies one word of each lane: 32
-// codes of the chunk. Groups of 128 take them as they lie; for shorter groups
+// Lane l holds row l % 16's codes [32 p, 32 p + 32) of each half of a chunk, p =
+// l / 16, as one 16-byte load. Matrix instruction i of a half multiplies one word
+// of each lane: 32 codes. Groups of 128 take them as they lie; for shorter groups
 // lanes exchange words first, so that the 32 codes are of one group.
 //
 // Zero points: sum (q - z) x = sum q x - z sum x; the second sums are made once
 // for all tiles, by the same instruction with ones.
 constexpr int kFWaves = 8, kFThreads = 64 * kFWaves;
-constexpr int kDeep = 4;
+constexpr int kDeep = 3, kChunk = 256;
+enum { kZeros, kPlain, kRagged };
 constexpr int kFewLds = 163840 - 512, kFewRed = 2 * kFWaves * 1024;  // a CU's LDS but for the rows' largest values
 constexpr int kFewHalf = 81920 - 512;
 constexpr int kSlabLds = 131072;  // of x, but for the rows' 16 bytes more
@@ -241,7 +244,9 @@ constexpr int kSlabLds = 131072;  // of x, but for the rows' 16 bytes more
 // A row of k values of x in LDS: whole loads, and 16 bytes against bank conflicts.
 __host__ __device__ constexpr int64_t few_pitch(int64_t k, int64_t size) { return (k * size + 1023) / 1024 * 1024 + 16; }
 // Sums of x by groups, [group][row].
-__host__ __device__ constexpr int64_t few_table(int64_t k, int64_t group, int mt) { return (k + 127) / 128 * (128 / group) * mt * 64; }
+__host__ __device__ constexpr int64_t few_table(int64_t k, int64_t group, int mt) {
+  return (k + kChunk - 1) / kChunk * (kChunk / group) * mt * 64;
+}
 
 template <int G>
 __device__ __forceinline__ void regroup(u32x4& w) {
@@ -265,27 +270,34 @@ __device__ __forceinline__ int place_of(int p, int i) {
   else return i * 32 + p * 8;
 }
 
+// Of a lane's row: a chunk's codes, and the scales and zero points of its groups,
+// the first lowest. Each is what one load gives: anything done to it on the way
+// would wait for it, and for all loads before it.
+template <int G>
 struct Chunk {
-  u32x4 w;
-  uint32_t s[2], z;  // scales and zero points of its groups, the first lowest
+  static constexpr int groups = kChunk / G;
+  u32x4 w[2];
+  uint32_t s[groups / 2], z[groups > 4 ? groups / 4 : 1];
 };
 
-// BYTES of LDS: half of a CU's where that does, for two workgroups a CU. slab:
-// values of K of a workgroup. Outputs, or (parts given) a slab's sums, [slab][M][N].
-template <typename X, typename T, int G, int MT, bool SHARE, int BYTES>
+// KIND: K of whole chunks with zero points, without, or neither. BYTES of LDS: half of a CU's where that does, for
+// two workgroups a CU. slab: values of K of a workgroup. Outputs, or (parts given) a slab's sums, [slab][M][N].
+template <typename X, int G, int MT, bool SHARE, int KIND, int BYTES>
 __global__ __launch_bounds__(kFThreads) void k_linear_int4_few(const X* __restrict__ x, const uint8_t* __restrict__ codes,
                                                               const uint16_t* __restrict__ scales,
                                                               const uint8_t* __restrict__ zeros,
                                                               const float* __restrict__ bias, int M, int64_t N, int K,
                                                               int slab, float* __restrict__ parts, int64_t pitch_out,
-                                                              T* __restrict__ out) {
-  constexpr int P = Mfma<X>::parts, GP = 128 / G;  // groups of a chunk
+                                                              void* __restrict__ out, int out_f32) {
+  constexpr bool RAGGED = KIND == kRagged;
+  const bool ZEROS = KIND == kZeros || (RAGGED && zeros);
+  constexpr int P = Mfma<X>::parts, GP = 128 / G, GC = 2 * GP;  // groups of half a chunk, of a chunk
   __shared__ __attribute__((aligned(16))) uint8_t lds[BYTES];
   __shared__ uint32_t rmax[P > 1 ? 16 * MT : 1];
   f32x4* red = reinterpret_cast<f32x4*>(lds);  // SHARE: [2][waves][64]
   const int t = threadIdx.x, wave = uniform(t >> 6), lane = t & 63, col = lane & 15, p = lane >> 4;
   const int k0 = SHARE ? 0 : (int)blockIdx.y * slab, k_end = K - k0 < slab ? K : k0 + slab;  // this workgroup's K
-  const int chunks = (k_end - k0 + 127) / 128, pitch = (int)few_pitch(slab, sizeof(X));
+  const int chunks = (k_end - k0 + kChunk - 1) / kChunk, pitch = (int)few_pitch(slab, sizeof(X));
   f32x4* table = reinterpret_cast<f32x4*>(lds + (SHARE ? kFewRed : 0));
   uint8_t* xs = lds + (SHARE ? kFewRed : 0) + few_table(slab, G, MT);
   {
@@ -306,53 +318,52 @@ __global__ __launch_bounds__(kFThreads) void k_linear_int4_few(const X* __restri
   const int KG = K / G;
   const int c0 = SHARE ? chunks * wave / kFWaves : 0;  // this wave's chunks
   const int nc = SHARE ? chunks * (wave + 1) / kFWaves - c0 : chunks;
+  const int64_t total = tile0 < tiles ? ((tiles - 1 - tile0) / stride + 1) * nc : 0;  // chunks of this wave
   int64_t ft = tile0;  // the tile and the chunk that are asked for next
   int fc = 0;
-  const uint8_t* at_w;
-  const uint16_t* at_s;
-  const uint8_t* at_z;
-  auto aim = [&] {  // this lane's row of the tile
-    int64_t n = ft * 16 + col;
+  auto fetch = [&](Chunk<G>& f) {
+    int64_t n = ft * 16 + col;  // this lane's row
     if (n >= N) n = N - 1;
-    at_w = codes + n * (K / 2) + k0 / 2 + c0 * 64 + p * 16;
-    at_s = scales + n * KG + k0 / G + c0 * GP;
-    at_z = zeros ? zeros + n * KG + k0 / G + c0 * GP : nullptr;
-  };
-  auto fetch = [&](Chunk& f) {
-    const int k = k0 + (c0 + fc) * 128;
-    if (k + p * 32 < K) f.w = *reinterpret_cast<const u32x4*>(at_w + fc * 64);
-    else f.w = (u32x4){0, 0, 0, 0};
-    f.s[0] = f.s[1] = 0;
-    f.z = 0x08080808u;
-    const int g = fc * GP;
-    if (GP == 1 || k + 128 <= K) {
-      __builtin_memcpy(f.s, at_s + g, 2 * GP);
-      if (zeros) __builtin_memcpy(&f.z, at_z + g, GP);
-    } else {  // the last groups of a row
+    const int k = k0 + (c0 + fc) * kChunk;
+    const uint8_t* at_w = codes + n * (K / 2) + k / 2 + p * 16;
+    const int64_t g = n * KG + k / G;
+    if constexpr (!RAGGED) {
+      f.w[0] = *reinterpret_cast<const u32x4*>(at_w);
+      f.w[1] = *reinterpret_cast<const u32x4*>(at_w + 64);
+      __builtin_memcpy(f.s, scales + g, 2 * GC);
+      if constexpr (KIND == kZeros) {
+        if constexpr (GC == 2) {
+          uint16_t z;
+          __builtin_memcpy(&z, zeros + g, 2);
+          f.z[0] = z;
+        } else {
+          __builtin_memcpy(f.z, zeros + g, GC);
+        }
+      }
+    } else {  // the last chunk of a row may be a part of one
+      f = Chunk<G>{};
 #pragma unroll
-      for (int j = 0; j < GP; ++j)
+      for (int h = 0; h < 2; ++h)
+        if (k + h * 128 + p * 32 < K) f.w[h] = *reinterpret_cast<const u32x4*>(at_w + h * 64);
+#pragma unroll
+      for (int j = 0; j < GC; ++j)
         if (k + j * G < K) {
-          f.s[j / 2] |= (uint32_t)at_s[g + j] << (16 * (j & 1));
-          if (zeros) f.z = (f.z & ~(0xFFu << (8 * j))) | (uint32_t)at_z[g + j] << (8 * j);
+          f.s[j / 2] |= (uint32_t)scales[g + j] << (16 * (j & 1));
+          if (ZEROS) f.z[j / 4] |= (uint32_t)zeros[g + j] << (8 * (j & 3));
         }
     }
-    if (++fc == nc) {
-      fc = 0;
-      ft += stride;
-      if (ft < tiles) aim();
-    }
+    const bool end = ++fc == nc;
+    fc = end ? 0 : fc;
+    ft = end ? ft + stride : ft;
   };
-  Chunk ring[kDeep];
-  if (nc && ft < tiles) {
-    aim();
+  Chunk<G> ring[kDeep];
 #pragma unroll
-    for (int d = 0; d < kDeep; ++d)
-      if (ft < tiles) fetch(ring[d]);
-  }
+  for (int d = 0; d < kDeep; ++d)
+    if (d < total) fetch(ring[d]);
   wait_loads<0>();
   __syncthreads();
-  if ((k_end - k0) % 128) {  // past the end of K anything may lie there
-    const int from = (k_end - k0) * (int)sizeof(X), per = (chunks * 128 * (int)sizeof(X) - from) / 16;
+  if ((k_end - k0) % kChunk) {  // past the end of K anything may lie there
+    const int from = (k_end - k0) * (int)sizeof(X), per = (chunks * kChunk * (int)sizeof(X) - from) / 16;
     for (int u = t; u < M * per; u += kFThreads)
       *reinterpret_cast<u32x4*>(xs + u / per * pitch + from + u % per * 16) = (u32x4){0, 0, 0, 0};
     if constexpr (P == 1) __syncthreads();  // else those of the parts
@@ -390,7 +401,7 @@ __global__ __launch_bounds__(kFThreads) void k_linear_int4_few(const X* __restri
   auto load_x = [&](int m, int k, int part) {
     return *reinterpret_cast<const u32x4*>(my_x[m] + k * (int)sizeof(X) + part * 16);
   };
-  for (int c = wave; c < chunks; c += kFWaves) {
+  for (int c = wave; c < 2 * chunks; c += kFWaves) {  // halves
     const u32x4 ones = {Mfma<X>::ones, Mfma<X>::ones, Mfma<X>::ones, Mfma<X>::ones};
 #pragma unroll
     for (int j = 0; j < GP; ++j)
@@ -407,37 +418,47 @@ __global__ __launch_bounds__(kFThreads) void k_linear_int4_few(const X* __restri
   }
   __syncthreads();
   f32x4 acc[MT] = {};
-  auto multiply = [&](Chunk f, int c) {
-    regroup<G>(f.w);
+  auto multiply = [&](Chunk<G>& f, int c) {
 #pragma unroll
-    for (int j = 0; j < GP; ++j) {
-      f32x4 sum[MT] = {};
+    for (int h = 0; h < 2; ++h) {
+      regroup<G>(f.w[h]);
 #pragma unroll
-      for (int i = j * (4 / GP); i < (j + 1) * (4 / GP); ++i) {
-        const int k = c * 128 + place_of<G>(p, i);
-        const u32x4 b = codes_of<X>(f.w[i]);
+      for (int jj = 0; jj < GP; ++jj) {
+        const int j = h * GP + jj;  // group of the chunk
+        f32x4 sum[MT] = {};
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int i = jj * (4 / GP); i < (jj + 1) * (4 / GP); ++i) {
+          const int k = c * kChunk + h * 128 + place_of<G>(p, i);
+          const u32x4 b = codes_of<X>(f.w[h][i]);
 #pragma unroll
-          for (int part = 0; part < P; ++part) sum[m] = Mfma<X>::mul16(load_x(m, k, part), b, sum[m]);
-      }
-      const float s = __uint_as_float(j & 1 ? f.s[j / 2] & 0xFFFF0000u : f.s[j / 2] << 16);
-      const float z = (float)(f.z >> (8 * j) & 0xFFu);
+          for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const f32x4 of_x = table[(c * GP + j) * MT * 4 + m * 4 + p];
+            for (int part = 0; part < P; ++part) sum[m] = Mfma<X>::mul16(load_x(m, k, part), b, sum[m]);
+        }
+        const float s = __uint_as_float(j & 1 ? f.s[j / 2] & 0xFFFF0000u : f.s[j / 2] << 16);
+        const float z = ZEROS ? (float)(f.z[j / 4] >> (8 * (j & 3)) & 0xFFu) : 8.0f;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[m][r] = __builtin_fmaf(s, __builtin_fmaf(-z, of_x[r], sum[m][r]), acc[m][r]);
+        for (int m = 0; m < MT; ++m) {
+          const f32x4 of_x = table[(c * GC + j) * MT * 4 + m * 4 + p];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[m][r] = __builtin_fmaf(s, __builtin_fmaf(-z, of_x[r], sum[m][r]), acc[m][r]);
+        }
       }
     }
   };
+  // the bias of a tile's weight row, asked for a tile ahead
+  auto bias_of = [&](int64_t tile) {
+    const int64_t n = tile * 16 + (SHARE ? t >> 2 & 15 : col);
+    return bias ? bias[n < N ? n : N - 1] : 0.0f;
+  };
+  float add = bias_of(tile0 < tiles ? tile0 : 0);
   auto store = [&](int m, int64_t n, float y) {  // row m's sum for weight row n
     if constexpr (P > 1) y *= of_exponent(254u - row_factor(rmax[m]));
     if (!SHARE && parts) {
       parts[((int64_t)blockIdx.y * M + m) * N + n] = y;
     } else {
-      if (bias) y += bias[n];
-      store1(out + m * pitch_out + n, y);
+      if (out_f32) store1(static_cast<float*>(out) + m * pitch_out + n, y + add);
+      else store1(static_cast<uint16_t*>(out) + m * pitch_out + n, y + add);
     }
   };
   int buf = 0;
@@ -467,28 +488,42 @@ __global__ __launch_bounds__(kFThreads) void k_linear_int4_few(const X* __restri
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[m] = (f32x4){0, 0, 0, 0};
+    add = bias_of(tile + stride < tiles ? tile + stride : tile);
   };
   if (nc == 0) {
     if constexpr (SHARE)
       for (int64_t tile = tile0; tile < tiles; tile += stride) finish(tile);
     return;
   }
-  int64_t tile = tile0;
+  int64_t tile = tile0, it = 0;
   int c = 0;
-  while (tile < tiles) {
+  auto step = [&](Chunk<G>& f) {
+    multiply(f, c0 + c);
+    ++it;
+    if (++c == nc) {
+      finish(tile);
+      c = 0;
+      tile += stride;
+    }
+  };
+  // Whole rounds of the ring, with no branch around a load: behind one the compiler would not know how many are on
+  // their way, and wait for nearly all.
+  while (it + 2 * kDeep <= total) {
 #pragma unroll
     for (int d = 0; d < kDeep; ++d) {
-      if (tile < tiles) {
-        multiply(ring[d], c0 + c);
-        if (ft < tiles) fetch(ring[d]);
-        if (++c == nc) {
-          finish(tile);
-          c = 0;
-          tile += stride;
-        }
-      }
+      step(ring[d]);
+      fetch(ring[d]);
     }
   }
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      if (it >= total) return;
+      const bool more = it + kDeep < total;
+      step(ring[d]);
+      if (r == 0 && more) fetch(ring[d]);
+    }
 }
 
 // ---------------------------------------------------------------- many rows
@@ -902,34 +937,34 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int64_t group, int dtype) {
   return p;
 }
 
-template <typename X, typename T, int G>
+template <typename X, int G, int KIND>
 void launch_share(const X* x, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, const float* bias,
-                  int64_t M, int64_t N, int64_t K, T* out, hipStream_t s) {
+                  int64_t M, int64_t N, int64_t K, void* out, int out_f32, hipStream_t s) {
   const int64_t tiles = (N + 15) / 16;
   const bool half = share_bytes(M, K, G, sizeof(X)) <= kFewHalf;
   const int64_t most = bsqh::device_cus() * (half ? 2 : 1);
   const dim3 grid((unsigned)(tiles < most ? tiles : most));
 #define BSQ_FEW(BYTES)                                                                                                 \
-  hipLaunchKernelGGL((k_linear_int4_few<X, T, G, 1, true, BYTES>), grid, dim3(kFThreads), 0, s, x, codes, scales, zeros, \
-                     bias, (int)M, N, (int)K, (int)K, nullptr, N, out)
+  hipLaunchKernelGGL((k_linear_int4_few<X, G, 1, true, KIND, BYTES>), grid, dim3(kFThreads), 0, s, x, codes, scales, zeros, \
+                     bias, (int)M, N, (int)K, (int)K, nullptr, N, out, out_f32)
   if (half) BSQ_FEW(kFewHalf);
   else BSQ_FEW(kFewLds);
 #undef BSQ_FEW
 }
 
 // The slabs' sums go to `parts` where there are several.
-template <typename X, typename T, int G>
+template <typename X, int G, int KIND>
 void launch_slabs(const Plan& p, const X* x, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros,
-                  const float* bias, int64_t M, int64_t N, int64_t K, float* parts, int64_t pitch_out, T* out,
-                  hipStream_t s) {
+                  const float* bias, int64_t M, int64_t N, int64_t K, float* parts, int64_t pitch_out, void* out,
+                  int out_f32, hipStream_t s) {
   const int64_t tiles = (N + 15) / 16, groups = (tiles + kFWaves - 1) / kFWaves;
   int64_t most = bsqh::device_cus() / p.splits;  // workgroups of a slab
   if (most < 1) most = 1;
   const dim3 grid((unsigned)(groups < most ? groups : most), (unsigned)p.splits);
 #define BSQ_FEW(MT)                                                                                             \
-  hipLaunchKernelGGL((k_linear_int4_few<X, T, G, MT, false, kSlabLds + 256 * MT + 8192>), grid, dim3(kFThreads), 0, s, \
+  hipLaunchKernelGGL((k_linear_int4_few<X, G, MT, false, KIND, kSlabLds + 256 * MT + 8192>), grid, dim3(kFThreads), 0, s, \
                      x, codes, scales, zeros, bias, (int)M, N, (int)K, (int)p.slab, p.splits > 1 ? parts : nullptr,   \
-                     pitch_out, out)
+                     pitch_out, out, out_f32)
   if (p.mt == 1) BSQ_FEW(1);
   else if (p.mt == 2) BSQ_FEW(2);
   else BSQ_FEW(4);
@@ -968,7 +1003,8 @@ int run_linear(const X* x, const uint8_t* codes, const uint16_t* scales, const u
                        parts, p.splits, part, m, n, add, N, to);
   };
   if (p.way == Plan::kShare) {
-    launch_share<X, T, G>(x, codes, scales, zeros, bias, M, N, K, out, s);
+    const auto launch = K % kChunk ? launch_share<X, G, kRagged> : zeros ? launch_share<X, G, kZeros> : launch_share<X, G, kPlain>;
+    launch(x, codes, scales, zeros, bias, M, N, K, out, sizeof(T) == 4, s);
     return bsqh::launch_status();
   }
   if (p.way == Plan::kSlabs) {
@@ -979,8 +1015,9 @@ int run_linear(const X* x, const uint8_t* codes, const uint16_t* scales, const u
       for (int64_t m0 = 0; m0 < M; m0 += p.rows) {
         const int64_t m = M - m0 < p.rows ? M - m0 : p.rows;
         T* to = out + m0 * N + n0;
-        launch_slabs<X, T, G>(p, x + m0 * K, codes + n0 * (K / 2), scales + g0, zeros ? zeros + g0 : nullptr, add, m, n, K,
-                              parts, N, to, s);
+        const auto launch = K % kChunk ? launch_slabs<X, G, kRagged> : zeros ? launch_slabs<X, G, kZeros> : launch_slabs<X, G, kPlain>;
+        launch(p, x + m0 * K, codes + n0 * (K / 2), scales + g0, zeros ? zeros + g0 : nullptr, add, m, n, K, parts, N, to,
+               sizeof(T) == 4, s);
         if (p.splits > 1) join(parts, m, n, add, to);
       }
     }
