@@ -10,7 +10,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libbsq.so")
 SOURCES = ["quantize.hip", "transpose_quant.hip", "route.hip", "gemm.hip", "gemm_inreg.hip", "codec.hip", "probe.hip",
            "moe_gate.hip", "moe_group_gate.hip", "moe_few.hip", "int8.hip",
-           "int4.hip", "logprob.hip"]
+           "int4.hip", "int4_few.hip", "logprob.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
