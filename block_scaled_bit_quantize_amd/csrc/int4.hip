@@ -164,10 +164,15 @@ __global__ __launch_bounds__(kUThreads) void k_unpack_int4(const uint32_t* __res
     const uint32_t c = codes[row * units + u];
     const int64_t g = row * KG + (u >> shift);
     const float z = zeros ? (float)zeros[g] : 8.0f, own = from_bf16(scales[g]), s = raised(own);
-    const float f = s == own ? 1.0f : own / s;  // NaN: f is NaN, and the values
     typename Mfma<X>::V v;
+    if (s == own) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = Mfma<X>::near(((float)(c >> (4 * j) & 15u) - z) * f);
+      for (int j = 0; j < 8; ++j) v[j] = Mfma<X>::near((float)(c >> (4 * j) & 15u) - z);
+    } else {  // raised, or NaN: so are the values
+      const float f = own / s;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = Mfma<X>::near(((float)(c >> (4 * j) & 15u) - z) * f);
+    }
     w[row * units + u] = __builtin_bit_cast(u32x4, v);
   }
 }

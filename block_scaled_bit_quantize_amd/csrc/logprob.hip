@@ -15,9 +15,9 @@
 // Alternatives: the pass also leaves the maximum of every block of 64
 // neighbours. Ordered by value, then by lower index, the k best elements lie
 // in the k best blocks (each block ahead of an element's own holds an element
-// ahead of it), and the same holds for groups of blocks. So the second launch
-// ranks groups, blocks of the best groups, eighths of the best blocks and their
-// elements, each rank by counting the larger ones among a few hundred.
+// ahead of it), and the same holds for any groups of blocks or elements. So the
+// second launch ranks groups, keeps the best ones' members, and so on to blocks,
+// then in the same way to elements, each rank by counting the larger ones.
 #include <math.h>
 
 #include "bsq_device.h"
@@ -217,26 +217,36 @@ __global__ __launch_bounds__(kThreads) void k_token_stats(const T* __restrict__ 
   }
 }
 
-// The alternatives' kernel: 1024 threads a row, four to a key.
+// The alternatives' kernel: 1024 threads a row, eight to a key. A ranking of n
+// keys is n^2 comparisons, so that lists of more than 128 are narrowed by groups
+// first (rankings of up to 512 made it 13 us for one row of 100003, top 20).
 constexpr int kJThreads = 1024, kJWaves = kJThreads / 64;
-constexpr int kMost = 512;  // keys that are ranked at a time
+constexpr int kMost = 128;          // keys that are ranked at a time
 constexpr int kLarge = 1 << 20, kSmall = 1 << 18;  // vocabularies
 constexpr int blocks_of(int V) { return V / kBlock + 1; }  // at most: the row may begin within a block
+// groups of a row's blocks, so that the best ones' blocks fit the list
+constexpr int first_of(int V) { return V > kSmall ? 512 : kMost; }
 
-// keys[0, n) are distinct but for zeros, n <= kMost. Each key's rank is the
-// number of larger ones, of which its four threads count a quarter each; `take`
-// gets (index, rank) of those that are not zero and among the `top` first, in
-// each of the four threads.
+template <int CTRL>
+__device__ __forceinline__ u64 dpp(u64 v) {
+  return (u64)(uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, 0xF, 0xF, false) << 32 |
+         (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, 0xF, 0xF, false);
+}
+
+// keys[0, n) are distinct but for zeros. Each key's rank is the number of larger
+// ones, of which its eight threads count an eighth each; `take` gets (index,
+// rank) of those that are not zero and among the `top` first, in each of them.
 template <typename Take>
 __device__ __forceinline__ void ranks(const u64* keys, int n, int top, Take take) {
   const int t = threadIdx.x;
-  for (int i = t >> 2; i < n; i += kJThreads / 4) {
+  for (int i = t >> 3; i < n; i += kJThreads / 8) {
     const u64 mine = keys[i];
     int rank = 0;
 #pragma unroll 8
-    for (int j = t & 3; j < n; j += 4) rank += keys[j] > mine;
+    for (int j = t & 7; j < n; j += 8) rank += keys[j] > mine;
     rank += __builtin_amdgcn_update_dpp(0, rank, 0xB1, 0xF, 0xF, false);
     rank += __builtin_amdgcn_update_dpp(0, rank, 0x4E, 0xF, 0xF, false);
+    rank += __builtin_amdgcn_update_dpp(0, rank, 0x141, 0xF, 0xF, false);
     if (mine && rank < top) take(i, rank);
   }
 }
@@ -246,30 +256,49 @@ __device__ __forceinline__ void best_of(const u64* keys, int n, int top, u64* be
   if (t < top) best[t] = 0ull;
   __syncthreads();
   ranks(keys, n, top, [&](int i, int rank) {
-    if ((t & 3) == 0) best[rank] = keys[i];
+    if ((t & 7) == 0) best[rank] = keys[i];
   });
   __syncthreads();
 }
-// Groups of `size` of n items, key(i) distinct but for zeros, at most kMost
-// groups: the items of the best `top` groups to out[0, top * size).
+// Groups of `size` of n items, key(i) distinct but for zeros: the items of the
+// best `top` groups to out[0, top * size).
 template <typename Key>
 __device__ __forceinline__ void narrow(Key key, int n, int size, int top, u64* most, u64* out) {
   const int t = threadIdx.x, groups = (n + size - 1) / size;
-  for (int g = t; g < groups; g += kJThreads) {
+  for (int g = t >> 3; g < groups; g += kJThreads / 8) {
     u64 m = 0;
-    for (int i = g * size; i < (g + 1) * size && i < n; ++i) {
+    for (int i = g * size + (t & 7); i < (g + 1) * size && i < n; i += 8) {
       const u64 k = key(i);
       m = k > m ? k : m;
     }
-    most[g] = m;
+    u64 o = dpp<0xB1>(m);
+    m = o > m ? o : m;
+    o = dpp<0x4E>(m);
+    m = o > m ? o : m;
+    o = dpp<0x141>(m);
+    m = o > m ? o : m;
+    if ((t & 7) == 0) most[g] = m;
   }
   for (int i = t; i < top * size; i += kJThreads) out[i] = 0ull;
   __syncthreads();
   ranks(most, groups, top, [&](int g, int rank) {
-    for (int i = t & 3; i < size; i += 4)
+    for (int i = t & 7; i < size; i += 8)
       if (g * size + i < n) out[rank * size + i] = key(g * size + i);
   });
   __syncthreads();
+}
+// The same of a list, until few enough are left: list[0, n) and `other` are overwritten.
+__device__ __forceinline__ void best_of_list(u64* list, u64* other, int n, int top, u64* most, u64* best) {
+  while (n > kMost) {  // ends: 64 ceil(n / 128) < n
+    const int size = (n + kMost - 1) / kMost;
+    const u64* from = list;
+    narrow([&](int i) { return from[i]; }, n, size, top, most, other);
+    n = top * size;
+    u64* was = list;
+    list = other;
+    other = was;
+  }
+  best_of(list, n, top, best);
 }
 
 // A workgroup a row: the parts' sums, then the alternatives. MAXV: the largest
@@ -281,15 +310,17 @@ __global__ __launch_bounds__(kJThreads) void k_token_join(const T* __restrict__ 
                                                          Out out) {
   constexpr int E = Row<T>::E, PB = kBlock / E;  // elements of a piece, pieces of a block
   constexpr int kBlocks = blocks_of(MAXV);
-  constexpr int kList = kMaxTop * ((kBlocks + kMost - 1) / kMost);  // blocks of the best groups
-  constexpr int kElements = kMaxTop * kBlock;                      // of the best blocks
-  static_assert((kList + kMost - 1) / kMost * kMaxTop <= kMost && kElements / 8 <= kMost, "two steps at most");
+  constexpr int kFirst = first_of(MAXV);
+  constexpr int kList = kMaxTop * ((kBlocks + kFirst - 1) / kFirst);  // blocks of the best groups
+  constexpr int kElements = kMaxTop * kBlock;                        // of the best blocks
+  constexpr int kOther = kMaxTop * ((kList + kMost - 1) / kMost);    // what a list narrows to
+  static_assert(kMaxTop * ((kElements + kMost - 1) / kMost) <= kList, "the elements of the best groups fit the list");
   __shared__ Sums lds[kJWaves];
   __shared__ union {
     uint32_t maxima[kBlocks];
     u64 element[kElements];
   } a_;
-  __shared__ u64 list[kList > kMost ? kList : kMost], most[kMost], few[kMost], best[kMaxTop];
+  __shared__ u64 list[kList], other[kOther], most[kFirst], best[kMaxTop];
   const int t = threadIdx.x;
   const int64_t row = row0 + blockIdx.x;
   const Row<T> r(x, row, V);
@@ -303,17 +334,10 @@ __global__ __launch_bounds__(kJThreads) void k_token_join(const T* __restrict__ 
   a = joined(a, lds, kJWaves);  // its barrier is the maxima's, too
   if (t == 0) finish(x, targets, row, V, a, out);
   if (top == 0) return;
-  const int size = (blocks + kMost - 1) / kMost;
-  int n = top * size;
+  const int size = (blocks + kFirst - 1) / kFirst;
   narrow([&](int b) { return ranked(a_.maxima[b], (uint32_t)b); }, blocks, size, top, most, list);
-  if (n <= kMost) {
-    best_of(list, n, top, best);
-  } else {
-    const int again = (n + kMost - 1) / kMost;
-    narrow([&](int i) { return list[i]; }, n, again, top, most, few);
-    best_of(few, top * again, top, best);
-  }
-  // the elements of the best blocks, then those of their best eighths
+  best_of_list(list, other, top * size, top, most, best);
+  // the elements of the best blocks
   for (int i = t; i < top * PB; i += kJThreads) {
     const u64 g = best[i / PB];
     const int p = (int)(uint32_t)~(uint32_t)g * PB + i % PB;
@@ -325,8 +349,9 @@ __global__ __launch_bounds__(kJThreads) void k_token_join(const T* __restrict__ 
     for (int e = 0; e < E; ++e) a_.element[i * E + e] = ranked(key_of(v[e]), (uint32_t)(p * E + e));
   }
   __syncthreads();
-  narrow([&](int i) { return a_.element[i]; }, top * kBlock, 8, top, most, few);
-  best_of(few, top * 8, top, best);
+  const int of = (top * kBlock + kMost - 1) / kMost;
+  narrow([&](int i) { return a_.element[i]; }, top * kBlock, of, top, most, list);
+  best_of_list(list, other, top * of, top, most, best);
   if (t < top) {
     const bool none = !(a.m > -kInf) && a.s == 0.0f;
     const u64 k = best[t];

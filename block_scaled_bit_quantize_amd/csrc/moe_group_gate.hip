@@ -45,6 +45,7 @@ constexpr float kInf = __builtin_inff();
 struct Choice {
   int E, k, groups, size, group_k, group_top;  // groups 1: no restriction
   int lanes;                                   // lanes that share a group, 0: through LDS
+  int over_size;                               // e / size = e * over_size >> 20, for e < 1024 and size <= 512
   bool softmax, renorm;
   float scale;
 };
@@ -347,6 +348,7 @@ __global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ l
       wave_fence();
       for (int q = sub; q < c.groups; q += L) {
         Top o = {-kInf, -kInf, most};
+#pragma unroll 4
         for (int e = q * c.size; e < (q + 1) * c.size; ++e) {
           const float v = lds.key[mine][e];
           o.b = fmaxf(o.b, fminf(o.a, v));
@@ -373,7 +375,7 @@ __global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ l
 #pragma unroll
       for (int o = 1; o < L; o *= 2) kept |= __shfl_xor((unsigned long long)kept, o, 64);
 #pragma unroll
-      for (int i = 0; i < V; ++i) b[i] = e0 + i < c.E && (kept >> ((e0 + i) / c.size) & 1) ? b[i] : -kInf;
+      for (int i = 0; i < V; ++i) b[i] = e0 + i < c.E && (kept >> ((e0 + i) * c.over_size >> 20) & 1) ? b[i] : -kInf;
     }
   }
   double key[V];
@@ -731,6 +733,7 @@ extern "C" int bsq_moe_gate_grouped(const void* logits, int dtype, const float* 
   hipStream_t s = bsqh::as_stream(stream);
   // all groups kept: no choice of groups
   const Choice c = {(int)E, (int)k, group_k == groups ? 1 : (int)groups, (int)(E / groups), (int)group_k, group_top, 0,
+                    (int)(((1 << 20) + E / groups - 1) / (E / groups)),
                     score == BSQ_SCORE_SOFTMAX, renormalize == 1, scale};
   if (dtype == BSQ_F32) {
     BSQ_GROUP_SHAPES(launch_gate, float, static_cast<const float*>(logits), bias, tokens, c, weights, topk_ids, s);
@@ -751,7 +754,7 @@ extern "C" int bsq_moe_gate_grouped_backward(const float* dweights, const float*
                   (((uintptr_t)weights | (uintptr_t)dweights | (uintptr_t)topk_ids) & 3) == 0,
               BSQ_E_ALIGN);
   hipStream_t s = bsqh::as_stream(stream);
-  const Choice c = {(int)E, (int)k, 1, (int)E, 1, 1, 0, score == BSQ_SCORE_SOFTMAX, renormalize == 1, scale};
+  const Choice c = {(int)E, (int)k, 1, (int)E, 1, 1, 0, 0, score == BSQ_SCORE_SOFTMAX, renormalize == 1, scale};
   if (dtype == BSQ_F32) {
     BSQ_GATE_SHAPES(launch_back, float, dweights, weights, topk_ids, static_cast<const float*>(logits), tokens, c,
                     static_cast<float*>(dlogits), s);

@@ -1,5 +1,7 @@
 """PyTorch-facing wrappers of the bsq_* entry points (argument marshalling
 only: shapes, output allocation, device pointers, the current stream)."""
+import functools
+
 import torch
 
 from ._lib import BsqError, check, load_library
@@ -42,6 +44,15 @@ def _dev(*ts):
 
 def _ws(nbytes, device):
     return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
+
+
+@functools.lru_cache(maxsize=4096)
+def _ws_bytes(name, index, *sizes):
+    """A workspace query's answer for these sizes on device `index` (a decode loop asks the same again and again)."""
+    if _raw_device is not None and _raw_device() == index:
+        return getattr(load_library(), name)(*sizes)
+    with torch.cuda.device(index):
+        return getattr(load_library(), name)(*sizes)
 
 
 def _run(name, first, others, *args):
@@ -639,7 +650,6 @@ def linear_int4(x, codes, scales, zeros=None, bias=None, out_dtype=None):
     bfloat16) and weights in 4-bit groups as quantize_int4 returns them; bias
     float32 [N] or None; out_dtype is x's unless given. One token or few: bound
     by reading the codes once."""
-    lib = load_library()
     _dev(x, codes, scales, zeros, bias)
     _need(x.dim() == 2, "linear_int4: x must be [M, K]")
     dt = _dtype(x, "x")
@@ -650,7 +660,7 @@ def linear_int4(x, codes, scales, zeros=None, bias=None, out_dtype=None):
     _need(bias is None or (bias.dtype == torch.float32 and bias.numel() == N), "linear_int4: bias must be float32 [N]")
     _need(out_dtype in _OUT, "out_dtype must be float32 or bfloat16")
     out = torch.empty((M, N), dtype=out_dtype, device=x.device)
-    wsb = lib.bsq_linear_int4_workspace(M, N, K, group, dt)
+    wsb = _ws_bytes("bsq_linear_int4_workspace", x.get_device(), M, N, K, group, dt)
     ws = _ws(wsb, x.device) if wsb else None
     _run("bsq_linear_int4", x, (codes, scales, zeros, bias), x.data_ptr(), dt, codes.data_ptr(), scales.data_ptr(),
          _ptr(zeros), group, _ptr(bias), M, N, K, out.data_ptr(), _OUT[out_dtype], _ptr(ws), wsb)
@@ -665,7 +675,6 @@ def token_logprobs(logits, targets, top=0):
     largest alternatives, ties to the lowest index, id -1 where no unmasked
     logit is left. stats (the row's maximum and log sum e^(x - maximum), which
     add up to the log-sum-exp) is for token_logprobs_backward, the gradient."""
-    lib = load_library()
     _dev(logits, targets)
     _need(logits.dim() == 2, "token_logprobs: logits must be [tokens, vocabulary]")
     T, V = logits.shape
@@ -676,7 +685,7 @@ def token_logprobs(logits, targets, top=0):
     logprobs, entropy, stats = f32(T), f32(T), f32(T, 2)
     top_lp = f32(T, top) if top else None
     top_ids = torch.empty((T, top), dtype=torch.int32, device=logits.device) if top else None
-    wsb = lib.bsq_token_logprobs_workspace(T, V, top, dt)
+    wsb = _ws_bytes("bsq_token_logprobs_workspace", logits.get_device(), T, V, top, dt)
     ws = _ws(wsb, logits.device) if wsb else None
     _run("bsq_token_logprobs", logits, (targets,), logits.data_ptr(), dt, targets.data_ptr(), T, V, top,
          logprobs.data_ptr(), entropy.data_ptr(), stats.data_ptr(), _ptr(top_lp), _ptr(top_ids), _ptr(ws), wsb)
