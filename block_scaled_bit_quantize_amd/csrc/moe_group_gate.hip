@@ -148,6 +148,12 @@ __device__ __forceinline__ void worth(const Top& t, int group_top, bool softmax,
   }
   const bool two = group_top == 2 && t.b > -kInf;
   const float w = two ? t.a + t.b : t.a;
+  constexpr float kBig = __FLT_MAX__ * (1.0f - 0x1p-20f);
+  if (!(fabsf(w) <= kBig)) {  // an infinite bias, or a sum past float32
+    low = w > 0.0f ? kBig : -kInf;
+    high = w > 0.0f ? kInf : -kBig;
+    return;
+  }
   float tol = key_bound(t.s, t.a, softmax);
   if (two) tol += key_bound(t.s, t.b, softmax) + fabsf(w) * 0x1p-23f;
   low = w - tol;
@@ -292,7 +298,10 @@ __global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ l
     for (int i = 0; i < V; ++i) s[i] = sigmoid32(x[i]);
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i) b[i] = x[i] > -kInf ? s[i] + b[i] : -kInf;  // the key; NaN is masked below
+  for (int i = 0; i < V; ++i) {  // the key
+    const float v = s[i] + b[i];
+    b[i] = x[i] > -kInf && v > -kInf ? v : -kInf;  // no NaN, of a logit or a bias
+  }
   bool unsure = false;
   if (c.groups > 1) {
     Top g = {-kInf, -kInf, 0.0f};
@@ -493,7 +502,8 @@ __global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ l
       kd[q] = -(double)kInf;
       if (ri[q] >= 0) {
         look(ri[q], rx[q], rb[q], ls, lc, lt);
-        kd[q] = key64(rx[q], rb[q], c.softmax, m, total);
+        // NaN where a softmax row holds +inf: above the empty places, so that ranks are distinct there too
+        kd[q] = fmax(key64(rx[q], rb[q], c.softmax, m, total), -__DBL_MAX__);
       }
       const float vc = __shfl(lc, first + (c.k - 1) % L, 64), vt = __shfl(lt, first + (c.k - 1) % L, 64);
       if (q == (c.k - 1) / L) cut = vc, cut_tol = vt;

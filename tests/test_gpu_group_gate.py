@@ -102,6 +102,63 @@ def test_special_rows(E, groups, score):
     check(rows, 4, F32, bias, groups, max(1, groups // 2), 1, score, True)
 
 
+@pytest.mark.parametrize("E,groups", [(64, 8), (64, 4), (60, 5), (256, 8), (512, 8)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_special_biases(E, groups, score):
+    """A bias of NaN counts as no key in its group's worth; infinite and huge ones order the groups like others."""
+    size = E // groups
+    x = np.random.default_rng(E).standard_normal((9, E))
+    bias = np.zeros(E)
+    bias[:size], bias[size:2 * size] = np.nan, -np.inf
+    bias[3], bias[size + 1] = 0.8, 0.7                # the only keys of the first two groups
+    bias[2 * size:2 * size + 2] = 0.6                 # two that are worth more together
+    for group_top in (1, 2):
+        check(x, 2, F32, bias, groups, 1, group_top, score, True)
+        check(x, 3, F32, bias, groups, 2, group_top, score, True)
+    bias = np.zeros(E)
+    bias[1::size] = np.inf                            # one in each group: ties
+    check(x, 4, F32, bias, groups, 2, 2, score, True)
+    bias[1::2 * size] = 0.0                           # in every second group
+    check(x, 4, F32, bias, groups, 1, 2, score, True)
+    check(x, 4, F32, bias, groups, 1, 1, score, True)
+    most = float(torch.finfo(F32).max)
+    bias = np.zeros(E)
+    bias[2 * size], bias[2 * size + 1] = most, most / 2  # sums past float32, in two groups
+    bias[size:size + 2] = most
+    check(x, 3, F32, bias, groups, 1, 2, score, True)
+    check(x, min(size + 2, 64), F32, bias, groups, 2, 2, score, True)
+    bias = np.full(E, -most)
+    bias[3 * size:3 * size + 2] = -most / 2
+    check(x, 3, F32, bias, groups, 2, 2, score, True)
+
+
+@pytest.mark.parametrize("E,groups", [(64, 8), (60, 5), (128, 1), (256, 8), (512, 1), (20, 1)])
+def test_infinite_logits(E, groups):
+    """+inf in a softmax row: its ids are in range and no expert comes twice; other rows are as ever. Sigmoid rows take
+    +inf as a score of 1."""
+    x = np.random.default_rng(E).standard_normal((11, E)).astype(np.float32)
+    check(x, 4, F32, None, groups, max(1, groups // 2), 2, "sigmoid", False)
+    for r in (0, 3, 4):
+        x[r, np.arange(r + 1) * 4 + 1] = np.inf
+    y = x.copy()
+    y[7, 2] = np.inf
+    y[7, 3] = -np.inf
+    for rows in (x, y):
+        for bias in (None, np.linspace(0, 1, E).astype(np.float32)):
+            how = dict(groups=groups, group_k=max(1, groups // 2))
+            b = None if bias is None else t(bias)
+            w, ids = bsq.moe_gate_grouped(t(rows), 4, bias=b, score="softmax", **how)
+            wo, io = R.group_gate(rows, 4, bias, groups, how["group_k"], 2, "softmax")
+            ids = h(ids)
+            assert ((ids >= -1) & (ids < E)).all()
+            for r in range(11):
+                there = ids[r][ids[r] >= 0]
+                assert len(set(there.tolist())) == len(there)
+                if np.isfinite(rows[r]).all():
+                    np.testing.assert_array_equal(ids[r], io[r])
+            check(rows, 4, F32, bias, groups, how["group_k"], 2, "sigmoid", False)
+
+
 @pytest.mark.parametrize("E,groups,group_k", [(64, 1, 1), (64, 8, 4), (60, 5, 2), (256, 8, 4), (512, 4, 2)])
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 def test_near_ties(E, groups, group_k, score):
