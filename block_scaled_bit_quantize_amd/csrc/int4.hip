@@ -7,8 +7,8 @@
 // The products compute with integers, which bf16 holds exactly, and bring the
 // scale in once a group, in float32:
 //   y[m, n] = sum_g s[n, g] sum_(k in g) (q[n, k] - z[n, g]) x[m, k]
-// so that float32 sums are the only roundings before the output's. float32
-// activations go as three bf16 parts whose sum they are (24 bits in 8 + 8 + 8).
+// so that float32 sums are the only roundings before the output's for bf16
+// activations. float32 ones go as two fp16 parts of their scaled row, 22 bits.
 #include "bsq_int4.h"
 
 using namespace bsqd;
@@ -392,7 +392,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm_int4(
   if (st0 < st1) {
     const int g = (st1 * kStep < K ? st1 * kStep : K) / G - 1;
 #pragma unroll
-    for (int j = 0; j < NI; ++j) scale[j] = turned[(int64_t)(KG + g) * pitch + n0 + (wn * NI + j) * 32 + (lane & 31)];
+    for (int j = 0; j < NI; ++j) {
+      const int n = n0 + (wn * NI + j) * 32 + (lane & 31);  // the last tile may be wider than the scales' pitch
+      if (n < N) scale[j] = turned[(int64_t)(KG + g) * pitch + n];
+    }
   }
   T* to_part = out + split * part;
   uint8_t* mylds = lds + wave * OUT;
@@ -464,6 +467,7 @@ struct Plan {
 constexpr int64_t kUnpacked = (int64_t)128 << 20;  // bytes of unpacked weights at a time
 constexpr int64_t kPlanes = (int64_t)64 << 20;    // bytes of split activations at a time
 constexpr int64_t kParts = (int64_t)128 << 20;    // bytes of slabs' sums at a time
+constexpr int64_t kSplits = (int64_t)96 << 20;    // bytes of the sums of a split K
 
 Plan plan_of(int64_t M, int64_t N, int64_t K, int64_t group, int dtype) {
   Plan p = {};
@@ -529,6 +533,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int64_t group, int dtype) {
     for (int64_t sp = 1; sp <= 8 && (sp == 1 || steps >= 8 * sp); sp *= 2) {
       const auto& tile = kTilesOf[dtype == BSQ_F32][t];
       const int64_t n = ((p.rows + tile.m - 1) / tile.m) * ((p.slice + tile.n - 1) / tile.n) * sp;
+      if (sp > 1 && sp * p.rows * p.slice * 4 > kSplits) break;
       double us = (double)((n + cus - 1) / cus) * (double)((steps + sp - 1) / sp) * tile.us;
       if (sp > 1) us += 5.0 + (double)(sp * p.rows * p.slice) * 8.0 / 4e6;
       if (us < least) least = us, p.tile = t, p.splits = (int)sp;

@@ -450,7 +450,7 @@ int bsq_moe_gate_backward(const float* dweights, const float* weights, const int
  *            scale * s_j / (sum of the row's selected scores), in float32.
  *   topk_ids int32 [tokens, k] (a row with a -1 is no input for bsq_route).
  *   A softmax row with a logit of +inf gives unspecified weights and ids
- *   (distinct, in range).
+ *   (-1 or in range, none twice).
  * bsq_moe_gate_grouped_backward: gradient of sum dweights * weights to the
  *   logits, the selection held fixed (the bias has none). dweights, weights,
  *   topk_ids, logits as above, ids of a row distinct (ids outside [0, E) add
@@ -562,12 +562,16 @@ int bsq_linear_int8(const void* x, int dtype, const int8_t* b_codes, const float
  * bsq_dequantize_int4: out [N, K] of out_dtype, (q - z) * s exact in float32,
  *   rounded to nearest even in bf16.
  * bsq_linear_int4: out[m, n] = sum_k x[m, k] w[n, k] + bias[n], x [M, K] of
- *   `dtype`, bias FP32 [N] or NULL, out [M, N] of out_dtype. x (F32 too) and
- *   the integers q - z enter unrounded; sums over a group and over groups are
- *   float32, and the output is rounded once. A row of x with a NaN or an
- *   infinity gives no finite output; sums of |x| * 15 over a group stay below
- *   2^128. ws bsq_linear_int4_workspace() bytes (0, and ws may be NULL, for
- *   few rows; 320 MiB at most).
+ *   `dtype`, bias FP32 [N] or NULL, out [M, N] of out_dtype. The integers q - z
+ *   and bf16 x enter unrounded. F32 x enters with 22 significant bits: off by
+ *   2^-22 of itself, or 2^-39 of its row's largest magnitude if that is more
+ *   (in rows whose largest is below 2^-112, by 2^-151). Sums over a group and
+ *   over groups are float32, and the output is rounded once. Calls of many rows
+ *   (those that need ws for their weights) take a scale of less than 2^-64 of
+ *   the largest of its weight row's as that, with values rounded to x's 16-bit
+ *   type. A row of x with a NaN or an infinity gives no finite output; sums of
+ *   |x| * 15 over a group stay below 2^128. ws bsq_linear_int4_workspace()
+ *   bytes (0, and ws may be NULL, for few rows; 320 MiB at most).
  * group <= K <= 32768, K % group == 0, N and M < 2^31. x, w, codes and ws (and
  * bsq_dequantize_int4's out) 16-byte aligned, out and scales to their type,
  * bias 4. Codes of a batch past M, N or K are neither read nor written.

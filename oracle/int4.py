@@ -48,9 +48,10 @@ def values(codes, scales, zeros=None):
 
 def linear(x, codes, scales, zeros=None, bias=None):
     """(y, bound) float64 [M, N]. bound: what float32 sums may be off by. A group's sums of q x and of z x (or of
-    (q - z) x) are exact products added one after the other, three parts of each for float32 activations, then a sum
+    (q - z) x) are exact products added one after the other, two parts of each for float32 activations, then a sum
     over groups and parts of K: one rounding, or one cut at the same place, for each addition, 2^-23 of at most the sum
-    of the terms' sizes."""
+    of the terms' sizes. (Two additions a value of a group; the third covers the cut of float32 activations to 22 bits,
+    2^-22 of the sum of the terms' sizes.)"""
     x = np.asarray(x, dtype=np.float64)
     q, z, s = parts(codes, scales, zeros)
     N, KG, group = q.shape

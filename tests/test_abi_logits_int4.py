@@ -103,6 +103,8 @@ def test_int4_workspace(lib):
             for K, group in ((32, 32), (4096, 128), (32768, 32), (32736, 32)):
                 for dtype in (0, 1):
                     assert w(M, N, K, group, dtype) <= 320 << 20, (M, N, K, group, dtype)
+    for M, N, K, group, dtype in ((26592, 482364, 32768, 32, 1), (13127, 23388, 32768, 32, 1), (1189, 32112, 9472, 32, 0)):
+        assert w(M, N, K, group, dtype) <= 320 << 20  # sizes that K could be split for
 
 
 def test_logprobs(lib):
