@@ -50,7 +50,8 @@ __device__ __forceinline__ float rounded_quotient(float v, float s, float inv) {
 }
 
 // A lane holds 16 neighbours; G / 16 lanes share a group. The weights are one
-// long array of groups: K is whole groups. Bound by memory.
+// long array of groups: K is whole groups. Bound by memory: 50021 x 4096 bf16,
+// groups of 128, in 117 us, 4.4 TB/s; 2048 x 7168 float32, groups of 32, in 13.7.
 template <typename T, int G>
 __global__ __launch_bounds__(kQThreads) void k_quant_int4(const T* __restrict__ w, int64_t units, int symmetric,
                                                          u32x2* __restrict__ codes, uint16_t* __restrict__ scales,
@@ -95,7 +96,8 @@ __global__ __launch_bounds__(kQThreads) void k_quant_int4(const T* __restrict__ 
 }
 
 // Pieces of 16 bytes of the output, neighbouring lanes side by side: bound by
-// memory (a lane's four pieces side by side took 22 us for 2048 x 7168 float32).
+// memory (a lane's four pieces side by side took 22 us for 2048 x 7168 float32, this
+// 12.4, 5.3 TB/s; 50021 x 4096 to bf16 78 us, 6.6 TB/s).
 constexpr int kDPieces = 4;
 template <typename T>
 __global__ __launch_bounds__(kQThreads) void k_dequant_int4(const uint8_t* __restrict__ codes,
@@ -216,7 +218,10 @@ __global__ __launch_bounds__(kUThreads) void k_split_f32(const f32x4* __restrict
 // counted here. A wave reads the fragments of the instructions after the next
 // while it multiplies (the ones right ahead came too late: 0.67 us a step of
 // 128 x 128 tiles): the barrier stands before the last kAhead instructions along
-// a step, whose fragments are in registers by then.
+// a step, whose fragments are in registers by then. 16384 x 4096 x 4096 in bf16:
+// 470 to 490 us, 1.12 to 1.17 PFLOP/s (a library's bf16 product of these sizes 430
+// us); 1001 x 4099 x 1536 in float32, two products each: 41 us, one round of 198
+// tiles and their steps' latency.
 constexpr int kStep = 64, kAhead = 2;
 template <typename X, typename T, int G, int WM, int WN, int MI, int NI, int ST>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm_int4(

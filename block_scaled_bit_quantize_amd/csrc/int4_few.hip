@@ -4,7 +4,9 @@
 // once. Weights go from memory to registers: a wave keeps kDeep chunks of 16 rows
 // by 256 codes on their way, across tiles of 16 rows. (With chunks of 128 the loads
 // of scales and zero points, a row a lane, kept the address unit as busy as those
-// of the codes: 72 us for 100003 x 4096 and one row.)
+// of the codes: 72 us for 100003 x 4096 and one row. As it is 5 rows take 43 us,
+// 4.9 TB/s; 4096 x 4096 and one row 6.8 us, its latency from launch to first weights,
+// 16 tiles' rounds and the joined sums.)
 //   SHARE: up to 16 rows of x, whole in LDS. The eight waves of a workgroup share
 //   K, and their partial sums meet in LDS; a workgroup takes tile after tile.
 //   else: more rows, or longer ones. A workgroup has a slab of K of them in LDS,

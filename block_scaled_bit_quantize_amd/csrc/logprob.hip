@@ -9,8 +9,10 @@
 //
 // One pass over the logits with a running maximum: sums relative to m become
 // sums relative to m' > m by s' = s f, u' = (u + (m - m') s) f, f = e^(m - m').
-// Bound by memory for many rows; few rows are cut into parts for as many
-// workgroups, whose sums meet in a second launch.
+// Bound by memory for many rows (4096 x 131072 bf16: 220 to 250 us, 4.3 to 4.9
+// TB/s; the gradient, which reads and writes, 350 to 360, 6 TB/s); few rows are cut
+// into parts for as many workgroups, whose sums meet in a second launch (one row of
+// 100003 float32, top 20: 3.8 and 11.7 us, 64 of 131072 bf16, top 5: 10.4 and 8.4).
 //
 // Alternatives: the pass also leaves the maximum of every block of 64
 // neighbours. Ordered by value, then by lower index, the k best elements lie
