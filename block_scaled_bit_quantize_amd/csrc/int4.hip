@@ -135,32 +135,45 @@ __global__ __launch_bounds__(kQThreads) void k_dequant_int4(const uint8_t* __res
 // are multiplied by s[g - 1] / s[g], at the end by the last scale, so that there
 // is one set of them (a second one for the group's own sum left room for tiles of
 // 256 x 128 only, which are bound by L2: 12 TB/s, 1.07 PFLOP/s).
-constexpr int kUThreads = 256;
-// A wave a row of weights. The tiles hold sums in units of a group's scale, so no
+constexpr int kUThreads = 256, kURows = 16;
+// A wave a row of weights, 16 rows a workgroup, whose scales are turned in LDS (a
+// wave's own stores of them, a line each: 4099 x 1536 in 11.6 and not 10.2 us). The tiles hold sums in units of a group's scale, so no
 // scale may be too small for the others': one below 2^-64 of the row's largest is
 // raised to that, and its integers become the (then rounded) smaller values.
 // turned: [group][row] the scale of the group before over the group's, then the
 // same of the scales (divisions here, once, cost the tiles nothing).
 template <typename X>
-__global__ __launch_bounds__(kUThreads) void k_unpack_int4(const uint32_t* __restrict__ codes,
+__global__ __launch_bounds__(64 * kURows) void k_unpack_int4(const uint32_t* __restrict__ codes,
                                                           const uint16_t* __restrict__ scales,
                                                           const uint8_t* __restrict__ zeros, int64_t rows, int units,
                                                           int shift, int KG, int64_t pitch, u32x4* __restrict__ w,
                                                           float* __restrict__ turned) {
-  const int64_t row = (int64_t)blockIdx.x * (kUThreads / 64) + (threadIdx.x >> 6);
-  if (row >= rows) return;
+  __shared__ float table[2][64][kURows + 1];
+  const int64_t row0 = (int64_t)blockIdx.x * kURows, row = row0 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
+  const int mine = row < rows ? KG : 0;  // groups: waves past the end have none
   float most = 0.0f;
-  for (int g = lane; g < KG; g += 64) most = fmaxf(most, fabsf(from_bf16(scales[row * KG + g])));
+  for (int g = lane; g < mine; g += 64) most = fmaxf(most, fabsf(from_bf16(scales[row * KG + g])));
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor(most, o, 64));
   const float least = most > 0.0f ? most * 0x1p-64f : 1.0f;
   auto raised = [&](float v) { return fabsf(v) < least ? least : v; };
-  for (int g = lane; g < KG; g += 64) {
-    const float s = raised(from_bf16(scales[row * KG + g]));
-    turned[g * pitch + row] = g ? raised(from_bf16(scales[row * KG + g - 1])) / s : 0.0f;
-    turned[(KG + g) * pitch + row] = s;
+  for (int g0 = 0; g0 < KG; g0 += 64) {
+    const int g = g0 + lane;
+    if (g < mine) {
+      const float s = raised(from_bf16(scales[row * KG + g]));
+      table[0][lane][threadIdx.x >> 6] = g ? raised(from_bf16(scales[row * KG + g - 1])) / s : 0.0f;
+      table[1][lane][threadIdx.x >> 6] = s;
+    }
+    __syncthreads();
+    const int r = threadIdx.x % kURows, to = g0 + threadIdx.x / kURows;
+    if (to < KG && row0 + r < rows) {
+      turned[to * pitch + row0 + r] = table[0][threadIdx.x / kURows][r];
+      turned[(KG + to) * pitch + row0 + r] = table[1][threadIdx.x / kURows][r];
+    }
+    __syncthreads();
   }
+  if (row >= rows) return;
 #pragma unroll 4
   for (int u = lane; u < units; u += 64) {  // eight codes
     const uint32_t c = codes[row * units + u];
@@ -609,7 +622,7 @@ int run_linear(const X* x, const uint8_t* codes, const uint16_t* scales, const u
   const int64_t KG = K / G;
   for (int64_t n0 = 0; n0 < N; n0 += p.slice) {
     const int64_t n = N - n0 < p.slice ? N - n0 : p.slice;
-    hipLaunchKernelGGL((k_unpack_int4<X>), dim3((unsigned)((n + kUThreads / 64 - 1) / (kUThreads / 64))), dim3(kUThreads), 0,
+    hipLaunchKernelGGL((k_unpack_int4<X>), dim3((unsigned)((n + kURows - 1) / kURows)), dim3(64 * kURows), 0,
                        s, reinterpret_cast<const uint32_t*>(codes + n0 * (K / 2)), scales + n0 * KG,
                        zeros ? zeros + n0 * KG : nullptr, n, (int)(K / 8), G == 32 ? 2 : G == 64 ? 3 : 4, (int)KG, p.slice,
                        w, turned);
