@@ -15,13 +15,16 @@
 //
 // How the order can be that of float64 keys at the speed of float32: keys are
 // made in float32 with a bound on their error, the selection is made by them,
-// and the groups at the cut and the selected keys next to each other are then
-// looked at. Where two are nearer than their bounds and do not come from equal
-// logits and biases (equal inputs are a true tie), the row is ambiguous (1 row in
-// about 500). Where all that may be selected has a place in its lanes, those are
-// put in order by float64 keys; else its wave selects from the start in float64
-// with all 64 lanes (with that for all ambiguous rows 38.6 us in place of 32: 65536
-// tokens, 128 experts, bf16).
+// and the groups at the cut, the selected keys next to each other, and the least
+// of them with all that are not selected are then looked at (all: a bound goes
+// with the score, so a key that a bias takes back from a large score may reach
+// past one that is ahead of it). Where two are nearer than their bounds and are not
+// keys of equal logits and biases (a true tie), the row is ambiguous (1 row in about
+// 500 of random logits). Where all that may be selected has a place in its lanes,
+// those are put in order by float64 keys; else, and where it is groups that are
+// near or tie, its wave selects from the start in float64 with all 64 lanes (with
+// that for all ambiguous rows 38.6 us in place of 32: 65536 tokens, 128 experts,
+// bf16).
 //
 // 8 lanes share a row up to 128 experts, 16 up to 256 and 64 above; a lane holds
 // V neighbouring experts in registers. Bound by vector instructions: k + 1 rounds
@@ -43,6 +46,7 @@ constexpr int kMaxGroups = 64;
 // number whatever its low word holds.
 constexpr uint32_t kGone = 0xFFEFFFFFu;
 constexpr float kInf = __builtin_inff();
+constexpr float kBig = __FLT_MAX__ * (1.0f - 0x1p-20f);  // below an infinite key, and below a sum past float32
 
 struct Choice {
   int E, k, groups, size, group_k, group_top;  // groups 1: no restriction
@@ -71,9 +75,10 @@ __device__ __forceinline__ float sigmoid32(float x) {
 // reciprocal 2);
 // a softmax score by less than 2^-16 s (its sum by 2^-19, |l - m| 2^-24 from the
 // difference, up to 64 of it: beyond, s is below 2^-92 and the last term covers it);
-// the sum with the bias by 2^-24 |c|. Exponentials that flush to zero are below 2^-110.
+// the sum with the bias by 2^-24 |c|, and the bound's own sum or difference with c
+// by as much. Exponentials that flush to zero are below 2^-110.
 __device__ __forceinline__ float key_bound(float s, float c, bool softmax) {
-  return s * (softmax ? 0x1p-16f : 0x1p-21f) + fabsf(c) * 0x1p-23f + 0x1p-90f;
+  return s * (softmax ? 0x1p-16f : 0x1p-21f) + fabsf(c) * 0x1.8p-23f + 0x1p-90f;
 }
 
 // Key above its index in one float64: a larger number is a larger key, or the
@@ -150,7 +155,6 @@ __device__ __forceinline__ void worth(const Top& t, int group_top, bool softmax,
   }
   const bool two = group_top == 2 && t.b > -kInf;
   const float w = two ? t.a + t.b : t.a;
-  constexpr float kBig = __FLT_MAX__ * (1.0f - 0x1p-20f);
   if (!(fabsf(w) <= kBig)) {  // an infinite bias, or a sum past float32
     low = w > 0.0f ? kBig : -kInf;
     high = w > 0.0f ? kInf : -kBig;
@@ -162,12 +166,15 @@ __device__ __forceinline__ void worth(const Top& t, int group_top, bool softmax,
   high = w + tol;
 }
 
-// What a wave needs of LDS: the rows' float32 keys (or one row's in float64),
-// a word for each of their groups (or the groups' worth in float64), the groups kept.
+// What a wave needs of LDS: the rows' float32 keys, then what they are at most, by
+// lanes (in registers, 124 in place of 98, 65536 x 128 took 31 us and not 29), or
+// one row's keys in float64; a word for each of their groups (or the groups' worth
+// in float64), the groups kept.
 template <int L, int V>
 struct WaveLds {
   union {
     float key[64 / L][L * V];
+    float high[V][64];
     double key64[L * V];
   };
   union {
@@ -390,8 +397,12 @@ __global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ l
     }
   }
   double key[V];
+  wave_fence();
 #pragma unroll
-  for (int i = 0; i < V; ++i) key[i] = with_index(b[i], e0 + i);
+  for (int i = 0; i < V; ++i) {
+    key[i] = with_index(b[i], e0 + i);
+    lds.high[i][lane] = b[i] + key_bound(s[i], b[i], c.softmax);
+  }
   auto next = [&]() {  // the row's largest key, which is taken out
     double best = key[0];
 #pragma unroll
@@ -401,6 +412,12 @@ __global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ l
     for (int i = 0; i < V; ++i)
       key[i] = key[i] == best ? __hiloint2double((int)kGone, __double2loint(key[i])) : key[i];
     return best;
+  };
+  auto left = [&]() {  // the most that a key not taken out may be, of this lane's
+    float most = -kInf;
+#pragma unroll
+    for (int i = 0; i < V; ++i) most = fmaxf(most, is_gone(key[i]) ? -kInf : lds.high[i][lane]);
+    return most;
   };
   int ri[KR];
 #pragma unroll
@@ -422,11 +439,12 @@ __global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ l
   };
 #pragma unroll
   for (int q = 0; q < KR; ++q) look(ri[q] >= 0 ? ri[q] : 0, rx[q], rb[q], rs[q], rc[q], tol[q]);
-  // each against the one after it
+  // the selected each against the one after it; the first that is not, and all others, against the least of them
   const int first = mine * L;  // the row's first lane
   bool tied = false;           // the last selected and the first that is not come from equal inputs
-  bool close = false;          // two that follow each other are nearer than the bounds
-  bool open = false;           // the last selected and the first that is not are
+  bool close = false;          // two selected that follow each other are nearer than the bounds
+  float low = kInf;            // what the selected keys are at least
+  float rest = left();         // what the others are at most, but for the first one of a tie
 #pragma unroll
   for (int q = 0; q < KR; ++q) {
     const int from = first + (sub + 1) % L;
@@ -443,39 +461,37 @@ __global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ l
     const int j = q * L + sub;
     if (j < c.k && ri[q] >= 0 && ni >= 0) {
       const bool same = nx == rx[q] && nb == rb[q];
-      const bool near = !same && !(rc[q] - nc > tol[q] + nt);
-      close |= near;
-      open |= near && j == c.k - 1;
-      tied |= same && j == c.k - 1;
+      if (j < c.k - 1) close |= !same && !(rc[q] - nc > tol[q] + nt);
+      else if (same) tied = true;
+      else rest = fmaxf(rest, nc + nt);
     }
+    if (j < c.k && ri[q] >= 0) low = fminf(low, rc[q] == kInf ? kBig : rc[q] - tol[q]);
   }
-  if (__any(tied)) {  // more of the same may follow, and behind them one that is nearer than the bounds
+  low = over_row<L>(low, [](float p, float q) { return fminf(p, q); });
+  bool open = row_maxf<L>(rest) >= low;  // it is open what is selected
+  if (__any(tied && open && ok)) {  // of the others, those of the same inputs are behind the last selected by their index
     const int at = first + (c.k - 1) % L;
-    float lx = 0, lb = 0, lc = 0, lt = 0;
-    bool go = false;
+    float lx = 0, lb = 0;
+    bool tie = false;
 #pragma unroll
     for (int q = 0; q < KR; ++q)
       if (q == (c.k - 1) / L) {
-        lx = __shfl(rx[q], at, 64), lb = __shfl(rb[q], at, 64), lc = __shfl(rc[q], at, 64), lt = __shfl(tol[q], at, 64);
-        go = __shfl((int)tied, at, 64);
+        lx = __shfl(rx[q], at, 64), lb = __shfl(rb[q], at, 64);
+        tie = __shfl((int)(tied && open), at, 64);
       }
-    while (__any(go)) {  // ends: every turn takes a key out of each row
-      const double best = next();
-      if (go) {
-        go = false;
-        if (!is_gone(best)) {
-          float nx, nb, ns, nc, nt;
-          look(index_of(best), nx, nb, ns, nc, nt);
-          if (nx == lx && nb == lb) go = true;
-          else unsure |= !(lc - nc > lt + nt);
-        }
-      }
-    }
-    unsure |= close;
-  } else if (KR <= 2 && __any(close && ok)) {
+    rest = -kInf;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (tie && !is_gone(key[i]) && !(load1(row + e0 + i) == lx && (bias ? bias[e0 + i] : 0.0f) == lb))
+        rest = fmaxf(rest, lds.high[i][lane]);
+    rest = row_maxf<L>(rest);
+    if (tie) open = rest >= low;
+    unsure |= tie && close;  // one of the same may belong before a selected one
+  }
+  if (KR <= 2 && __any((close || open) && ok)) {
     // Where it is open what is selected, the free places of a row take the keys that follow: all that may be
-    // selected are then there, unless the last of them is still near the last selected one. What is there is put in
-    // order by float64 keys.
+    // selected are then there, unless one that is left may still reach the least of the selected. What is there is
+    // put in order by float64 keys.
     constexpr int C = L * KR;
     const bool more = __any(open && ok);
     for (int j = c.k + 1; more && j < C; ++j) {
@@ -485,7 +501,8 @@ __global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ l
         if (j == q * L + sub && !is_gone(best)) ri[q] = index_of(best);
     }
     const uint64_t of_row = (L == 64 ? ~0ull : (1ull << (L & 63)) - 1) << first;
-    const bool sort = (__ballot(close) & of_row) != 0, cuts = (__ballot(open) & of_row) != 0;
+    const bool sort = (__ballot(close || open) & of_row) != 0;
+    unsure |= row_maxf<L>(left()) >= low && open;
     double total = 1.0;
     if (c.softmax) {
       total = 0.0;
@@ -497,21 +514,16 @@ __global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ l
       total = over_row<L>(total, [](double p, double q) { return p + q; });
     }
     double kd[KR];
-    float cut = 0.0f, cut_tol = 0.0f, end = -kInf, end_tol = 0.0f;
 #pragma unroll
     for (int q = 0; q < KR; ++q) {
-      float ls, lc = -kInf, lt = 0.0f;
+      float ls, lc, lt;
       kd[q] = -(double)kInf;
       if (ri[q] >= 0) {
         look(ri[q], rx[q], rb[q], ls, lc, lt);
         // NaN where a softmax row holds +inf: above the empty places, so that ranks are distinct there too
         kd[q] = fmax(key64(rx[q], rb[q], c.softmax, m, total), -__DBL_MAX__);
       }
-      const float vc = __shfl(lc, first + (c.k - 1) % L, 64), vt = __shfl(lt, first + (c.k - 1) % L, 64);
-      if (q == (c.k - 1) / L) cut = vc, cut_tol = vt;
-      if (q == KR - 1) end = __shfl(lc, first + L - 1, 64), end_tol = __shfl(lt, first + L - 1, 64);
     }
-    if (cuts && end > -kInf && !(cut - end > cut_tol + end_tol)) unsure = true;
     int rank[KR];
 #pragma unroll
     for (int q = 0; q < KR; ++q) rank[q] = 0;
@@ -540,7 +552,7 @@ __global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ l
     }
     wave_fence();
   } else {
-    unsure |= close;
+    unsure |= close || open;
   }
   // rows that float32 cannot settle, one after the other
   uint64_t again = __ballot(unsure && ok);
