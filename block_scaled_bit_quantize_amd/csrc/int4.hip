@@ -136,10 +136,24 @@ __global__ __launch_bounds__(kQThreads) void k_dequant_int4(const uint8_t* __res
 // is one set of them (a second one for the group's own sum left room for tiles of
 // 256 x 128 only, which are bound by L2: 12 TB/s, 1.07 PFLOP/s).
 constexpr int kUThreads = 256, kURows = 16;
+constexpr int kSpread = 64;  // the tiles' scales are at least 2^-kSpread of their row's largest, but for a factor of 2
+// Scales too small for their row's largest are raised by a power of two, and their
+// integers are that much smaller: exact, as long as the 16-bit type has the bits
+// (fp16 down to 2^-24, bf16 to 2^-133). So the ratios of scales are finite, and
+// none is zero: a scale of zero stands for integers of zero at the least scale.
+struct Raised {
+  float scale, factor;  // of the integers
+};
+// top: exponent of the row's largest scale, 1/2 <= f < 1 in f 2^top.
+__device__ __forceinline__ int least_exponent(int top) { return top - kSpread > -125 ? top - kSpread : -125; }
+__device__ __forceinline__ Raised raised(float s, int least) {
+  if (s == 0.0f) return {__builtin_ldexpf(0.5f, least), 0.0f};
+  const int up = least - __builtin_amdgcn_frexp_expf(s);  // of a NaN or an infinity 0: no output is finite
+  if (up <= 0 || !(fabsf(s) < __builtin_inff())) return {s, 1.0f};
+  return {__builtin_ldexpf(s, up), __builtin_ldexpf(1.0f, -up)};
+}
 // A wave a row of weights, 16 rows a workgroup, whose scales are turned in LDS (a
-// wave's own stores of them, a line each: 4099 x 1536 in 11.6 and not 10.2 us). The tiles hold sums in units of a group's scale, so no
-// scale may be too small for the others': one below 2^-64 of the row's largest is
-// raised to that, and its integers become the (then rounded) smaller values.
+// wave's own stores of them, a line each: 4099 x 1536 in 11.6 and not 10.2 us).
 // turned: [group][row] the scale of the group before over the group's, then the
 // same of the scales (divisions here, once, cost the tiles nothing).
 template <typename X>
@@ -153,16 +167,18 @@ __global__ __launch_bounds__(64 * kURows) void k_unpack_int4(const uint32_t* __r
   const int lane = threadIdx.x & 63;
   const int mine = row < rows ? KG : 0;  // groups: waves past the end have none
   float most = 0.0f;
-  for (int g = lane; g < mine; g += 64) most = fmaxf(most, fabsf(from_bf16(scales[row * KG + g])));
+  for (int g = lane; g < mine; g += 64) {
+    const float s = fabsf(from_bf16(scales[row * KG + g]));
+    most = s < __builtin_inff() ? fmaxf(most, s) : most;
+  }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor(most, o, 64));
-  const float least = most > 0.0f ? most * 0x1p-64f : 1.0f;
-  auto raised = [&](float v) { return fabsf(v) < least ? least : v; };
+  const int least = least_exponent(__builtin_amdgcn_frexp_expf(most));
   for (int g0 = 0; g0 < KG; g0 += 64) {
     const int g = g0 + lane;
     if (g < mine) {
-      const float s = raised(from_bf16(scales[row * KG + g]));
-      table[0][lane][threadIdx.x >> 6] = g ? raised(from_bf16(scales[row * KG + g - 1])) / s : 0.0f;
+      const float s = raised(from_bf16(scales[row * KG + g]), least).scale;
+      table[0][lane][threadIdx.x >> 6] = g ? raised(from_bf16(scales[row * KG + g - 1]), least).scale / s : 0.0f;
       table[1][lane][threadIdx.x >> 6] = s;
     }
     __syncthreads();
@@ -178,16 +194,10 @@ __global__ __launch_bounds__(64 * kURows) void k_unpack_int4(const uint32_t* __r
   for (int u = lane; u < units; u += 64) {  // eight codes
     const uint32_t c = codes[row * units + u];
     const int64_t g = row * KG + (u >> shift);
-    const float z = zeros ? (float)zeros[g] : 8.0f, own = from_bf16(scales[g]), s = raised(own);
+    const float z = zeros ? (float)zeros[g] : 8.0f, f = raised(from_bf16(scales[g]), least).factor;
     typename Mfma<X>::V v;
-    if (s == own) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = Mfma<X>::near((float)(c >> (4 * j) & 15u) - z);
-    } else {  // raised, or NaN: so are the values
-      const float f = own / s;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = Mfma<X>::near(((float)(c >> (4 * j) & 15u) - z) * f);
-    }
+    for (int j = 0; j < 8; ++j) v[j] = Mfma<X>::near(((float)(c >> (4 * j) & 15u) - z) * f);
     w[row * units + u] = __builtin_bit_cast(u32x4, v);
   }
 }
