@@ -136,16 +136,22 @@ __global__ __launch_bounds__(kQThreads) void k_dequant_int4(const uint8_t* __res
 // is one set of them (a second one for the group's own sum left room for tiles of
 // 256 x 128 only, which are bound by L2: 12 TB/s, 1.07 PFLOP/s).
 constexpr int kUThreads = 256, kURows = 16;
-constexpr int kSpread = 64;  // the tiles' scales are at least 2^-kSpread of their row's largest, but for a factor of 2
 // Scales too small for their row's largest are raised by a power of two, and their
 // integers are that much smaller: exact, as long as the 16-bit type has the bits
 // (fp16 down to 2^-24, bf16 to 2^-133). So the ratios of scales are finite, and
 // none is zero: a scale of zero stands for integers of zero at the least scale.
+// The sums in units of the least scale must not pass float32: bf16 x comes in any
+// size, and all scales are raised to the largest's binade, so that the sums are
+// below 30 sum |x|; float32 x is below 2^15, and 2^-64 leaves them below 2^100.
 struct Raised {
   float scale, factor;  // of the integers
 };
 // top: exponent of the row's largest scale, 1/2 <= f < 1 in f 2^top.
-__device__ __forceinline__ int least_exponent(int top) { return top - kSpread > -125 ? top - kSpread : -125; }
+template <typename X>
+__device__ __forceinline__ int least_exponent(int top) {
+  const int least = top - (sizeof(X) == 4 ? 64 : 0);
+  return least > -125 ? least : -125;
+}
 __device__ __forceinline__ Raised raised(float s, int least) {
   if (s == 0.0f) return {__builtin_ldexpf(0.5f, least), 0.0f};
   const int up = least - __builtin_amdgcn_frexp_expf(s);  // of a NaN or an infinity 0: no output is finite
@@ -173,7 +179,7 @@ __global__ __launch_bounds__(64 * kURows) void k_unpack_int4(const uint32_t* __r
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor(most, o, 64));
-  const int least = least_exponent(__builtin_amdgcn_frexp_expf(most));
+  const int least = least_exponent<X>(__builtin_amdgcn_frexp_expf(most));
   for (int g0 = 0; g0 < KG; g0 += 64) {
     const int g = g0 + lane;
     if (g < mine) {

@@ -567,10 +567,11 @@ int bsq_linear_int8(const void* x, int dtype, const int8_t* b_codes, const float
  *   2^-22 of itself, or 2^-39 of its row's largest magnitude if that is more
  *   (in rows whose largest is below 2^-112, by 2^-151). Sums over a group and
  *   over groups are float32, and the output is rounded once. Calls of many rows
- *   (those that need ws for their weights) hold the weights of a row as they
- *   are down to 2^-87 of its largest scale, and off by 2^-88 of it below. A row
- *   of x with a NaN or an infinity gives no finite output; sums of
- *   |x| * 15 over a group stay below 2^128. ws bsq_linear_int4_workspace()
+ *   (those that need ws for their weights) sum in units of about their weight
+ *   row's largest scale: with BF16 x, weights and products of less than 2^-125
+ *   of it may be lost; with F32 x, weights of less than 2^-87 of it are off by
+ *   2^-88 of it. A row of x with a NaN or an infinity gives no finite output;
+ *   sums of |x| * 30 over a row stay below 2^128. ws bsq_linear_int4_workspace()
  *   bytes (0, and ws may be NULL, for few rows; 320 MiB at most).
  * group <= K <= 32768, K % group == 0, N and M < 2^31. x, w, codes and ws (and
  * bsq_dequantize_int4's out) 16-byte aligned, out and scales to their type,

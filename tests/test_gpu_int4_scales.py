@@ -72,6 +72,26 @@ def test_negative_scales(M, zeros, dtype):
     product(dev(rng.standard_normal((M, K)), dtype)[0], c, s, z, group)
 
 
+@pytest.mark.parametrize("M", ROWS)
+@pytest.mark.parametrize("group", [32, 128])
+def test_large_activations_and_scales_far_apart(M, group):
+    """bf16 x around 2^60, scales of 1 and 2^-64 and all between: sums and outputs are far from float32's end, whatever
+    the order of the scales."""
+    rng = np.random.default_rng(M + group)
+    N, K = 48, 1024
+    c, z = codes(rng, N, K, group)
+    KG = K // group
+    s = np.exp2(rng.uniform(-64, 0, (N, KG)))
+    s[0] = np.where(np.arange(KG) % 2, 2.0 ** -64, 1.0)
+    s[1] = np.where(np.arange(KG) % 2, 1.0, 2.0 ** -64)
+    s[2] = np.exp2(-64.0 * np.arange(KG) / KG)
+    s[3] = s[2, ::-1]
+    s[4], s[4, 0] = 2.0 ** -64, 1.0
+    s[5], s[5, 0] = 2.0 ** -120, 2.0 ** -40
+    for size in (60, 100):
+        product(dev(rng.standard_normal((M, K)) * 2.0 ** size, BF16)[0], c, s, z, group)
+
+
 @pytest.mark.parametrize("dtype,far", [(BF16, 100), (F32, 80)])
 @pytest.mark.parametrize("M", ROWS)
 @pytest.mark.parametrize("group", [32, 128])
