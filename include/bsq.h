@@ -571,7 +571,8 @@ int bsq_linear_int8(const void* x, int dtype, const int8_t* b_codes, const float
  *   row's largest scale: with BF16 x, weights and products of less than 2^-125
  *   of it may be lost; with F32 x, weights of less than 2^-87 of it are off by
  *   2^-88 of it. A row of x with a NaN or an infinity gives no finite output;
- *   sums of |x| * 30 over a row stay below 2^128. ws bsq_linear_int4_workspace()
+ *   sums of |x| * 30 over a row stay below 2^128, and scales below 2^93 with F32
+ *   x (whose rows are brought to 2^15 on the way). ws bsq_linear_int4_workspace()
  *   bytes (0, and ws may be NULL, for few rows; 320 MiB at most).
  * group <= K <= 32768, K % group == 0, N and M < 2^31. x, w, codes and ws (and
  * bsq_dequantize_int4's out) 16-byte aligned, out and scales to their type,

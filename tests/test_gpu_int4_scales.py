@@ -111,3 +111,17 @@ def test_small_scales_beside_large_ones(M, group, dtype, far):
     got, want = product(dev(x, dtype)[0], c, s, z, group)
     small = (got[::2, ::2], want[::2, ::2])
     assert (np.abs(small[1]) < 2.0 ** (20 - far)).all() and (small[0] != 0).mean() > 0.99
+
+
+@pytest.mark.parametrize("M", ROWS)
+@pytest.mark.parametrize("K", [1024, 32768])
+def test_largest_scales_of_float32_activations(M, K):
+    """Scales just below 2^93 and small activations, all of one sign with the largest integers: the rows are brought to
+    2^15 on the way, and 2^15 * 15 * 32768 * 2^93 is below 2^127."""
+    rng = np.random.default_rng(M + K)
+    N, group = 20, 128
+    c, z = codes(rng, N, K, group)
+    c[:4], z[:4] = 0xFF, 0
+    s = np.exp2(rng.uniform(88, 92.9, (N, K // group)))
+    x = rng.uniform(0.9, 1, (M, K)) * np.exp2(rng.integers(-100, 15, (M, 1)))
+    product(dev(x)[0], c, s, z, group)
