@@ -24,6 +24,7 @@
 
 #include "bsq_device.h"
 #include "bsq_internal.h"
+#include "bsq_rows.h"
 
 using namespace bsqd;
 
@@ -39,8 +40,6 @@ constexpr int kMaxParts = 256;  // of a row
 constexpr float kInf = __builtin_inff();
 constexpr float kFar = -200.0f;  // e^kFar is 0 in float32
 
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ float load1(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
 
@@ -94,11 +93,6 @@ struct Row {
     }
   }
 };
-
-template <int CTRL>
-__device__ __forceinline__ float dpp(float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
-}
 
 struct Sums {
   float m, s, u;  // maximum, sum e^(x - m), sum (x - m) e^(x - m)
@@ -229,6 +223,7 @@ constexpr int blocks_of(int V) { return V / kBlock + 1; }  // at most: the row m
 // groups of a row's blocks, so that the best ones' blocks fit the list
 constexpr int first_of(int V) { return V > kSmall ? 512 : kMost; }
 
+using bsqd::dpp;
 template <int CTRL>
 __device__ __forceinline__ u64 dpp(u64 v) {
   return (u64)(uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, 0xF, 0xF, false) << 32 |

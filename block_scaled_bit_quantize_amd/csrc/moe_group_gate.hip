@@ -95,10 +95,7 @@ __device__ __forceinline__ int index_of(double d) {
   return __double2hiint(d) < 0 ? low : 1023 - low;
 }
 
-template <int CTRL>
-__device__ __forceinline__ float dpp(float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
-}
+using bsqd::dpp;
 template <int CTRL>
 __device__ __forceinline__ double dpp(double v) {
   return __hiloint2double(__builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, 0xF, 0xF, false),
@@ -692,9 +689,17 @@ void launch_gate(const T* logits, const float* bias, int64_t tokens, Choice c, f
     const unsigned grid = (unsigned)((n + per - 1) / per);
 #define BSQ_K(KR) \
   hipLaunchKernelGGL((k_group_gate<T, L, V, WHOLE, KR>), dim3(grid), dim3(kThreads), 0, s, logits, bias, n, c, weights, ids)
-    if (c.k < L) BSQ_K(1);
-    else if (c.k < 16) BSQ_K((16 + L - 1) / L);
-    else BSQ_K(64 / L + 1);
+    if (c.k < L) {
+      BSQ_K(1);
+      continue;
+    }
+    if constexpr (L < 16) {
+      if (c.k < 16) {
+        BSQ_K(16 / L);
+        continue;
+      }
+    }
+    BSQ_K(64 / L + 1);
 #undef BSQ_K
   }
 }
