@@ -27,7 +27,7 @@
 // bf16).
 //
 // 8 lanes share a row up to 128 experts, 16 up to 256 and 64 above; a lane holds
-// V neighbouring experts in registers. Bound by vector instructions: k + 1 rounds
+// V neighbouring experts in registers. Bound by vector instructions: k rounds
 // of a search of V keys and an exchange over L lanes (65536 x 128, top 8 of 4 of 8
 // groups: 32 us, for bytes of 4; 16381 x 60, top 6 of 3 of 5: 15.8; one token 5).
 #include <math.h>
@@ -258,8 +258,8 @@ __device__ __noinline__ void select64(const T* __restrict__ row, const float* __
   }
 }
 
-// KR: registers that hold a row's results, lane j % L holding result j; k + 1
-// of them, since the first that is not selected is looked at too.
+// KR: registers that hold a row's results, lane j % L holding result j; more than
+// k of them, for those that may be selected in place of others.
 template <typename T, int L, int V, bool WHOLE, int KR>
 __global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ logits, const float* __restrict__ bias,
                                                         int64_t tokens, Choice c, float* __restrict__ weights,
@@ -419,11 +419,12 @@ __global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ l
   int ri[KR];
 #pragma unroll
   for (int q = 0; q < KR; ++q) ri[q] = -1;
-  for (int j = 0; j <= c.k; ++j) {
-    const double best = next();
+  double last = 0.0;
+  for (int j = 0; j < c.k; ++j) {
+    last = next();
 #pragma unroll
     for (int q = 0; q < KR; ++q)
-      if (j == q * L + sub && !is_gone(best)) ri[q] = index_of(best);
+      if (j == q * L + sub && !is_gone(last)) ri[q] = index_of(last);
   }
   // the selected ones' logits, biases, scores and keys
   float rx[KR], rb[KR], rs[KR], rc[KR], tol[KR];
@@ -436,12 +437,11 @@ __global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ l
   };
 #pragma unroll
   for (int q = 0; q < KR; ++q) look(ri[q] >= 0 ? ri[q] : 0, rx[q], rb[q], rs[q], rc[q], tol[q]);
-  // the selected each against the one after it; the first that is not, and all others, against the least of them
+  // the selected each against the one after it, and all others against the least of them
   const int first = mine * L;  // the row's first lane
-  bool tied = false;           // the last selected and the first that is not come from equal inputs
+  const uint64_t of_row = (L == 64 ? ~0ull : (1ull << (L & 63)) - 1) << first;
   bool close = false;          // two selected that follow each other are nearer than the bounds
   float low = kInf;            // what the selected keys are at least
-  float rest = left();         // what the others are at most, but for the first one of a tie
 #pragma unroll
   for (int q = 0; q < KR; ++q) {
     const int from = first + (sub + 1) % L;
@@ -456,34 +456,37 @@ __global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ l
       if (sub == L - 1) ni = li, nx = lx, nb = lb, nc = lc, nt = lt;
     }
     const int j = q * L + sub;
-    if (j < c.k && ri[q] >= 0 && ni >= 0) {
-      const bool same = nx == rx[q] && nb == rb[q];
-      if (j < c.k - 1) close |= !same && !(rc[q] - nc > tol[q] + nt);
-      else if (same) tied = true;
-      else rest = fmaxf(rest, nc + nt);
-    }
+    if (j < c.k - 1 && ri[q] >= 0 && ni >= 0)
+      close |= !(nx == rx[q] && nb == rb[q]) && !(rc[q] - nc > tol[q] + nt);
     if (j < c.k && ri[q] >= 0) low = fminf(low, rc[q] == kInf ? kBig : rc[q] - tol[q]);
   }
   low = over_row<L>(low, [](float p, float q) { return fminf(p, q); });
-  bool open = row_maxf<L>(rest) >= low;  // it is open what is selected
-  if (__any(tied && open && ok)) {  // of the others, those of the same inputs are behind the last selected by their index
-    const int at = first + (c.k - 1) % L;
-    float lx = 0, lb = 0;
-    bool tie = false;
+  bool open = row_maxf<L>(left()) >= low;  // it is open what is selected
+  if (__any(open && ok)) {  // of the others, those of the same inputs are behind the last selected by their index
+    uint32_t equal = 0;  // this lane's of the same float32 key
 #pragma unroll
-    for (int q = 0; q < KR; ++q)
-      if (q == (c.k - 1) / L) {
-        lx = __shfl(rx[q], at, 64), lb = __shfl(rb[q], at, 64);
-        tie = __shfl((int)(tied && open), at, 64);
+    for (int i = 0; i < V; ++i) {
+      const uint32_t low_bits = (uint32_t)(__double2loint(key[i]) ^ __double2loint(last));
+      equal |= (uint32_t)(__double2hiint(key[i]) == __double2hiint(last) && low_bits < 1u << 29) << i;
+    }
+    if (__any(open && ok && equal)) {
+      const int at = first + (c.k - 1) % L;
+      float lx = 0, lb = 0, rest = -kInf;
+#pragma unroll
+      for (int q = 0; q < KR; ++q)
+        if (q == (c.k - 1) / L) lx = __shfl(rx[q], at, 64), lb = __shfl(rb[q], at, 64);
+      bool tie = false;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        bool same = open && (equal >> i & 1);
+        if (same) same = load1(row + e0 + i) == lx && (bias ? bias[e0 + i] : 0.0f) == lb;
+        tie |= same;
+        rest = fmaxf(rest, same || is_gone(key[i]) ? -kInf : lds.high[i][lane]);
       }
-    rest = -kInf;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (tie && !is_gone(key[i]) && !(load1(row + e0 + i) == lx && (bias ? bias[e0 + i] : 0.0f) == lb))
-        rest = fmaxf(rest, lds.high[i][lane]);
-    rest = row_maxf<L>(rest);
-    if (tie) open = rest >= low;
-    unsure |= tie && close;  // one of the same may belong before a selected one
+      open = row_maxf<L>(rest) >= low;
+      tie = (__ballot(tie) & of_row) != 0;
+      unsure |= tie && close;  // one of the same may belong before a selected one
+    }
   }
   if (KR <= 2 && __any((close || open) && ok)) {
     // Where it is open what is selected, the free places of a row take the keys that follow: all that may be
@@ -491,13 +494,12 @@ __global__ __launch_bounds__(kThreads) void k_group_gate(const T* __restrict__ l
     // put in order by float64 keys.
     constexpr int C = L * KR;
     const bool more = __any(open && ok);
-    for (int j = c.k + 1; more && j < C; ++j) {
+    for (int j = c.k; more && j < C; ++j) {
       const double best = next();
 #pragma unroll
       for (int q = 0; q < KR; ++q)
         if (j == q * L + sub && !is_gone(best)) ri[q] = index_of(best);
     }
-    const uint64_t of_row = (L == 64 ? ~0ull : (1ull << (L & 63)) - 1) << first;
     const bool sort = (__ballot(close || open) & of_row) != 0;
     unsure |= row_maxf<L>(left()) >= low && open;
     double total = 1.0;
