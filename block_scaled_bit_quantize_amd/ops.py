@@ -648,8 +648,9 @@ def dequantize_int4(codes, scales, zeros=None, out_dtype=torch.float32):
 def linear_int4(x, codes, scales, zeros=None, bias=None, out_dtype=None):
     """y [M, N] = x W^T + bias of unquantized activations x [M, K] (float32 or
     bfloat16) and weights in 4-bit groups as quantize_int4 returns them; bias
-    float32 [N] or None; out_dtype is x's unless given. One token or few: bound
-    by reading the codes once."""
+    float32 [N] or None; out_dtype is x's unless given. float32 x enters with 22
+    significant bits (the limits are bsq.h's). One token or few: bound by reading
+    the codes once."""
     _dev(x, codes, scales, zeros, bias)
     _need(x.dim() == 2, "linear_int4: x must be [M, K]")
     dt = _dtype(x, "x")
