@@ -445,7 +445,8 @@ int bsq_moe_gate_backward(const float* dweights, const float* weights, const int
  *            lowest index. groups 1: no restriction.
  *   The k largest keys of the groups that stay, largest first, ties to the
  *   lowest index. The order of keys and groups is that of their values in
- *   float64. Slots past the last unmasked expert get id -1 and weight 0.
+ *   float64 (sums of other pairs of keys that differ by float64's own roundings
+ *   alone come in either order). Slots past the last unmasked expert get id -1 and weight 0.
  *   weights  FP32 [tokens, k]: scale * s_j, or with renormalize 1
  *            scale * s_j / (sum of the row's selected scores), in float32.
  *   topk_ids int32 [tokens, k] (a row with a -1 is no input for bsq_route).
